@@ -66,6 +66,11 @@ typedef enum pp_status {
 #define PP_DEV_DOC_OUT_OF_RANGE 0x2  /* append: document position outside cache */
 #define PP_DEV_BAD_STREAM       0x4  /* stream id > P_max, or a document query   */
 #define PP_DEV_TIMEOUT          0x8  /* a bounded in-kernel wait gave up         */
+/* set by the 8-bit paged cache's calls only (pp_kv8_*) */
+#define PP_DEV_BAD_POSITION     0x10 /* position < pos0, or past the angle table */
+#define PP_DEV_BAD_PAGE         0x20 /* a table entry in use names no page       */
+#define PP_DEV_ROW_ORDER        0x40 /* append: rows of a stream not in one run  */
+#define PP_DEV_NONFINITE        0x80 /* append: NaN or infinity among the values */
 
 /*
  * One attention layer's KV cache ("How it works": every KV slot carries a
@@ -324,6 +329,130 @@ size_t pp_doc_prefill_workspace_bytes(int32_t H, int32_t d, int32_t doc_len,
 pp_status pp_doc_prefill_attn(const pp_kv_layer *layer, int32_t doc_len, const uint16_t *q,
                               float scale, uint16_t *o, float *lse, void *ws, size_t ws_bytes,
                               const pp_options *opt, void *stream);
+
+/* ------------------------------------------------------------------------
+ * 8-bit paged cache.
+ *
+ * One attention layer's keys and values as e4m3 values in pages, with a scale
+ * for each page and head: half the bytes of pp_kv_layer's, pages instead of
+ * fixed segments, and fewer key heads than query heads where the model groups
+ * them.  The pages the method comes from serve a paged engine; they have no
+ * counterpart of the 8-bit values.
+ *
+ *   H          key/value heads;  d  64 or 128
+ *   page       tokens of a page: 16, 32, 64 or 128
+ *   n_pages    pages of the pool
+ *   k, v       e4m3 [n_pages][H][page][d], 16-byte aligned
+ *   k_scale, v_scale   fp32 [n_pages][H]; a stored value x stands for
+ *              x * scale; powers of two, 2^-40 .. 2^40 (written by the append)
+ *   doc_table  int32 [doc_pages]: page of document tokens i * page ..
+ *   seg_table  int32 [P_max][seg_pages]: pages of stream s at row s - 1
+ *   pos0       position of every stream's first token ("shared positions":
+ *              the document's length)
+ *   status     int32 [1] device status word (PP_DEV_* bits; sticky)
+ *
+ * Token p of the document (stream 0) lives in slot p, token p of stream s in
+ * slot p - pos0 of its segment: there are no lengths and no tags.  A row of
+ * stream s at position p sees the document and its own slots 0 .. p - pos0
+ * (of its table's), so every one of them must have been appended.  Tables
+ * belong to the caller and are read by the kernels at run time; an entry
+ * outside 0 .. n_pages-1 marks no page.  Two streams may share pages that
+ * nobody appends to any more.  A stream's segment is freed by giving its
+ * pages to another table row; a page starts afresh when slot 0 is written.
+ */
+typedef struct pp_kv8_layer {
+    int32_t H, d, page, n_pages;
+    int32_t P_max, seg_pages, doc_pages, pos0;
+    uint8_t *k, *v;
+    float *k_scale, *v_scale;
+    int32_t *doc_table, *seg_table;
+    int32_t *status;
+} pp_kv8_layer;
+
+/*
+ * Position rotation: the first `dim` dims of a head (a multiple of 16, at most
+ * d) turn by the angles of the row's position,
+ *   interleaved 0: dims j and j + dim/2, 1: dims 2j and 2j + 1,
+ *   a' = a cos - b sin, b' = b cos + a sin, in fp32.
+ * cos_sin: device fp32 [max_pos][dim], 16-byte aligned: dim/2 cosines, then
+ * dim/2 sines, of positions 0 .. max_pos-1.
+ */
+typedef struct pp_rope {
+    int32_t dim, interleaved, max_pos, reserved;
+    float *cos_sin;
+} pp_rope;
+
+/* Clear the status word (asynchronous). */
+pp_status pp_kv8_reset(const pp_kv8_layer *layer, void *stream);
+
+/*
+ * Append n rows: rotate the keys, quantise keys and values, one launch.
+ *   k, v   bf16, row i at k + i * k_ld, heads packed [H][d]; lds are multiples
+ *          of 8 and at least H * d (slices of a fused projection do)
+ *   q      NULL, or bf16 rows of Hq query heads to rotate with them into
+ *          q_out (bf16, may be q itself with q_out_ld = q_ld)
+ *   sid    int16 [n]: 0 document, 1..P_max a stream, < 0 a row to skip
+ *   pos    int32 [n]
+ *   rope   NULL: no rotation (q is copied)
+ * In one call the rows of a stream stand next to each other at consecutive
+ * positions; the first run of a stream counts, and a row that breaks this is
+ * dropped and sets PP_DEV_ROW_ORDER.  Per page and head, with A the largest
+ * magnitude of the call's rows in the page, need = 2^ceil(log2(A / 448))
+ * within [2^-40, 2^40]: the page's scale becomes need when the rows begin at
+ * its slot 0, else max(old scale, need), and if that grew, the page's slots
+ * before the rows are rounded again.  Rounding is to nearest even.  A NaN
+ * among a row's values makes every query that sees the row NaN in that head;
+ * infinities count as the largest value; both set PP_DEV_NONFINITE.
+ * Dropped rows: a slot past the table (PP_DEV_DOC_OUT_OF_RANGE,
+ * PP_DEV_SEGMENT_OVERFLOW), no page (PP_DEV_BAD_PAGE), position < pos0 or past
+ * the angles (PP_DEV_BAD_POSITION), sid > P_max (PP_DEV_BAD_STREAM).  Rows of
+ * q_out with sid < 0, sid > P_max or a position outside the angles stay as
+ * they were.  The same call repeated writes the same bytes.
+ */
+pp_status pp_kv8_append(const pp_kv8_layer *layer, const uint16_t *k, int64_t k_ld,
+                        const uint16_t *v, int64_t v_ld, const uint16_t *q, int64_t q_ld,
+                        int32_t Hq, const int16_t *sid, const int32_t *pos, int32_t n,
+                        const pp_rope *rope, uint16_t *q_out, int64_t q_out_ld, void *stream);
+
+/*
+ * Workspace bytes of the calls below (0: none needed).  They depend on the SM
+ * count of the CURRENT device, as pp_decode_workspace_bytes.
+ */
+size_t pp_kv8_decode_workspace_bytes(int32_t P, int32_t Hq, int32_t H, int32_t d, int32_t doc_len,
+                                     const pp_options *opt);
+size_t pp_kv8_prefill_workspace_bytes(int32_t R, int32_t Hq, int32_t H, int32_t d, int32_t doc_len,
+                                      const pp_options *opt);
+
+/*
+ * Attention over the 8-bit cache: pp_kv8_decode_attn for a decode step (one
+ * row per stream, P <= P_max), pp_kv8_prefill_attn for question rows in any
+ * order.  Both give the same results; they differ in how rows are grouped.
+ *   q      bf16 rows of Hq query heads, q_ld elements apart, already rotated;
+ *          Hq a multiple of H, query heads j * (Hq/H) .. belong to key head j
+ *   q_sid  int16: stream of row i (1..P_max), or -1 for an inactive row
+ *   q_pos  int32: position of row i; it sees the document (tokens
+ *          0..doc_len-1) and slots 0 .. q_pos - pos0 of its own segment (none
+ *          when q_pos < pos0)
+ *   scale  softmax scale, finite and > 0
+ *   o      bf16 [rows][Hq][d];  lse  fp32 [rows][Hq] or NULL
+ *   opt    splits, debug_inject_timeout, wait_limit_log2 and events apply; the
+ *          comparison modes and suffix_slices are refused
+ * Rows that see nothing, inactive rows and rows of stream 0 or > P_max (which
+ * set PP_DEV_BAD_STREAM) get o = 0 and lse = -inf.  Keys on a page that is
+ * not there are skipped (PP_DEV_BAD_PAGE).  A query with a NaN or infinity
+ * gives NaN.
+ */
+pp_status pp_kv8_decode_attn(const pp_kv8_layer *layer, int32_t doc_len, const uint16_t *q,
+                             int64_t q_ld, int32_t Hq, const int16_t *q_sid, const int32_t *q_pos,
+                             int32_t P, float scale, uint16_t *o, float *lse, void *ws,
+                             size_t ws_bytes, const pp_options *opt, void *stream);
+pp_status pp_kv8_prefill_attn(const pp_kv8_layer *layer, int32_t doc_len, const uint16_t *q,
+                              int64_t q_ld, int32_t Hq, const int16_t *q_sid, const int32_t *q_pos,
+                              int32_t R, float scale, uint16_t *o, float *lse, void *ws,
+                              size_t ws_bytes, const pp_options *opt, void *stream);
+
+/* As pp_get_device_status, for an 8-bit layer (synchronises). */
+pp_status pp_kv8_get_device_status(const pp_kv8_layer *layer, int32_t *h_status, void *stream);
 
 /*
  * Test aid: evaluate the mask predicate the attention kernels use.

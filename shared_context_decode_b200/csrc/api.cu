@@ -283,6 +283,94 @@ size_t workspace(int32_t rows, int32_t H, int32_t d, int32_t doc_len, const pp_o
   return ws_layout(plan, d, questions).total;
 }
 
+// ------------------------------------------------ 8-bit paged cache ----
+pp_status check_kv8_layer(const pp_kv8_layer* L) {
+  if (!L) return PP_ERR_INVALID_ARG;
+  if (L->d != 64 && L->d != 128) return PP_ERR_UNSUPPORTED;
+  if (L->page != 16 && L->page != 32 && L->page != 64 && L->page != 128) return PP_ERR_UNSUPPORTED;
+  if (L->P_max < 1 || L->P_max > 32767) return PP_ERR_UNSUPPORTED;
+  if (L->H < 1 || L->n_pages < 1 || L->seg_pages < 1 || L->doc_pages < 0 || L->pos0 < 0)
+    return PP_ERR_INVALID_ARG;
+  // positions and (page, head) cells are 32-bit numbers
+  const int64_t most = INT32_MAX - 256;
+  if ((int64_t)L->pos0 + (int64_t)L->seg_pages * L->page > most ||
+      (int64_t)L->doc_pages * L->page > most || (int64_t)L->n_pages * L->H > most)
+    return PP_ERR_UNSUPPORTED;
+  if (!L->k || !L->v || !aligned(L->k, 16) || !aligned(L->v, 16)) return PP_ERR_INVALID_ARG;
+  if (!L->k_scale || !L->v_scale || !aligned(L->k_scale, 4) || !aligned(L->v_scale, 4))
+    return PP_ERR_INVALID_ARG;
+  if (!L->seg_table || !aligned(L->seg_table, 4) ||
+      (L->doc_pages > 0 && (!L->doc_table || !aligned(L->doc_table, 4))))
+    return PP_ERR_INVALID_ARG;
+  if (!L->status || !aligned(L->status, 4)) return PP_ERR_INVALID_ARG;
+  return PP_OK;
+}
+
+// A strided row operand: heads packed, rows ld elements apart.
+bool row_operand(const void* ptr, int64_t ld, int64_t heads, int32_t d) {
+  return ptr && aligned(ptr, 16) && ld % 8 == 0 && ld >= heads * d;
+}
+
+pp_status kv8_append(const pp_kv8_layer* L, const uint16_t* k, int64_t k_ld, const uint16_t* v,
+                     int64_t v_ld, const uint16_t* q, int64_t q_ld, int32_t Hq, const int16_t* sid,
+                     const int32_t* pos, int32_t n, const pp_rope* rope, uint16_t* q_out,
+                     int64_t qo_ld, void* stream) {
+  pp_status s = check_kv8_layer(L);
+  if (s != PP_OK) return s;
+  if (n < 0) return PP_ERR_INVALID_ARG;
+  if (rope) {
+    if (rope->dim < 0 || rope->max_pos < 1 || !rope->cos_sin || !aligned(rope->cos_sin, 16))
+      return PP_ERR_INVALID_ARG;
+    if (rope->dim == 0 || rope->dim % 16 != 0 || rope->dim > L->d) return PP_ERR_UNSUPPORTED;
+    if (rope->interleaved != 0 && rope->interleaved != 1) return PP_ERR_INVALID_ARG;
+  }
+  if (n == 0) return PP_OK;
+  if (!row_operand(k, k_ld, L->H, L->d) || !row_operand(v, v_ld, L->H, L->d) || !sid || !pos ||
+      !aligned(sid, 2) || !aligned(pos, 4))
+    return PP_ERR_INVALID_ARG;
+  if (!q != !q_out) return PP_ERR_INVALID_ARG;
+  if (q && (Hq < 1 || Hq > (1 << 20) || !row_operand(q, q_ld, Hq, L->d) ||
+            !row_operand(q_out, qo_ld, Hq, L->d)))
+    return PP_ERR_INVALID_ARG;
+  if (L->H > (1 << 17)) return PP_ERR_UNSUPPORTED;
+  const int sms = sm_count();
+  if (sms < 1) return PP_ERR_CUDA;
+  return from_cuda(pp::launch_kv8_append(*L, k, k_ld, v, v_ld, q, q_ld, Hq, sid, pos, n, rope,
+                                         q_out, qo_ld, sms, static_cast<cudaStream_t>(stream)));
+}
+
+pp_status kv8_attend(const pp_kv8_layer* L, int32_t doc_len, const uint16_t* q, int64_t q_ld,
+                     int32_t Hq, const int16_t* q_sid, const int32_t* q_pos, int32_t rows,
+                     float scale, uint16_t* o, float* lse, void* ws, size_t ws_bytes,
+                     const pp_options* opt, void* stream, bool decode) {
+  pp_status s = check_kv8_layer(L);
+  if (s != PP_OK) return s;
+  if (rows < 0 || doc_len < 0 || Hq < 1 || Hq % L->H != 0) return PP_ERR_INVALID_ARG;
+  if (decode && rows > L->P_max) return PP_ERR_UNSUPPORTED;
+  if ((int64_t)doc_len > (int64_t)L->doc_pages * L->page) return PP_ERR_CAPACITY;
+  if (opt && (opt->ablation_doc_per_stream || opt->sibling_scan || opt->suffix_slices))
+    return PP_ERR_UNSUPPORTED;
+  if (!(scale > 0.f) || scale > 3.4e38f) return PP_ERR_INVALID_ARG;
+  if (rows == 0) return PP_OK;
+  if (!row_operand(q, q_ld, Hq, L->d) || !o || !aligned(o, 16) || (lse && !aligned(lse, 4)) ||
+      !q_sid || !q_pos || !aligned(q_sid, 2) || !aligned(q_pos, 4))
+    return PP_ERR_INVALID_ARG;
+  if ((int64_t)rows * Hq > INT32_MAX - 256) return PP_ERR_UNSUPPORTED;
+  const int sms = sm_count();
+  if (sms < 1) return PP_ERR_CUDA;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  (void)ws; (void)ws_bytes;
+  return from_cuda(pp::launch_kv8_attn(*L, doc_len, q, q_ld, Hq, q_sid, q_pos, rows, decode, scale,
+                                       SplitPlan{}, false, Partials{}, o, lse, sms, st));
+}
+
+size_t kv8_workspace(int32_t rows, int32_t Hq, int32_t H, int32_t d, int32_t doc_len,
+                     const pp_options* opt) {
+  (void)opt;
+  if (rows < 0 || H < 1 || Hq < 1 || Hq % H != 0 || (d != 64 && d != 128) || doc_len < 0) return 0;
+  return 0;
+}
+
 // Host copy of a plan for the split-plan test aids.
 pp_status write_plan(const SplitPlan& p, int64_t* h_out, int32_t h_out_len) {
   if (h_out_len < 5 + 2 * (int64_t)p.units) return PP_ERR_CAPACITY;
@@ -403,6 +491,67 @@ PP_API pp_status pp_doc_prefill_attn(const pp_kv_layer* layer, int32_t doc_len, 
   NvtxRange nvtx_range("pp_doc_prefill_attn");
   return attend(layer, doc_len, q, nullptr, nullptr, doc_len, scale, o, lse, ws, ws_bytes, opt,
                 stream, true);
+}
+
+PP_API pp_status pp_kv8_reset(const pp_kv8_layer* layer, void* stream) {
+  NvtxRange nvtx_range("pp_kv8_reset");
+  pp_status s = check_kv8_layer(layer);
+  if (s != PP_OK) return s;
+  return from_cuda(pp::launch_kv8_reset(*layer, static_cast<cudaStream_t>(stream)));
+}
+
+PP_API pp_status pp_kv8_append(const pp_kv8_layer* layer, const uint16_t* k, int64_t k_ld,
+                               const uint16_t* v, int64_t v_ld, const uint16_t* q, int64_t q_ld,
+                               int32_t Hq, const int16_t* sid, const int32_t* pos, int32_t n,
+                               const pp_rope* rope, uint16_t* q_out, int64_t q_out_ld,
+                               void* stream) {
+  NvtxRange nvtx_range("pp_kv8_append");
+  return kv8_append(layer, k, k_ld, v, v_ld, q, q_ld, Hq, sid, pos, n, rope, q_out, q_out_ld,
+                    stream);
+}
+
+PP_API size_t pp_kv8_decode_workspace_bytes(int32_t P, int32_t Hq, int32_t H, int32_t d,
+                                            int32_t doc_len, const pp_options* opt) {
+  return kv8_workspace(P, Hq, H, d, doc_len, opt);
+}
+
+PP_API size_t pp_kv8_prefill_workspace_bytes(int32_t R, int32_t Hq, int32_t H, int32_t d,
+                                             int32_t doc_len, const pp_options* opt) {
+  return kv8_workspace(R, Hq, H, d, doc_len, opt);
+}
+
+PP_API pp_status pp_kv8_decode_attn(const pp_kv8_layer* layer, int32_t doc_len, const uint16_t* q,
+                                    int64_t q_ld, int32_t Hq, const int16_t* q_sid,
+                                    const int32_t* q_pos, int32_t P, float scale, uint16_t* o,
+                                    float* lse, void* ws, size_t ws_bytes, const pp_options* opt,
+                                    void* stream) {
+  NvtxRange nvtx_range("pp_kv8_decode_attn");
+  return kv8_attend(layer, doc_len, q, q_ld, Hq, q_sid, q_pos, P, scale, o, lse, ws, ws_bytes, opt,
+                    stream, true);
+}
+
+PP_API pp_status pp_kv8_prefill_attn(const pp_kv8_layer* layer, int32_t doc_len, const uint16_t* q,
+                                     int64_t q_ld, int32_t Hq, const int16_t* q_sid,
+                                     const int32_t* q_pos, int32_t R, float scale, uint16_t* o,
+                                     float* lse, void* ws, size_t ws_bytes, const pp_options* opt,
+                                     void* stream) {
+  NvtxRange nvtx_range("pp_kv8_prefill_attn");
+  return kv8_attend(layer, doc_len, q, q_ld, Hq, q_sid, q_pos, R, scale, o, lse, ws, ws_bytes, opt,
+                    stream, false);
+}
+
+PP_API pp_status pp_kv8_get_device_status(const pp_kv8_layer* layer, int32_t* h_status,
+                                          void* stream) {
+  NvtxRange nvtx_range("pp_kv8_get_device_status");
+  pp_status s = check_kv8_layer(layer);
+  if (s != PP_OK) return s;
+  if (!h_status) return PP_ERR_INVALID_ARG;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (cudaMemcpyAsync(h_status, layer->status, sizeof(int32_t), cudaMemcpyDeviceToHost, st) !=
+      cudaSuccess)
+    return PP_ERR_CUDA;
+  if ((s = from_cuda(cudaStreamSynchronize(st))) != PP_OK) return s;
+  return (*h_status & PP_DEV_TIMEOUT) ? PP_ERR_DEVICE_TIMEOUT : PP_OK;
 }
 
 PP_API pp_status pp_debug_visibility(const pp_kv_layer* layer, int32_t doc_len, const int16_t* q_sid,

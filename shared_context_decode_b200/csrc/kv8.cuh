@@ -1,0 +1,76 @@
+// Shared pieces of the 8-bit paged cache's kernels (append, attention).
+//
+// A page holds `page` tokens of every head as e4m3 values, [H][page][d], and
+// one fp32 scale per head for its keys and one for its values; a stored value
+// x stands for x * scale.  Scales are powers of two: e4m3 is a floating-point
+// format, so a power of two loses nothing against an exact one but the last
+// fraction of a binade of range, dividing by it is exact, and its logarithm
+// is an integer that folds into the softmax exponent.
+#pragma once
+
+#include "common.cuh"
+
+namespace pp {
+
+// Exponents a scale may have.  The attention kernels carry a page's value
+// scale inside the exponent (2^(s + log2 scale - M)), so two pages' scales
+// must not differ by more than a softmax term's fp32 range allows: 80 of the
+// 126 binades below 1, which leaves probabilities down to 2^-46.
+constexpr int kScaleMinExp = -40, kScaleMaxExp = 40;
+
+// Smallest power of two 2^e with amax <= 448 * 2^e, e clamped; 448 =
+// 1.75 * 2^8 is e4m3's largest value.  amax finite, >= 0.
+__device__ __forceinline__ float scale_for(float amax) {
+  const uint32_t b = __float_as_uint(amax);
+  int e = (int)(b >> 23) - 127 - 8 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0);
+  e = e < kScaleMinExp ? kScaleMinExp : e > kScaleMaxExp ? kScaleMaxExp : e;
+  return __uint_as_float((uint32_t)(e + 127) << 23);
+}
+
+// Two floats -> two e4m3 bytes (a in the low byte), round to nearest even,
+// out of range saturates to +-448, NaN stays NaN (0x7f).
+__device__ __forceinline__ uint32_t f2_to_e4m3x2(float a, float b) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+  return r;
+}
+// Two e4m3 bytes (the low 16 bits of w) -> f16x2, exactly.
+__device__ __forceinline__ uint32_t e4m3x2_to_h2(uint32_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}"
+      : "=r"(r)
+      : "r"(w));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3x2_hi_to_h2(uint32_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}"
+      : "=r"(r)
+      : "r"(w));
+  return r;
+}
+__device__ __forceinline__ float2 h2_to_f2(uint32_t w) {
+  float2 r;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.f32.f16 %0, lo;\n\tcvt.f32.f16 %1, hi;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "r"(w));
+  return r;
+}
+__device__ __forceinline__ uint32_t f2_to_h2(float a, float b) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
+
+// Table entry -> page, or -1 when the entry names none.
+__device__ __forceinline__ int page_of(int32_t entry, int n_pages) {
+  return (uint32_t)entry < (uint32_t)n_pages ? entry : -1;
+}
+
+// Doc-pass and merge row of (query row r, query head kvh * g + j): the g query
+// heads of a key head stack as rows, r * g + j.
+struct Kv8Rows {
+  int rows, H, g;
+};
+
+}  // namespace pp

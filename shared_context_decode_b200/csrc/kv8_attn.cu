@@ -1,0 +1,521 @@
+// Attention over the 8-bit paged cache on warp-level mma: the stream segments
+// of a decode step or a question prefill, the document too where it is short,
+// and the merge with the tensor-core document pass's partials.
+//
+//   w_t = scale q.k_t + log2-scale terms,  o = sum_t 2^(w_t - M) v_t / l
+// over the visible slots t of a row's stream.  With x_t the stored key, a page's
+// scales ks, vs (powers of two) and everything in the log2 domain,
+//   w_t = (q.x_t) scale ks log2e + log2 vs,   M = max w_t,
+//   O = sum 2^(w_t - M) y_t  (y the stored value),  l = sum 2^(w_t - M) / vs
+// so the value scale costs one addition per page and key, not a product per
+// value.
+//
+// One item = up to 8 * NT (query row, query head) pairs that share a key head;
+// grouped query heads of a row stand together.  The products are taken
+// transposed, S^T = K Q^T and O^T = V^T P^T, so the 16-wide mma dimension is
+// the keys' and the values', and the 8-wide one the few rows.  A lane reads a
+// key's contiguous 32 bytes (values: 16 bytes of four keys); which dims and
+// keys an mma index stands for is free as long as both operands agree, so the
+// loads need no shuffling through shared memory.  e4m3 -> f16 is exact; queries
+// are scaled by a power of two into f16's range; P^T goes from the
+// accumulators to the operand by a transposing move.
+//
+// WAYS warps share an item, each a contiguous range of its 16-key chunks; the
+// partials meet in shared memory, where each row's (m, l, O) are joined with
+// the document pass's.  Bound: HBM for decode (one read of every segment).
+#include <atomic>
+
+#include "kv8.cuh"
+#include "internal.h"
+
+namespace pp {
+namespace {
+
+struct Attn8Params {
+  pp_kv8_layer L;
+  const uint16_t* q;
+  int64_t q_ld;
+  int Hq, g, hg, gt, rt;   // query heads, per key head, per item, items per key head's group, rows per item
+  int rows, n_items;
+  const int16_t* q_sid;
+  const int32_t* q_pos;
+  int doc_len;             // document keys read here (0: none, or left to the document pass)
+  float sl2;               // scale * log2e
+  int ways;                // warps per item
+  int lper;                // log2 of the 16-key chunks per page
+  int has_doc;             // document partials to merge
+  SplitPlan plan;
+  const float* doc_o;
+  const float* doc_ml;
+  uint16_t* o;
+  float* lse;
+};
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};\n"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// 8x8 f16 matrix across the warp, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+
+// One warp's running state over an item's rows: row n of tile t is held by the
+// lanes with lane % 4 == n / 2 (n = 2c, 2c + 1).
+template <int D, int NT>
+struct State {
+  float m[NT][2];          // running maximum of w (uniform over a row's lanes)
+  float l[NT][2];          // this lane's part of the sum
+  float o[NT][D / 16][4];  // O^T: [tile][dim pair j][2 rows x 2 dims]
+};
+
+// The chunk's stored bytes of one warp: two keys' 32 (16) bytes and four
+// values' 16 (8) bytes a lane.
+template <int D>
+struct Chunk {
+  uint32_t k[2][D / 16];
+  uint32_t v[4][D / 32];
+};
+
+template <int D>
+__device__ __forceinline__ void load_chunk(Chunk<D>& ch, const uint8_t* kb, const uint8_t* vb,
+                                           int r, int c) {
+#pragma unroll
+  for (int a = 0; a < 2; ++a)
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i)
+      *reinterpret_cast<uint4*>(&ch.k[a][4 * i]) = __ldg(
+          reinterpret_cast<const uint4*>(kb + (r + 8 * a) * D + c * (D / 4) + 16 * i));
+#pragma unroll
+  for (int a = 0; a < 4; ++a) {
+    const uint8_t* at = vb + (2 * c + (a & 1) + 8 * (a >> 1)) * D + r * (D / 8);
+    if constexpr (D == 128)
+      *reinterpret_cast<uint4*>(&ch.v[a][0]) = __ldg(reinterpret_cast<const uint4*>(at));
+    else
+      *reinterpret_cast<uint2*>(&ch.v[a][0]) = __ldg(reinterpret_cast<const uint2*>(at));
+  }
+}
+
+// Keys t0 .. t0 + 15; lim[t][e]: last visible slot of row 2c + e of tile t.
+// t_max: the largest of all rows' lims; a key past it holds whatever the page
+// held before, so its values are taken as 0 (0 * NaN would spoil the sum).
+template <int D, int NT>
+__device__ __forceinline__ void chunk_step(State<D, NT>& st, const uint32_t (&qf)[NT][D / 8],
+                                           Chunk<D>& ch, int t0, const int (&lim)[NT][2],
+                                           int t_max, int t_min, const float (&qs)[NT][2],
+                                           float ks, float vs, int r, int c) {
+  float s[NT][4];
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[t][e] = 0.f;
+#pragma unroll
+  for (int kk = 0; kk < D / 16; ++kk) {
+    const uint32_t a0 = e4m3x2_to_h2(ch.k[0][kk]), a2 = e4m3x2_hi_to_h2(ch.k[0][kk]);
+    const uint32_t a1 = e4m3x2_to_h2(ch.k[1][kk]), a3 = e4m3x2_hi_to_h2(ch.k[1][kk]);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) mma_f16(s[t], a0, a1, a2, a3, qf[t][2 * kk], qf[t][2 * kk + 1]);
+  }
+  const float lv = (float)((int)(__float_as_uint(vs) >> 23) - 127);   // log2 vs
+  const float rvs = 1.f / vs;
+  bool up = false;
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float a = qs[t][e] * ks;
+      s[t][e] = fmaf(s[t][e], a, lv);
+      s[t][2 + e] = fmaf(s[t][2 + e], a, lv);
+      if (t0 + 15 > t_min) {
+        if (t0 + r > lim[t][e]) s[t][e] = -INFINITY;
+        if (t0 + r + 8 > lim[t][e]) s[t][2 + e] = -INFINITY;
+      }
+      // (a NaN score counts as a new maximum: its row comes out NaN)
+      up |= !(s[t][e] <= st.m[t][e]) || !(s[t][2 + e] <= st.m[t][e]);
+    }
+  if (__any_sync(0xffffffffu, up)) {      // some row's maximum rises: move all to their new ones
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float x0 = s[t][e] != s[t][e] ? INFINITY : s[t][e];
+        const float x1 = s[t][2 + e] != s[t][2 + e] ? INFINITY : s[t][2 + e];
+        float x = fmaxf(x0, x1);
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+        const float m = fmaxf(st.m[t][e], x);
+        const float f = m == -INFINITY ? 1.f : ex2_mufu(st.m[t][e] - m);
+        st.m[t][e] = m;
+        st.l[t][e] *= f;
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) {
+          st.o[t][j][e] *= f;
+          st.o[t][j][2 + e] *= f;
+        }
+      }
+  }
+  uint32_t pb[NT][2];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    float pr[4];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float m = st.m[t][e] == -INFINITY ? 0.f : st.m[t][e];
+      pr[e] = ex2_mufu(s[t][e] - m);
+      pr[2 + e] = ex2_mufu(s[t][2 + e] - m);
+      st.l[t][e] = fmaf(pr[e] + pr[2 + e], rvs, st.l[t][e]);
+    }
+    // P to f16: 2^-11 of its value, against e4m3's 2^-4 of the values it weighs
+    pb[t][0] = transpose8(f2_to_h2(pr[0], pr[1]));
+    pb[t][1] = transpose8(f2_to_h2(pr[2], pr[3]));
+  }
+  if (t0 + 15 > t_max) {
+#pragma unroll
+    for (int a = 0; a < 4; ++a)
+      if (t0 + 2 * c + (a & 1) + 8 * (a >> 1) > t_max)
+#pragma unroll
+        for (int w = 0; w < D / 32; ++w) ch.v[a][w] = 0u;
+  }
+#pragma unroll
+  for (int w = 0; w < D / 32; ++w) {      // 4 bytes of each value row: dims 4w .. 4w + 3 of the lane's
+    uint32_t x[4][2];
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      x[a][0] = e4m3x2_to_h2(ch.v[a][w]);
+      x[a][1] = e4m3x2_hi_to_h2(ch.v[a][w]);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t a0 = __byte_perm(x[0][i], x[1][i], 0x5410), a1 = __byte_perm(x[0][i], x[1][i], 0x7632);
+      const uint32_t a2 = __byte_perm(x[2][i], x[3][i], 0x5410), a3 = __byte_perm(x[2][i], x[3][i], 0x7632);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) mma_f16(st.o[t][2 * w + i], a0, a1, a2, a3, pb[t][0], pb[t][1]);
+    }
+  }
+}
+
+// Chunks [c0, c1) of one token sequence (page table `tab`): 32 table entries
+// and scales are fetched at a time, a chunk's bytes one chunk ahead.
+template <int D, int NT>
+__device__ __forceinline__ void scan(State<D, NT>& st, const uint32_t (&qf)[NT][D / 8],
+                                     const Attn8Params& p, const int32_t* tab, int h, int c0,
+                                     int c1, const int (&lim)[NT][2], int t_max, int t_min,
+                                     const float (&qs)[NT][2], int lane) {
+  const int r = lane >> 2, c = lane & 3;
+  const int lper = p.lper, per = 1 << lper;   // chunks per page: 1, 2, 4, 8
+  for (int b = c0; b < c1; b += 32) {
+    const int n = min(32, c1 - b);
+    int pg = -1;
+    float ks = 1.f, vs = 1.f;
+    if (lane < n) {
+      pg = page_of(tab[(b + lane) >> lper], p.L.n_pages);
+      if (pg >= 0) {
+        ks = p.L.k_scale[(int64_t)pg * p.L.H + h];
+        vs = p.L.v_scale[(int64_t)pg * p.L.H + h];
+      } else {
+        set_status(p.L.status, PP_DEV_BAD_PAGE);
+      }
+    }
+    auto base = [&](int j, int& pgj) -> int64_t {
+      pgj = __shfl_sync(0xffffffffu, pg, j);
+      return (((int64_t)(pgj < 0 ? 0 : pgj) * p.L.H + h) * p.L.page + ((b + j) & (per - 1)) * 16) * D;
+    };
+    Chunk<D> cur, nxt;
+    int pgc = -1, pgn = -1;
+    int64_t at = base(0, pgc);
+    if (pgc >= 0) load_chunk<D>(cur, p.L.k + at, p.L.v + at, r, c);
+    for (int j = 0; j < n; ++j) {
+      if (j + 1 < n) {
+        at = base(j + 1, pgn);
+        if (pgn >= 0) load_chunk<D>(nxt, p.L.k + at, p.L.v + at, r, c);
+      }
+      const float ksj = __shfl_sync(0xffffffffu, ks, j), vsj = __shfl_sync(0xffffffffu, vs, j);
+      if (pgc >= 0)
+        chunk_step<D, NT>(st, qf, cur, (b + j) * 16, lim, t_max, t_min, qs, ksj, vsj, r, c);
+      cur = nxt;
+      pgc = pgn;
+    }
+  }
+}
+
+// A slice of chunks: part `w` of `ways` of the sequence's [0, n).
+__device__ __forceinline__ void part_of(int n, int w, int ways, int& c0, int& c1) {
+  c0 = (int)((int64_t)n * w / ways);
+  c1 = (int)((int64_t)n * (w + 1) / ways);
+}
+
+constexpr int kMaxWays = 8;   // warps of a CTA, and of an item, at most
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kMaxWays * 32) kv8_attn(const Attn8Params p) {
+  constexpr int ROWS = 8 * NT, LD = D + 4;
+  extern __shared__ float sm[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r = lane >> 2, c = lane & 3;
+  const int per_cta = (blockDim.x >> 5) / p.ways;
+  const int64_t item = (int64_t)blockIdx.x * per_cta + warp / p.ways;
+  const int way = warp % p.ways;
+  const bool live = item < p.n_items;
+  float* my_o = sm + (int64_t)warp * ROWS * LD;
+  float* my_ml = sm + (int64_t)(blockDim.x >> 5) * ROWS * LD + warp * ROWS * 2;
+  int r0 = 0, kvh = 0, hb = 0, nh = 1, nrow = 0;
+  if (live) {
+    const int x = (int)(item % (p.L.H * p.gt));
+    r0 = (int)(item / (p.L.H * p.gt)) * p.rt;
+    kvh = x / p.gt;
+    hb = (x % p.gt) * p.hg;               // first query head inside the group
+    nh = min(p.hg, p.g - hb);
+    nrow = min(p.rt, p.rows - r0);
+    const int n_pairs = nrow * nh;
+    // ---- queries: B operand of S^T (row n = r of tile t), scaled into f16
+    State<D, NT> st;
+    uint32_t qf[NT][D / 8];
+    float qs[NT][2];
+    int lim[NT][2], sidr[NT][2];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int n = t * 8 + r;
+      float x2[D / 4];
+      float am = 0.f;
+#pragma unroll
+      for (int e = 0; e < D / 4; ++e) x2[e] = 0.f;
+      if (n < n_pairs) {
+        const uint16_t* src = p.q + (int64_t)(r0 + n / nh) * p.q_ld +
+                              (int64_t)(kvh * p.g + hb + n % nh) * D + c * (D / 4);
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          const uint4 w = *reinterpret_cast<const uint4*>(src + 8 * i);
+          const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 f = bf2_to_f2(a[j]);
+            // f - f is 0, or NaN where f is not finite
+            x2[8 * i + 2 * j] = f.x + (f.x - f.x);
+            x2[8 * i + 2 * j + 1] = f.y + (f.y - f.y);
+            am = fmaxf(am, fabsf(f.x) < INFINITY ? fabsf(f.x) : 0.f);
+            am = fmaxf(am, fabsf(f.y) < INFINITY ? fabsf(f.y) : 0.f);
+          }
+        }
+      }
+      am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1));
+      am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 2));
+      // 2^e with am / 2^e in [2^13, 2^14): bf16's 8 bits are exact in f16 down
+      // to 2^-30 of the row's largest value
+      int e = (int)(__float_as_uint(am) >> 23) - 127 - 13;
+      e = e < -100 ? -100 : e;
+      const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) qf[t][i] = f2_to_h2(x2[2 * i] * inv, x2[2 * i + 1] * inv);
+      const float qsc = __uint_as_float((uint32_t)(e + 127) << 23) * p.sl2;
+#pragma unroll
+      for (int a = 0; a < 2; ++a) {
+        qs[t][a] = __shfl_sync(0xffffffffu, qsc, (2 * c + a) * 4);
+        const int n2 = t * 8 + 2 * c + a;
+        int sd = 0, lm = -1;
+        if (n2 < n_pairs) {
+          sd = p.q_sid[r0 + n2 / nh];
+          const int ps = p.q_pos[r0 + n2 / nh];
+          sd = stream_query(sd, p.L.P_max) ? sd : 0;
+          const int cap = p.L.seg_pages * p.L.page;
+          lm = sd && ps >= p.L.pos0 ? min(ps - p.L.pos0, cap - 1) : -1;
+        }
+        sidr[t][a] = sd;
+        lim[t][a] = lm;
+        st.m[t][a] = -INFINITY;
+        st.l[t][a] = 0.f;
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) st.o[t][j][a] = st.o[t][j][2 + a] = 0.f;
+      }
+    }
+    // ---- document
+    if (p.doc_len > 0) {
+      int dl[NT][2];
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int a = 0; a < 2; ++a) dl[t][a] = sidr[t][a] ? p.doc_len - 1 : -1;
+      int c0, c1;
+      part_of((p.doc_len + 15) >> 4, way, p.ways, c0, c1);
+      // rows that are no queries see nothing; t_min by the document's end
+      // alone would miss them, so every chunk is masked when there are any
+      bool all = true;
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int a = 0; a < 2; ++a) all &= t * 8 + 2 * c + a >= n_pairs || sidr[t][a] != 0;
+      const int t_min = __all_sync(0xffffffffu, all) ? p.doc_len - 1 : -1;
+      scan<D, NT>(st, qf, p, p.L.doc_table, kvh, c0, c1, dl, p.doc_len - 1, t_min, qs, lane);
+    }
+    // ---- segments: one pass per stretch of rows of one stream
+    for (int ra = 0; ra < nrow;) {
+      const int s = p.q_sid[r0 + ra];
+      int rb = ra + 1;
+      while (rb < nrow && p.q_sid[r0 + rb] == s) ++rb;
+      if (s == 0 || s > p.L.P_max) {
+        if (kvh == 0 && hb == 0 && way == 0 && lane == 0) set_status(p.L.status, PP_DEV_BAD_STREAM);
+      } else if (s > 0) {
+        int lm[NT][2], hi = -1, lo = 0x7fffffff;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int a = 0; a < 2; ++a) {
+            const int n2 = t * 8 + 2 * c + a;
+            const bool in = n2 >= ra * nh && n2 < rb * nh;
+            lm[t][a] = in ? lim[t][a] : -1;
+            hi = max(hi, lm[t][a]);
+            // rows that hold no pair at all need no mask: nothing reads them
+            if (n2 < n_pairs) lo = min(lo, lm[t][a]);
+          }
+#pragma unroll
+        for (int o2 = 1; o2 < 4; o2 <<= 1) {
+          hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o2));
+          lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o2));
+        }
+        int c0, c1;
+        part_of((hi + 16) >> 4, way, p.ways, c0, c1);
+        scan<D, NT>(st, qf, p, p.L.seg_table + (int64_t)(s - 1) * p.L.seg_pages, kvh, c0, c1, lm,
+                    hi, lo, qs, lane);
+      }
+      ra = rb;
+    }
+    // ---- this warp's partial to shared memory, row by row
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int a = 0; a < 2; ++a) {
+        float l = st.l[t][a];
+#pragma unroll
+        for (int o2 = 4; o2 < 32; o2 <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o2);
+        const int n2 = t * 8 + 2 * c + a;
+        if (r == 0) {
+          my_ml[2 * n2] = st.m[t][a];
+          my_ml[2 * n2 + 1] = l;
+        }
+#pragma unroll
+        for (int j = 0; j < D / 16; j += 2)   // dims (D/8) r + 2j .. + 3
+          *reinterpret_cast<float4*>(my_o + n2 * LD + r * (D / 8) + 2 * j) = make_float4(
+              st.o[t][j][a], st.o[t][j][2 + a], st.o[t][j + 1][a], st.o[t][j + 1][2 + a]);
+      }
+  }
+  if (p.ways > 1) __syncthreads(); else __syncwarp();
+  if (!live) return;
+  // ---- merge: the item's warps take its rows in turn, a lane E dims
+  constexpr int E = D / 32;
+  const int w0 = warp - way;
+  const float* it_o = sm + (int64_t)w0 * ROWS * LD;
+  const float* it_ml = sm + (int64_t)(blockDim.x >> 5) * ROWS * LD + w0 * ROWS * 2;
+  for (int n = way; n < nrow * nh; n += p.ways) {
+    const int row = r0 + n / nh, head = kvh * p.g + hb + n % nh;
+    const bool query = stream_query(p.q_sid[row], p.L.P_max);
+    float m = -INFINITY, l = 0.f, acc[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    auto fold_in = [&](float m2, float l2, const float* src) {
+      if (m2 == -INFINITY) return;        // saw no key
+      const float mm = fmaxf(m, m2);
+      const float x = m == -INFINITY ? 0.f : ex2_mufu(m - mm), y = ex2_mufu(m2 - mm);
+      l = l * x + l2 * y;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = acc[e] * x + src[lane * E + e] * y;
+      m = mm;
+    };
+    if (query) {
+      for (int w = 0; w < p.ways; ++w)
+        fold_in(it_ml[(w * ROWS + n) * 2], it_ml[(w * ROWS + n) * 2 + 1],
+                it_o + (w * ROWS + n) * LD);
+      if (p.has_doc) {
+        const int64_t dr = (int64_t)row * p.g + hb + n % nh;
+        const int u = kvh * p.plan.G + (int)(dr / kGroupRows);
+        const int64_t ub = plan_unit_begin(p.plan, u);
+        const int d0 = plan_cta_of(p.plan, ub);
+        const int d1 = plan_cta_of(p.plan, ub + p.plan.T - 1);
+        const int64_t sl0 = (int64_t)u * p.plan.max_chunks * kGroupRows + dr % kGroupRows;
+        for (int d = d0; d <= d1; ++d) {
+          const int64_t sl = sl0 + (int64_t)(d - d0) * kGroupRows;
+          const float2 ml = *reinterpret_cast<const float2*>(p.doc_ml + sl * 2);
+          fold_in(ml.x, ml.y, p.doc_o + sl * D);
+        }
+      }
+    }
+    const bool any = query && m != -INFINITY;
+    const float inv = any ? 1.f / l : 0.f;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + ((int64_t)row * p.Hq + head) * D + lane * E);
+#pragma unroll
+    for (int e = 0; e < E; e += 2) dst[e / 2] = any ? f2_to_bf2(acc[e] * inv, acc[e + 1] * inv) : 0u;
+    if (p.lse && lane == 0)
+      p.lse[(int64_t)row * p.Hq + head] = any ? (m + log2f(l)) * kLn2 : -INFINITY;
+  }
+}
+
+template <int D, int NT>
+cudaError_t launch(const Attn8Params& p, int warps, cudaStream_t st) {
+  const int smem = warps * 8 * NT * (D + 4 + 2) * (int)sizeof(float);
+  static std::atomic<uint64_t> ready{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(ready.load() & bit)) {
+    e = cudaFuncSetAttribute(kv8_attn<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kMaxWays * 8 * NT * (D + 6) * (int)sizeof(float));
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(bit);
+  }
+  const int per = warps / p.ways;
+  const int64_t grid = ((int64_t)p.n_items + per - 1) / per;
+  kv8_attn<D, NT><<<(unsigned)grid, warps * 32, smem, st>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_kv8_attn(const pp_kv8_layer& L, int doc_len, const uint16_t* q, int64_t q_ld,
+                            int Hq, const int16_t* q_sid, const int32_t* q_pos, int rows,
+                            bool one_row_per_stream, float scale, const SplitPlan& plan,
+                            bool doc_pass, const Partials& part, uint16_t* o, float* lse,
+                            int num_sms, cudaStream_t st) {
+  Attn8Params p{};
+  p.L = L;
+  p.q = q; p.q_ld = q_ld;
+  p.Hq = Hq;
+  p.g = Hq / L.H;
+  // A decode step's rows belong to different streams, an item each; question
+  // rows share their segment, so 16 (row, head) pairs go together.
+  const int most = one_row_per_stream && p.g <= 8 ? 8 : 16;
+  p.hg = p.g < most ? p.g : most;
+  p.gt = (p.g + p.hg - 1) / p.hg;
+  p.rt = one_row_per_stream ? 1 : most / p.hg;
+  p.rows = rows;
+  const int64_t items = (int64_t)((rows + p.rt - 1) / p.rt) * L.H * p.gt;
+  if (items > 0x7fffffff / 16) return cudaErrorInvalidValue;
+  p.n_items = (int)items;
+  p.q_sid = q_sid; p.q_pos = q_pos;
+  p.doc_len = doc_pass ? 0 : doc_len;
+  p.sl2 = scale * kLog2e;
+  p.has_doc = doc_pass ? 1 : 0;
+  p.plan = plan;
+  p.doc_o = part.doc_o; p.doc_ml = part.doc_ml;
+  p.o = o; p.lse = lse;
+  // Warps per item: enough to fill the GPU when items are few, and a long
+  // segment cut so that one item is not a CTA's whole tail; at least four
+  // chunks a warp.
+  const int64_t chunks = (int64_t)L.seg_pages * L.page / 16 + (p.doc_len + 15) / 16;
+  int ways = 1;
+  while (ways < kMaxWays && chunks / (2 * ways) >= 4 &&
+         (items * ways < 12LL * num_sms || (ways < 4 && chunks / ways > 16)))
+    ways *= 2;
+  p.ways = ways;
+  p.lper = L.page == 16 ? 0 : L.page == 32 ? 1 : L.page == 64 ? 2 : 3;
+  const int warps = ways > 4 ? ways : 4;
+  if (L.d == 128)
+    return most == 8 ? launch<128, 1>(p, warps, st) : launch<128, 2>(p, warps, st);
+  return most == 8 ? launch<64, 1>(p, warps, st) : launch<64, 2>(p, warps, st);
+}
+
+}  // namespace pp

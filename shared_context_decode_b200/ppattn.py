@@ -8,6 +8,7 @@ fallback of any kind.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -31,6 +32,10 @@ PP_DEV_SEGMENT_OVERFLOW = 0x1
 PP_DEV_DOC_OUT_OF_RANGE = 0x2
 PP_DEV_BAD_STREAM = 0x4
 PP_DEV_TIMEOUT = 0x8
+PP_DEV_BAD_POSITION = 0x10
+PP_DEV_BAD_PAGE = 0x20
+PP_DEV_ROW_ORDER = 0x40
+PP_DEV_NONFINITE = 0x80
 
 _i32, _vp, _sz = ctypes.c_int32, ctypes.c_void_p, ctypes.c_size_t
 
@@ -64,7 +69,20 @@ class Options(ctypes.Structure):
         self.events = ctypes.cast(self._ev, ctypes.POINTER(_vp))
 
 
+class KV8LayerStruct(ctypes.Structure):
+    _fields_ = [("H", _i32), ("d", _i32), ("page", _i32), ("n_pages", _i32), ("P_max", _i32),
+                ("seg_pages", _i32), ("doc_pages", _i32), ("pos0", _i32), ("k", _vp), ("v", _vp),
+                ("k_scale", _vp), ("v_scale", _vp), ("doc_table", _vp), ("seg_table", _vp),
+                ("status", _vp)]
+
+
+class RopeStruct(ctypes.Structure):
+    _fields_ = [("dim", _i32), ("interleaved", _i32), ("max_pos", _i32), ("reserved", _i32),
+                ("cos_sin", _vp)]
+
+
 _LP = ctypes.POINTER(LayerStruct)
+_LP8 = ctypes.POINTER(KV8LayerStruct)
 _OP = ctypes.POINTER(Options)
 
 
@@ -100,13 +118,26 @@ _reset_streams = _sig("pp_kv_reset_streams", _i32, _LP, _vp, _i32, _vp)
 _doc_ws = _sig("pp_doc_prefill_workspace_bytes", _sz, _i32, _i32, _i32, _OP)
 _doc_prefill = _sig("pp_doc_prefill_attn", _i32, _LP, _i32, _vp, ctypes.c_float, _vp, _vp, _vp,
                     _sz, _OP, _vp)
+_i64 = ctypes.c_int64
+_kv8_reset = _sig("pp_kv8_reset", _i32, _LP8, _vp)
+_kv8_append = _sig("pp_kv8_append", _i32, _LP8, _vp, _i64, _vp, _i64, _vp, _i64, _i32, _vp, _vp,
+                   _i32, ctypes.POINTER(RopeStruct), _vp, _i64, _vp)
+_kv8_dec_ws = _sig("pp_kv8_decode_workspace_bytes", _sz, _i32, _i32, _i32, _i32, _i32, _OP)
+_kv8_pre_ws = _sig("pp_kv8_prefill_workspace_bytes", _sz, _i32, _i32, _i32, _i32, _i32, _OP)
+_kv8_decode = _sig("pp_kv8_decode_attn", _i32, _LP8, _i32, _vp, _i64, _i32, _vp, _vp, _i32,
+                   ctypes.c_float, _vp, _vp, _vp, _sz, _OP, _vp)
+_kv8_prefill = _sig("pp_kv8_prefill_attn", _i32, _LP8, _i32, _vp, _i64, _i32, _vp, _vp, _i32,
+                    ctypes.c_float, _vp, _vp, _vp, _sz, _OP, _vp)
+_kv8_status = _sig("pp_kv8_get_device_status", _i32, _LP8, ctypes.POINTER(_i32), _vp)
 
 EXPORTED = ("pp_status_str", "pp_abi_version", "pp_kv_reset", "pp_kv_append",
             "pp_decode_workspace_bytes", "pp_prefill_workspace_bytes", "pp_decode_attn",
             "pp_prefill_attn", "pp_debug_visibility", "pp_get_device_status",
             "pp_debug_split_plan", "pp_debug_exp2", "pp_decode_attn_noalloc",
             "pp_doc_prefill_workspace_bytes", "pp_doc_prefill_attn", "pp_debug_split_plan_causal",
-            "pp_kv_reset_streams", "pp_decode_step")
+            "pp_kv_reset_streams", "pp_decode_step", "pp_kv8_reset", "pp_kv8_append",
+            "pp_kv8_decode_workspace_bytes", "pp_kv8_prefill_workspace_bytes",
+            "pp_kv8_decode_attn", "pp_kv8_prefill_attn", "pp_kv8_get_device_status")
 
 # Size of the scratch array built into the library for pp_decode_attn_noalloc.
 NOALLOC_SCRATCH_BYTES = 32 << 20
@@ -396,6 +427,221 @@ def device_status_code(layer: KVLayer):
     if rc not in (PP_OK, PP_ERR_DEVICE_TIMEOUT):
         _check(rc, "pp_get_device_status")
     return rc, int(out.value)
+
+
+# --------------------------------------------------- 8-bit paged cache ---
+class KV8Layer:
+    """One layer's 8-bit paged KV cache (pp_kv8_layer).
+
+    k, v [n_pages, H, page, d] float8_e4m3fn; k_scale, v_scale [n_pages, H]
+    float32; doc_table [doc_pages] int32; seg_table [P_max, seg_pages] int32;
+    status [1] int32.  Buffers not given are allocated: pages zero, scales 1,
+    tables -1 (no page).  pos0: position of every stream's first token.
+    """
+
+    def __init__(self, H: int, d: int, page: int, n_pages: int, P_max: int, seg_pages: int,
+                 doc_pages: int, pos0: int, device="cuda", *, k: Optional[torch.Tensor] = None,
+                 v: Optional[torch.Tensor] = None, k_scale: Optional[torch.Tensor] = None,
+                 v_scale: Optional[torch.Tensor] = None,
+                 doc_table: Optional[torch.Tensor] = None,
+                 seg_table: Optional[torch.Tensor] = None):
+        dev = torch.device(device)
+        if dev.type == "cuda" and dev.index is None:
+            dev = torch.device("cuda", torch.cuda.current_device())
+        self.device = dev
+        self.H, self.d, self.page, self.n_pages = H, d, page, n_pages
+        self.P_max, self.seg_pages, self.doc_pages, self.pos0 = P_max, seg_pages, doc_pages, pos0
+
+        def buf(t, name, shape, dtype, fill):
+            if t is None:
+                if dtype == torch.float8_e4m3fn:
+                    return torch.zeros(shape, dtype=torch.uint8, device=dev).view(dtype)
+                return torch.full(shape, fill, dtype=dtype, device=dev)
+            _want(t, dtype, name, dev)
+            if tuple(t.shape) != shape:
+                raise ValueError(f"KV8Layer: {name} must be {list(shape)}, got {list(t.shape)}")
+            return t
+
+        f8 = torch.float8_e4m3fn
+        self.k = buf(k, "k", (n_pages, H, page, d), f8, 0)
+        self.v = buf(v, "v", (n_pages, H, page, d), f8, 0)
+        self.k_scale = buf(k_scale, "k_scale", (n_pages, H), torch.float32, 1.0)
+        self.v_scale = buf(v_scale, "v_scale", (n_pages, H), torch.float32, 1.0)
+        self.doc_table = buf(doc_table, "doc_table", (doc_pages,), torch.int32, -1)
+        self.seg_table = buf(seg_table, "seg_table", (P_max, seg_pages), torch.int32, -1)
+        self.status = torch.zeros((1,), dtype=torch.int32, device=dev)
+        self.struct = KV8LayerStruct(H, d, page, n_pages, P_max, seg_pages, doc_pages, pos0,
+                                     self.k.data_ptr(), self.v.data_ptr(),
+                                     self.k_scale.data_ptr(), self.v_scale.data_ptr(),
+                                     self.doc_table.data_ptr(), self.seg_table.data_ptr(),
+                                     self.status.data_ptr())
+        self.ref = ctypes.byref(self.struct)
+
+    def nbytes(self) -> int:
+        return sum(t.numel() * t.element_size() for t in
+                   (self.k, self.v, self.k_scale, self.v_scale, self.doc_table, self.seg_table,
+                    self.status))
+
+
+class Rope:
+    """Position rotation (pp_rope) from a table cos_sin [max_pos, dim] float32:
+    dim/2 cosines, then dim/2 sines, of positions 0 .. max_pos-1."""
+
+    def __init__(self, cos_sin: torch.Tensor, interleaved: bool = False):
+        if cos_sin.dim() != 2:
+            raise ValueError("Rope: cos_sin must be [max_pos, dim]")
+        _want(cos_sin, torch.float32, "cos_sin", cos_sin.device)
+        self.cos_sin, self.interleaved = cos_sin, bool(interleaved)
+        self.max_pos, self.dim = cos_sin.shape
+        self.struct = RopeStruct(self.dim, int(self.interleaved), self.max_pos, 0,
+                                 cos_sin.data_ptr())
+        self.ref = ctypes.byref(self.struct)
+
+    @classmethod
+    def make(cls, max_pos: int, dim: int, theta: float = 10000.0, interleaved: bool = False,
+             device="cuda") -> "Rope":
+        """Angles pos * theta^(-2j/dim), taken in 64 bits."""
+        inv = theta ** (-torch.arange(0, dim, 2, dtype=torch.float64, device=device) / dim)
+        ang = torch.arange(max_pos, dtype=torch.float64, device=device)[:, None] * inv
+        return cls(torch.cat([ang.cos(), ang.sin()], 1).to(torch.float32).contiguous(),
+                   interleaved)
+
+
+def _rows(t: torch.Tensor, name: str, n: int, heads: int, d: int, device) -> int:
+    """Checks rows [n, heads, d] bf16 whose heads are packed and whose rows may
+    be strided; returns the elements between rows."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.shape != (n, heads, d):
+        raise ValueError(f"{name} must be [{n}, {heads}, {d}], got {list(t.shape)}")
+    s0, s1, s2 = t.stride()
+    if n <= 1:
+        s0 = heads * d if n == 0 or s0 < heads * d or s0 % 8 else s0
+    if n and (s2 != 1 or (heads > 1 and s1 != d) or s0 < heads * d or s0 % 8):
+        raise ValueError(f"{name}: heads must be packed, rows at least heads * d apart and a "
+                         f"multiple of 8 elements (strides {t.stride()})")
+    return s0
+
+
+def _on(device):
+    """The device a call launches on, made current where it is not."""
+    return contextlib.nullcontext() if torch.cuda.current_device() == device.index \
+        else torch.cuda.device(device)
+
+
+def kv8_reset(layer: KV8Layer):
+    """Clear the layer's status word."""
+    with _on(layer.device):
+        _check(_kv8_reset(layer.ref, _stream(layer.device)), "pp_kv8_reset")
+
+
+def kv8_append(layer: KV8Layer, k: torch.Tensor, v: torch.Tensor, sid: torch.Tensor,
+               pos: torch.Tensor, rope: Optional[Rope] = None, q: Optional[torch.Tensor] = None,
+               q_out: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
+    """Append rows k, v [n, H, d] bf16 (rows may be strided) with stream ids
+    sid [n] int16 and positions pos [n] int32: keys rotated by `rope`, both
+    quantised into the streams' pages.  q [n, Hq, d]: queries to rotate as
+    well; returns q_out (new, given, or q itself)."""
+    dev = layer.device
+    _want(sid, torch.int16, "sid", dev)
+    _want(pos, torch.int32, "pos", dev)
+    if sid.dim() != 1 or pos.shape != sid.shape:
+        raise ValueError("kv8_append: sid and pos must be [n]")
+    n = sid.shape[0]
+    k_ld = _rows(k, "k", n, layer.H, layer.d, dev)
+    v_ld = _rows(v, "v", n, layer.H, layer.d, dev)
+    if rope is not None and rope.cos_sin.device != dev:
+        raise ValueError(f"rope must be on {dev}, got {rope.cos_sin.device}")
+    Hq = q_ld = qo_ld = 0
+    if q is not None:
+        if q.dim() != 3:
+            raise ValueError("q must be [n, Hq, d]")
+        Hq = q.shape[1]
+        q_ld = _rows(q, "q", n, Hq, layer.d, dev)
+        if q_out is None:
+            q_out = torch.empty((n, Hq, layer.d), dtype=torch.bfloat16, device=dev)
+        qo_ld = _rows(q_out, "q_out", n, Hq, layer.d, dev)
+    elif q_out is not None:
+        raise ValueError("kv8_append: q_out without q")
+    with _on(dev):
+        _check(_kv8_append(layer.ref, k.data_ptr(), k_ld, v.data_ptr(), v_ld,
+                           None if q is None else q.data_ptr(), q_ld, Hq, sid.data_ptr(),
+                           pos.data_ptr(), n, None if rope is None else rope.ref,
+                           None if q_out is None else q_out.data_ptr(), qo_ld, _stream(dev)),
+               "pp_kv8_append")
+    return q_out
+
+
+def kv8_decode_workspace_bytes(P: int, Hq: int, H: int, d: int, doc_len: int,
+                               opt: Optional[Options] = None) -> int:
+    return int(_kv8_dec_ws(P, Hq, H, d, doc_len, _opts(opt)))
+
+
+def kv8_prefill_workspace_bytes(R: int, Hq: int, H: int, d: int, doc_len: int,
+                                opt: Optional[Options] = None) -> int:
+    return int(_kv8_pre_ws(R, Hq, H, d, doc_len, _opts(opt)))
+
+
+def _kv8_attn(fn, name, layer, doc_len, q, q_sid, q_pos, scale, o, lse, ws, opt, ws_fn):
+    dev = layer.device
+    _want(q_sid, torch.int16, "q_sid", dev)
+    _want(q_pos, torch.int32, "q_pos", dev)
+    rows = q_sid.shape[0]
+    if q.dim() != 3 or q_sid.dim() != 1 or q_pos.shape != (rows,):
+        raise ValueError(f"{name}: q must be [rows, Hq, d], q_sid and q_pos [rows]")
+    Hq = q.shape[1]
+    q_ld = _rows(q, "q", rows, Hq, layer.d, dev)
+    if o is None:
+        o = torch.empty((rows, Hq, layer.d), dtype=torch.bfloat16, device=dev)
+    _want(o, torch.bfloat16, "o", dev)
+    if o.shape != q.shape:
+        raise ValueError(f"{name}: o must be [rows, Hq, d]")
+    if lse is not None:
+        _want(lse, torch.float32, "lse", dev)
+        if lse.shape != (rows, Hq):
+            raise ValueError(f"{name}: lse must be [rows, Hq]")
+    with _on(dev):
+        if ws is None:
+            ws = workspace(ws_fn(rows, Hq, layer.H, layer.d, doc_len, opt), dev)
+        _want(ws, torch.uint8, "ws", dev)
+        _check(fn(layer.ref, doc_len, q.data_ptr(), q_ld, Hq, q_sid.data_ptr(), q_pos.data_ptr(),
+                  rows, scale, o.data_ptr(), None if lse is None else lse.data_ptr(),
+                  ws.data_ptr(), ws.numel(), _opts(opt), _stream(dev)), name)
+    return o
+
+
+def kv8_decode_attn(layer: KV8Layer, doc_len: int, q: torch.Tensor, q_sid: torch.Tensor,
+                    q_pos: torch.Tensor, scale: float, o: Optional[torch.Tensor] = None,
+                    lse: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+                    opt: Optional[Options] = None) -> torch.Tensor:
+    """Decode attention of P rows (one per stream) over the 8-bit cache; q
+    [P, Hq, d] bf16, already rotated.  Returns o [P, Hq, d] bf16."""
+    return _kv8_attn(_kv8_decode, "pp_kv8_decode_attn", layer, doc_len, q, q_sid, q_pos, scale, o,
+                     lse, ws, opt, kv8_decode_workspace_bytes)
+
+
+def kv8_prefill_attn(layer: KV8Layer, doc_len: int, q: torch.Tensor, q_sid: torch.Tensor,
+                     q_pos: torch.Tensor, scale: float, o: Optional[torch.Tensor] = None,
+                     lse: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+                     opt: Optional[Options] = None) -> torch.Tensor:
+    """Question-prefill attention of R rows over the 8-bit cache; returns
+    o [R, Hq, d] bf16."""
+    return _kv8_attn(_kv8_prefill, "pp_kv8_prefill_attn", layer, doc_len, q, q_sid, q_pos, scale,
+                     o, lse, ws, opt, kv8_prefill_workspace_bytes)
+
+
+def kv8_device_status(layer: KV8Layer) -> int:
+    """The 8-bit layer's device status word (PP_DEV_* bits)."""
+    out = _i32(0)
+    with _on(layer.device):
+        rc = int(_kv8_status(layer.ref, ctypes.byref(out), _stream(layer.device)))
+    if rc not in (PP_OK, PP_ERR_DEVICE_TIMEOUT):
+        _check(rc, "pp_kv8_get_device_status")
+    return int(out.value)
 
 
 def split_plan(rows: int, H: int, doc_len: int, ctas: int, causal: bool = False):

@@ -1,0 +1,331 @@
+"""8-bit paged cache on the GPU: decode and question prefill attention against
+the fp64 oracle over the dequantised rows."""
+import numpy as np
+import pytest
+import torch
+
+from tests.kv8_util import check, make_cache, oracle_attn, pp
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def queries(rows, Hq, d, seed, pad=0):
+    """Query rows, `pad` further heads between them (a fused projection's)."""
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn((rows, Hq + pad, d), generator=g).to(torch.bfloat16).to(DEV)
+    return x[:, :Hq]
+
+
+def ids(sid, pos):
+    return (torch.tensor(sid, dtype=torch.int16, device=DEV),
+            torch.tensor(pos, dtype=torch.int32, device=DEV))
+
+
+def run(layer, doc, segs, N, sid, pos, g, kind, seed=1, doc_len=None, pad=0, what="", opt=None):
+    m = pp()
+    rows, Hq = len(sid), layer.H * g
+    q = queries(rows, Hq, layer.d, seed, pad)
+    qs, qp = ids(sid, pos)
+    scale = layer.d ** -0.5
+    o = torch.full((rows + 2, Hq, layer.d), 9.0, dtype=torch.bfloat16, device=DEV)
+    lse = torch.full((rows + 2, Hq), 9.0, device=DEV)
+    fn = m.kv8_decode_attn if kind == "decode" else m.kv8_prefill_attn
+    dl = N if doc_len is None else doc_len
+    fn(layer, dl, q, qs, qp, scale, o=o[:rows], lse=lse[:rows], opt=opt)
+    torch.cuda.synchronize()
+    assert (o[rows:] == 9).all() and (lse[rows:] == 9).all()     # rows behind the last one
+    ref = oracle_attn(doc, segs, N, q.cpu(), np.array(sid), np.array(pos), scale, dl)
+    check(o[:rows], lse[:rows], ref, what)
+    return q, o[:rows], lse[:rows]
+
+
+# heads, query heads per head, d, page, document, streams
+SHAPES = [
+    (1, 1, 64, 16, 1, 1), (2, 1, 128, 16, 0, 5), (4, 2, 64, 16, 257, 16), (3, 7, 128, 32, 1001, 9),
+    (2, 4, 128, 64, 130, 61), (1, 16, 64, 128, 300, 3), (1, 33, 128, 16, 129, 4),
+    (8, 1, 128, 32, 640, 130), (2, 3, 64, 64, 2049, 100), (2, 8, 128, 16, 999, 70),
+]
+
+
+@pytest.mark.parametrize("H,g,d,page,N,P", SHAPES)
+def test_decode(H, g, d, page, N, P):
+    rng = np.random.default_rng(N + P)
+    lens = [int(x) for x in rng.integers(1, 90, P)]
+    layer, doc, segs = make_cache(H, d, page, N, lens, seed=N)
+    sid = [s + 1 for s in rng.permutation(P)]
+    pos = [N + lens[s - 1] - 1 for s in sid]
+    run(layer, doc, segs, N, sid, pos, g, "decode", pad=1)
+    assert pp().kv8_device_status(layer) == 0
+    sid[0] = -1                          # inactive rows, rows that see nothing of their segment
+    if P > 2:
+        sid[2] = -1
+        pos[1] = N - 1
+    run(layer, doc, segs, N, sid, pos, g, "decode", seed=2)
+    run(layer, doc, segs, N, sid, pos, g, "decode", seed=3, doc_len=0)
+    if N > 3:                            # a document read in part
+        run(layer, doc, segs, N, sid, pos, g, "decode", seed=3, doc_len=N - 3)
+    assert pp().kv8_device_status(layer) == 0
+
+
+@pytest.mark.parametrize("H,g,d,page,N,P", SHAPES)
+def test_prefill(H, g, d, page, N, P):
+    rng = np.random.default_rng(N + P)
+    lens = [int(x) for x in rng.integers(1, 40, P)]
+    layer, doc, segs = make_cache(H, d, page, N, lens, seed=N + 1)
+    order = rng.permutation(P)
+    sid = sum(([int(s) + 1] * lens[s] for s in order), [])
+    pos = sum((list(range(N, N + lens[s])) for s in order), [])
+    run(layer, doc, segs, N, sid, pos, g, "prefill", pad=2)
+    # any order, idle rows among them, a part of the rows only
+    mix = rng.permutation(len(sid))[:max(1, len(sid) * 2 // 3)]
+    sid, pos = [sid[i] if i % 7 else -1 for i in mix], [pos[i] for i in mix]
+    run(layer, doc, segs, N, sid, pos, g, "prefill", seed=4)
+    run(layer, doc, segs, N, sid, pos, g, "prefill", seed=5, doc_len=0)
+    assert pp().kv8_device_status(layer) == 0
+
+
+def test_more_rows_than_one_group():
+    """Row groups of 256 (row, head) pairs, the last one partly filled."""
+    lens = [20] * 30
+    layer, doc, segs = make_cache(2, 128, 32, 700, lens, seed=3)
+    sid = sum(([s + 1] * 20 for s in range(30)), [])[:-7]
+    pos = (list(range(700, 720)) * 30)[:-7]
+    run(layer, doc, segs, 700, sid, pos, 1, "prefill")
+    run(layer, doc, segs, 700, sid, pos, 3, "prefill")
+
+
+def test_long_segments():
+    lens = [1, 1500, 3, 700, 64]
+    layer, doc, segs = make_cache(2, 64, 16, 50, lens, seed=5)
+    sid = [1, 2, 3, 4, 5]
+    run(layer, doc, segs, 50, sid, [50 + n - 1 for n in lens], 4, "decode")
+    run(layer, doc, segs, 50, [2] * 40 + [4] * 3, list(range(1510, 1550)) + [749, 50, 700], 2, "prefill")
+
+
+def test_all_rows_idle_and_no_rows():
+    m = pp()
+    layer, doc, segs = make_cache(2, 64, 16, 40, [3, 4], seed=6)
+    run(layer, doc, segs, 40, [-1, -1], [0, 0], 2, "decode")
+    run(layer, doc, segs, 40, [-1], [0], 2, "prefill")
+    q = queries(0, 4, 64, 1)
+    s, p = ids([], [])
+    assert m.kv8_decode_attn(layer, 40, q, s, p, 0.1).shape == (0, 4, 64)
+
+
+def test_rows_of_no_stream_are_zero_and_reported():
+    m = pp()
+    layer, doc, segs = make_cache(2, 64, 16, 300, [3, 4, 5], seed=7)
+    for fn in (m.kv8_decode_attn, m.kv8_prefill_attn):
+        q = queries(3, 2, 64, 1)
+        s, p = ids([0, 4, 2], [300, 300, 302])
+        lse = torch.zeros((3, 2), device=DEV)
+        o = fn(layer, 300, q, s, p, 0.125, lse=lse)
+        torch.cuda.synchronize()
+        assert m.kv8_device_status(layer) == m.PP_DEV_BAD_STREAM
+        m.kv8_reset(layer)
+        assert (o[:2] == 0).all() and (lse[:2] == -torch.inf).all()
+        ref = oracle_attn(doc, segs, 300, q.cpu()[2:], np.array([2]), np.array([302]), 0.125)
+        check(o[2:], lse[2:], ref)
+
+
+@pytest.mark.parametrize("N", [40, 700])
+def test_pages_that_are_not_there_are_skipped(N):
+    m = pp()
+    layer, doc, segs = make_cache(2, 128, 16, N, [40, 20], seed=8)
+    layer.doc_table[1] = -1
+    layer.doc_table[2] = layer.n_pages
+    layer.seg_table[0, 1] = -7
+    keep = torch.ones(N, dtype=torch.bool)
+    keep[16:48] = False
+    doc2 = [x[keep] for x in doc]
+    ks = torch.ones(40, dtype=torch.bool)
+    ks[16:32] = False
+    segs2 = [[x[ks] for x in segs[0]], segs[1]]
+    q = queries(2, 4, 128, 1)
+    s, p = ids([1, 2], [N + 39, N + 19])
+    n2 = int(keep.sum())
+    for fn in (m.kv8_decode_attn, m.kv8_prefill_attn):
+        lse = torch.zeros((2, 4), device=DEV)
+        o = fn(layer, N, q, s, p, 0.09, lse=lse)
+        torch.cuda.synchronize()
+        assert m.kv8_device_status(layer) == m.PP_DEV_BAD_PAGE
+        m.kv8_reset(layer)
+        ref = oracle_attn(doc2, segs2, n2, q.cpu(), np.array([1, 2]), np.array([n2 + 39, n2 + 19]), 0.09)
+        check(o, lse, ref)
+
+
+@pytest.mark.parametrize("N", [40, 900])
+@pytest.mark.parametrize("kind", ["decode", "prefill"])
+def test_nan_reaches_the_rows_that_see_it_and_no_others(N, kind):
+    m = pp()
+    layer, doc, segs = make_cache(2, 64, 32, N, [30, 30, 30], seed=9)
+    fn = m.kv8_decode_attn if kind == "decode" else m.kv8_prefill_attn
+    q = queries(3, 4, 64, 1)
+    s, p = ids([1, 2, 3], [N + 19, N + 20, N + 29])
+    scale = 0.125
+
+    def go():
+        lse = torch.zeros((3, 4), device=DEV)
+        o = fn(layer, N, q, s, p, scale, lse=lse)
+        torch.cuda.synchronize()
+        return o, lse
+
+    # key 20 of stream 2, head 1: its row sees it, nobody else does
+    pg = int(layer.seg_table[1, 0])
+    layer.k.view(torch.uint8)[pg, 1, 20, 0] = 0x7f
+    pg = int(layer.seg_table[0, 0])
+    layer.k.view(torch.uint8)[pg, 0, 20, 0] = 0x7f       # behind row 0's position
+    o, lse = go()
+    assert o[1, 2:].isnan().all() and lse[1, 2:].isnan().all()
+    o[1, 2:], lse[1, 2:] = 0, 0
+    assert not o.isnan().any() and not lse.isnan().any()
+    ref = oracle_attn(doc, segs, N, q.cpu()[[0, 2]], np.array([1, 3]), np.array([N + 19, N + 29]), scale)
+    check(o[[0, 2]], lse[[0, 2]], ref)
+    # a document key: everybody in its head
+    layer.k.view(torch.uint8)[int(layer.doc_table[N // 32]), 0, N % 32 - 1, 0] = 0x7f
+    o, lse = go()
+    assert o[:, :2].isnan().all() and lse[:, :2].isnan().all()
+    assert not o[0, 2:].isnan().any() and not o[2, 2:].isnan().any()
+
+
+@pytest.mark.parametrize("N", [0, 40, 900])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_non_finite_queries_give_nan_in_their_row(N, bad):
+    m = pp()
+    layer, doc, segs = make_cache(2, 64, 32, N, [30, 30, 30], seed=9)
+    q = queries(3, 4, 64, 1)
+    q[1, 2, 60] = bad
+    s, p = ids([1, 2, 3], [N + 19, N + 20, N + 29])
+    for fn in (m.kv8_decode_attn, m.kv8_prefill_attn):
+        lse = torch.zeros((3, 4), device=DEV)
+        o = fn(layer, N, q, s, p, 0.125, lse=lse)
+        torch.cuda.synchronize()
+        assert o[1, 2].isnan().all() and lse[1, 2].isnan()
+        o[1, 2], lse[1, 2] = 0, 0
+        assert not o.isnan().any() and not lse.isnan().any()
+
+
+@pytest.mark.parametrize("d,N", [(64, 100), (128, 1500)])
+def test_scales_far_apart_and_large_scores(d, N):
+    """Pages 2^-30 to 2^30 apart in value scale; keys large enough that one key
+    takes all the weight."""
+    m = pp()
+    layer, doc, segs = make_cache(1, d, 16, N, [50, 20], seed=10)
+    g = torch.Generator().manual_seed(3)
+    e = torch.randint(-30, 31, layer.v_scale.shape, generator=g).float()
+    old = layer.v_scale.cpu()
+    layer.v_scale.copy_(torch.exp2(e - 6))
+    ratio = torch.exp2(e - 6) / old
+    layer.k_scale *= 16
+
+    def scaled(x, tab, n):
+        f = ratio[tab.cpu().long()][:, :, None, None].expand(-1, -1, 16, d)
+        return x * f.transpose(1, 2).reshape(-1, 1, d)[:n]
+
+    doc = [doc[0] * 16, scaled(doc[1], layer.doc_table, N)]
+    segs = [[sg[0] * 16, scaled(sg[1], layer.seg_table[i], len(sg[0]))] for i, sg in enumerate(segs)]
+    q = queries(2, 3, d, 1)
+    s, p = ids([1, 2], [N + 49, N + 19])
+    lse = torch.zeros((2, 3), device=DEV)
+    o = m.kv8_decode_attn(layer, N, q, s, p, d ** -0.5, lse=lse)
+    torch.cuda.synchronize()
+    ro, rl, ra = oracle_attn(doc, segs, N, q.cpu(), np.array([1, 2]), np.array([N + 49, N + 19]), d ** -0.5)
+    # scores reach |q||k| scale ~ 600: their fp32 sums err by up to 2^-24 * 128
+    # terms * 600 ~ 2^-8 in the worst case, so probabilities by 2^-8 relative
+    # (and lse by as much), beside the 2^-8 + 2^-10 of their own rounding
+    err = np.abs(o.float().cpu().numpy() - ro)
+    assert np.isfinite(o.float().cpu().numpy()).all()
+    assert (err <= 2.0 ** -8 * np.abs(ro) + (2.0 ** -7 + 2.0 ** -8 + 2.0 ** -10) * ra + 1e-30).all()
+    assert np.abs(lse.cpu().numpy() - rl).max() <= 2.0 ** -8
+
+
+def test_one_workspace_serves_calls_in_order_and_graphs_replay():
+    m = pp()
+    N, P = 1100, 140
+    lens = [10 + i % 50 for i in range(P)]
+    layer, doc, segs = make_cache(2, 128, 32, N, lens, seed=11)
+    q = queries(P, 4, 128, 1)
+    s, p = ids(list(range(1, P + 1)), [N + n - 1 for n in lens])
+    n_ws = max(m.kv8_decode_workspace_bytes(P, 4, 2, 128, N), m.kv8_prefill_workspace_bytes(P, 4, 2, 128, N))
+    ws = m.workspace(n_ws, DEV)
+    ws.fill_(0xff)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        want = m.kv8_decode_attn(layer, N, q, s, p, 0.09, ws=ws)
+        want2 = m.kv8_prefill_attn(layer, N, q, s, p, 0.09, ws=ws)
+        again = m.kv8_decode_attn(layer, N, q, s, p, 0.09, ws=ws)
+    st.synchronize()
+    assert torch.equal(want, again)
+    o, o2 = torch.empty_like(want), torch.empty_like(want)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=st):
+        m.kv8_decode_attn(layer, N, q, s, p, 0.09, o=o, ws=ws)
+        m.kv8_prefill_attn(layer, N, q, s, p, 0.09, o=o2, ws=ws)
+    for _ in range(2):
+        o.zero_()
+        o2.zero_()
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, want) and torch.equal(o2, want2)
+    ref = oracle_attn(doc, segs, N, q.cpu(), s.cpu().numpy(), p.cpu().numpy(), 0.09)
+    check(want, None, ref)
+    check(want2, None, ref)
+    # calls at once on two streams, each with its own workspace
+    st2, ws2 = torch.cuda.Stream(), m.workspace(n_ws, DEV)
+    st2.wait_stream(torch.cuda.current_stream())
+    st.wait_stream(torch.cuda.current_stream())
+    for i in range(4):
+        with torch.cuda.stream(st):
+            m.kv8_decode_attn(layer, N, q, s, p, 0.09, o=o, ws=ws)
+        with torch.cuda.stream(st2):
+            m.kv8_prefill_attn(layer, N, q, s, p, 0.09, o=o2, ws=ws2)
+    torch.cuda.synchronize()
+    assert torch.equal(o, want) and torch.equal(o2, want2)
+
+
+def test_serving_run():
+    """A document, its questions and some answer tokens through append, prefill
+    and decode, as a program would run them; each attention against the oracle
+    over the cache's own dequantised rows."""
+    from oracle.kv8 import Kv8Replay
+    m = pp()
+    H, g, d, page, N, P = 2, 4, 64, 16, 345, 6
+    gen = torch.Generator().manual_seed(12)
+    rope = m.Rope.make(N + 100, d, device=DEV)
+    seg_pages, doc_pages = 5, -(-N // page)
+    tab = torch.randperm(doc_pages + P * seg_pages, generator=gen).to(torch.int32)
+    layer = m.KV8Layer(H, d, page, doc_pages + P * seg_pages, P, seg_pages, doc_pages, N, DEV,
+                       doc_table=tab[:doc_pages].to(DEV),
+                       seg_table=tab[doc_pages:].view(P, seg_pages).contiguous().to(DEV))
+    rep = Kv8Replay(H, d, page, layer.n_pages, N, tab[:doc_pages].numpy(),
+                    tab[doc_pages:].view(P, seg_pages).numpy())
+    have = [0] * P
+
+    def step(sid, pos, fn):
+        x = torch.randn((len(sid), (g + 2) * H, d), generator=gen).to(torch.bfloat16).to(DEV)
+        q, k, v = x[:, :g * H], x[:, g * H:(g + 1) * H], x[:, (g + 1) * H:]
+        s, p = ids(sid, pos)
+        qr = m.kv8_append(layer, k, v, s, p, rope=rope, q=q)
+        rep.append(k.float().cpu().numpy(), v.float().cpu().numpy(), sid, pos, rope.cos_sin.cpu().numpy())
+        if fn is None:
+            return
+        for i in sid:
+            have[i - 1] += 1
+        lse = torch.empty((len(sid), g * H), device=DEV)
+        o = fn(layer, N, qr, s, p, 0.125, lse=lse)
+        torch.cuda.synchronize()
+        doc = [torch.from_numpy(x).float() for x in rep.rows(0, N)]
+        segs = [[torch.from_numpy(x).float() for x in rep.rows(i + 1, have[i])] for i in range(P)]
+        check(o, lse, oracle_attn(doc, segs, N, qr.cpu(), np.array(sid), np.array(pos), 0.125))
+
+    step([0] * N, list(range(N)), None)
+    lens = [5, 17, 1, 32, 16, 9]
+    step(sum(([i + 1] * n for i, n in enumerate(lens)), []), sum((list(range(N, N + n)) for n in lens), []),
+         m.kv8_prefill_attn)
+    for t in range(6):
+        act = [i for i in range(P) if (i + t) % 5]
+        step([i + 1 for i in act], [N + have[i] for i in act], m.kv8_decode_attn)
+    assert m.kv8_device_status(layer) == 0
