@@ -8,6 +8,7 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include <algorithm>
+#include <cstdlib>
 #include <atomic>
 
 #include "common.cuh"
@@ -159,6 +160,14 @@ long long wait_limit(const pp_options* opt) {
   return 1LL << lg;
 }
 
+// Inside a stream capture the events become event-record nodes of the graph
+// (recorded at every replay), so per-kernel timing also works for graphs.
+cudaError_t record_mark(cudaEvent_t ev, cudaStreamCaptureStatus cap, cudaStream_t st) {
+  return cap == cudaStreamCaptureStatusActive
+             ? cudaEventRecordWithFlags(ev, st, cudaEventRecordExternal)
+             : cudaEventRecord(ev, st);
+}
+
 // Shared body of decode and prefill attention.
 // causal: a document prefill; rows = doc_len document tokens, no stream ids.
 // app_k, app_v: a decode step's new keys and values (one row per query row,
@@ -197,16 +206,9 @@ pp_status attend(const pp_kv_layer* L, int32_t doc_len, const uint16_t* q, const
   const Partials part = carve(ws, w);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaEvent_t* ev = (opt && opt->events) ? reinterpret_cast<cudaEvent_t*>(opt->events) : nullptr;
-  // Inside a stream capture the events become event-record nodes of the graph
-  // (recorded at every replay), so per-kernel timing also works for graphs.
   cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
   if (ev && cudaStreamIsCapturing(st, &cap) != cudaSuccess) return PP_ERR_CUDA;
-  auto mark = [&](int i) {
-    if (!ev) return cudaSuccess;
-    return cap == cudaStreamCaptureStatusActive
-               ? cudaEventRecordWithFlags(ev[i], st, cudaEventRecordExternal)
-               : cudaEventRecord(ev[i], st);
-  };
+  auto mark = [&](int i) { return ev ? record_mark(ev[i], cap, st) : cudaSuccess; };
   const bool other_doc = opt && (opt->ablation_doc_per_stream || opt->sibling_scan);
   // decode behind the tensor-core document pass: the suffix slices are
   // balanced by work, with counters that pass zeroes
@@ -311,6 +313,24 @@ bool row_operand(const void* ptr, int64_t ld, int64_t heads, int32_t d) {
   return ptr && aligned(ptr, 16) && ld % 8 == 0 && ld >= heads * d;
 }
 
+// Split of the document over the tensor-core pass's CTAs; C = 0: the document
+// is read by the segment kernel's warps instead (no pass, no workspace).
+SplitPlan kv8_plan(int32_t rows, int32_t Hq, int32_t H, int32_t doc_len, const pp_options* opt) {
+  const int ctas = (opt && opt->splits > 0) ? opt->splits : sm_count();
+  const char* e = getenv("PPKV8_DOC");
+  const int mode = e ? atoi(e) : 1;
+  if (mode == 0) return SplitPlan{};
+  return make_plan(rows * (Hq / H), H, doc_len, ctas);
+}
+
+WsLayout kv8_ws_layout(const SplitPlan& p, int d) {
+  WsLayout w{};
+  const size_t slots = p.C > 0 ? (size_t)p.units * p.max_chunks * pp::kGroupRows : 0;
+  w.doc_ml = up(slots * d * sizeof(float));
+  w.total = w.doc_ml + up(slots * 2 * sizeof(float));
+  return w;
+}
+
 pp_status kv8_append(const pp_kv8_layer* L, const uint16_t* k, int64_t k_ld, const uint16_t* v,
                      int64_t v_ld, const uint16_t* q, int64_t q_ld, int32_t Hq, const int16_t* sid,
                      const int32_t* pos, int32_t n, const pp_rope* rope, uint16_t* q_out,
@@ -358,17 +378,35 @@ pp_status kv8_attend(const pp_kv8_layer* L, int32_t doc_len, const uint16_t* q, 
   if ((int64_t)rows * Hq > INT32_MAX - 256) return PP_ERR_UNSUPPORTED;
   const int sms = sm_count();
   if (sms < 1) return PP_ERR_CUDA;
+  const SplitPlan plan = kv8_plan(rows, Hq, L->H, doc_len, opt);
+  const bool doc_pass = plan.C > 0;
+  const WsLayout w = kv8_ws_layout(plan, L->d);
+  if (w.total > 0 && (!ws || !aligned(ws, kAlign))) return PP_ERR_INVALID_ARG;
+  if (ws_bytes < w.total) return PP_ERR_CAPACITY;
+  const Partials part = carve(ws, w);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  (void)ws; (void)ws_bytes;
-  return from_cuda(pp::launch_kv8_attn(*L, doc_len, q, q_ld, Hq, q_sid, q_pos, rows, decode, scale,
-                                       SplitPlan{}, false, Partials{}, o, lse, sms, st));
+  cudaEvent_t* ev = (opt && opt->events) ? reinterpret_cast<cudaEvent_t*>(opt->events) : nullptr;
+  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+  if (ev && cudaStreamIsCapturing(st, &cap) != cudaSuccess) return PP_ERR_CUDA;
+  auto mark = [&](int i) { return ev ? record_mark(ev[i], cap, st) : cudaSuccess; };
+  if (mark(0) != cudaSuccess) return PP_ERR_CUDA;
+  if (doc_pass && (s = from_cuda(pp::launch_kv8_doc(*L, doc_len, q, q_ld, Hq, rows, scale, plan,
+                                                    part, wait_limit(opt),
+                                                    opt ? opt->debug_inject_timeout : 0, st))) !=
+                      PP_OK)
+    return s;
+  if (mark(1) != cudaSuccess) return PP_ERR_CUDA;
+  if ((s = from_cuda(pp::launch_kv8_attn(*L, doc_len, q, q_ld, Hq, q_sid, q_pos, rows, decode,
+                                         scale, plan, doc_pass, part, o, lse, sms, st))) != PP_OK)
+    return s;
+  return from_cuda(mark(2));
 }
 
 size_t kv8_workspace(int32_t rows, int32_t Hq, int32_t H, int32_t d, int32_t doc_len,
                      const pp_options* opt) {
-  (void)opt;
   if (rows < 0 || H < 1 || Hq < 1 || Hq % H != 0 || (d != 64 && d != 128) || doc_len < 0) return 0;
-  return 0;
+  if ((int64_t)rows * Hq > INT32_MAX - 256) return 0;
+  return kv8_ws_layout(kv8_plan(rows, Hq, H, doc_len, opt), d).total;
 }
 
 // Host copy of a plan for the split-plan test aids.

@@ -131,6 +131,11 @@ __device__ __forceinline__ float2 ex2_poly2(float2 x) {
   return r;
 }
 
+// Softmax exponentials: pairs p with p % 5 in {1, 3} go to the FMA-pipe
+// polynomial, the rest to MUFU, balancing the two pipes (MUFU issues a warp's
+// 32 lanes in 8 cycles; the polynomial costs about 5 issue slots a value).
+__host__ __device__ constexpr bool use_poly(int pair) { return pair % 5 == 1 || pair % 5 == 3; }
+
 // ---------------------------------------------------------------------------
 // Split plan of the document pass.  Work is the linear range of
 // units * T tiles, unit u = head * groups + group (head-major, so CTAs that
@@ -291,6 +296,40 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
       set_status(status, PP_DEV_TIMEOUT);
       return false;
     }
+  }
+}
+
+// Warp-uniform bounded wait (every lane polls; lane 0 decides to give up).
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                          long long limit, int32_t* status) {
+  const int lane = threadIdx.x & 31;
+  {
+    // fast path: a phase that has already completed costs one non-blocking
+    // test, no clock read and no suspension
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    if (__all_sync(0xffffffffu, done != 0)) return true;
+  }
+  const long long t0 = clock64();
+  while (true) {
+    const bool ok = mbar_try_wait_sleep(bar, parity, 20000);
+    if (__all_sync(0xffffffffu, ok)) return true;
+    int stop = 0;
+    if (lane == 0) {
+      if (*abort_flag) {
+        stop = 1;
+      } else if (clock64() - t0 > limit) {
+        *abort_flag = 1;
+        set_status(status, PP_DEV_TIMEOUT);
+        stop = 1;
+      }
+    }
+    if (__shfl_sync(0xffffffffu, stop, 0)) return false;
   }
 }
 
@@ -466,6 +505,11 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t start, uint32_t lbo
 __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, int b_mn_major) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)b_mn_major << 16) |
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+// The same with f16 A/B (format 0).
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, int b_mn_major) {
+  return (1u << 4) | ((uint32_t)b_mn_major << 16) | ((uint32_t)(N >> 3) << 17) |
+         ((uint32_t)(M >> 4) << 24);
 }
 
 }  // namespace pp

@@ -89,6 +89,10 @@ cudaError_t launch_kv8_append(const pp_kv8_layer& L, const uint16_t* k, int64_t 
                               int Hq, const int16_t* sid, const int32_t* pos, int n,
                               const pp_rope* rope, uint16_t* q_out, int64_t qo_ld, int num_sms,
                               cudaStream_t st);
+cudaError_t launch_kv8_doc(const pp_kv8_layer& L, int doc_len, const uint16_t* q, int64_t q_ld,
+                           int Hq, int rows, float scale, const SplitPlan& plan,
+                           const Partials& part, long long wait_limit, int inject_timeout,
+                           cudaStream_t st);
 cudaError_t launch_kv8_attn(const pp_kv8_layer& L, int doc_len, const uint16_t* q, int64_t q_ld,
                             int Hq, const int16_t* q_sid, const int32_t* q_pos, int rows,
                             bool one_row_per_stream, float scale, const SplitPlan& plan,

@@ -436,10 +436,16 @@ __global__ void __launch_bounds__(kMaxWays * 32) kv8_attn(const Attn8Params p) {
         const int d0 = plan_cta_of(p.plan, ub);
         const int d1 = plan_cta_of(p.plan, ub + p.plan.T - 1);
         const int64_t sl0 = (int64_t)u * p.plan.max_chunks * kGroupRows + dr % kGroupRows;
+        // a row group of one M tile has two partials a chunk, 128 rows apart
+        const bool two = (int64_t)p.rows * p.g - dr / kGroupRows * kGroupRows <= 128;
         for (int d = d0; d <= d1; ++d) {
           const int64_t sl = sl0 + (int64_t)(d - d0) * kGroupRows;
           const float2 ml = *reinterpret_cast<const float2*>(p.doc_ml + sl * 2);
           fold_in(ml.x, ml.y, p.doc_o + sl * D);
+          if (two) {
+            const float2 m2 = *reinterpret_cast<const float2*>(p.doc_ml + (sl + 128) * 2);
+            fold_in(m2.x, m2.y, p.doc_o + (sl + 128) * D);
+          }
         }
       }
     }

@@ -1,0 +1,621 @@
+// Document pass over the 8-bit paged cache on the 5th-generation tensor cores.
+//
+// For each key head all (query row, query head) pairs that share it are
+// stacked into one matrix Q; per tile of 128 document keys
+//     S = Q X^T                   X the stored keys, S fp32 in TMEM
+//     w = S a + log2 vs           a = query scale * page's key scale, log2 domain
+//     P = 2^(w - M) as f16,  l += P / vs,  O += P Y     Y the stored values
+// with M the running maximum (raised only when it would grow by 2^8), so a
+// page's value scale vs rides in the exponent and no value is multiplied.
+// Both products are f16 tcgen05 MMAs: e4m3 -> f16 is exact, queries are scaled
+// into f16's range by a power of two a row (bf16's 8 bits fit f16's 11), and P
+// keeps 2^-11 of its value.  (Products of e4m3 operands would need queries and
+// probabilities as pairs of e4m3 numbers for 2^-8: the same tensor time as
+// f16, and five more instructions for two probabilities in the softmax, which
+// is the tighter resource.)
+//
+// One CTA holds two "streams": two M tiles of 128 rows over the same keys, or,
+// when a row group has at most 128 rows, one M tile with even tiles on one
+// stream and odd tiles on the other (two partial results).  While one stream's
+// softmax runs, the tensor core works for the other; a converted tile serves
+// both M tiles.  Warp roles (512 threads):
+//   warp 0       loader: bulk copies of page chunks to shared memory, page
+//                tables and scales
+//   warp 1       MMA issuer          warp 2   TMEM allocator
+//   warps 4-7    e4m3 -> f16 into the MMA's 128-byte-swizzled layout
+//   warps 8-15   softmax, one thread a row; queries to f16; partial results
+// TMEM: O_0 | O_1 | S_0 | S_1, P over the first 64 columns of its S.
+//
+// Every wait is bounded: on expiry the kernel sets PP_DEV_TIMEOUT, raises a
+// CTA-wide abort flag, drains its own copies and MMAs (bounded), frees TMEM
+// and returns.
+#include <atomic>
+
+#include "kv8.cuh"
+#include "internal.h"
+
+namespace pp {
+namespace {
+
+// Register split: launched with 128 a thread (512 * 128 = 65536); the control
+// warps drop to 56, the converters to 96, the softmax warps rise to 176.
+constexpr int kThreads8 = 512;
+constexpr int kRegs8 = 128, kRegsCtl = 56, kRegsConv = 96, kRegsSoft = 176;
+static_assert(128 * kRegsCtl + 128 * kRegsConv + 256 * kRegsSoft <= kThreads8 * kRegs8,
+              "register split");
+constexpr int kInfo = 8;   // tiles of page scales kept; the loader runs at most 5 ahead
+
+struct Doc8Params {
+  pp_kv8_layer L;
+  const uint16_t* q;
+  int64_t q_ld;
+  int g;        // query heads per key head
+  int rows;     // (query row, query head) pairs of a key head
+  int doc_len;
+  SplitPlan plan;
+  float sl2;
+  float* doc_o;
+  float* doc_ml;
+  long long wait_limit;
+  int inject_timeout;
+};
+
+template <int D>
+struct Cfg8 {
+  static constexpr int KH = D / 64;               // 128-byte column halves of an f16 row
+  static constexpr int BOX = 128 * 64 * 2;        // [128 x 64] f16
+  static constexpr int TILE = KH * BOX;           // f16 tile of queries, keys or values
+  static constexpr int RAW = 128 * D;             // e4m3 tile
+  static constexpr int NF = 4;                    // f16 key / value tiles (alternating)
+  static constexpr int NR = D == 128 ? 2 : 4;     // e4m3 key / value tiles (alternating)
+  static constexpr int OFF_F = 2 * TILE;
+  static constexpr int OFF_R = OFF_F + NF * TILE;
+  static constexpr int OFF_INFO = OFF_R + NR * RAW;
+  static constexpr int OFF_BAR = OFF_INFO + kInfo * 8 * 16;
+  // raw_full[NR], raw_empty[NR], f_full[NF], f_empty[NF], q_full[2], s_full[2],
+  // p_full[2], o_done[2], drain
+  static constexpr int NBAR = 2 * NR + 2 * NF + 9;
+  static constexpr int USED = OFF_BAR + NBAR * 8;
+  // +1 KB for 1024-byte alignment; at least 120 KB so one CTA owns an SM's TMEM
+  static constexpr int SMEM = (USED + 1024) > 120 * 1024 ? (USED + 1024) : 120 * 1024;
+  static_assert(SMEM + 64 <= 227 * 1024, "shared memory above the per-CTA limit");
+  static constexpr uint32_t T_S = 2 * D, TMEM_COLS = 512;
+  static_assert(T_S + 2 * kBN <= TMEM_COLS, "TMEM budget");
+};
+
+// A run of tiles of one (key head, row group).
+struct Seg8 {
+  int u, h, gi, j0, n, chunk;
+  bool two;     // two M tiles; else one, its tiles dealt out to the streams
+};
+__device__ __forceinline__ bool next_seg8(const Doc8Params& p, int64_t& t, int64_t t_end, int cta,
+                                          Seg8& s) {
+  if (t >= t_end) return false;
+  int j;
+  plan_locate(p.plan, t, s.u, j);
+  s.h = s.u / p.plan.G;
+  s.gi = s.u - s.h * p.plan.G;
+  const int64_t ub = plan_unit_begin(p.plan, s.u);
+  const int64_t ue = ub + p.plan.T;
+  s.j0 = j;
+  s.n = (int)((ue < t_end ? ue : t_end) - t);
+  s.chunk = cta - plan_cta_of(p.plan, ub);
+  s.two = p.rows - s.gi * kGroupRows > 128;
+  t += s.n;
+  return true;
+}
+
+// max of three, NaN if any is NaN
+__device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// One row of queries to f16 in the swizzled tile; returns the power of two the
+// stored row stands for.  A NaN or infinity becomes NaN.
+template <int D>
+__device__ __forceinline__ float load_query_row(uint8_t* tile, const uint16_t* src, int r) {
+  uint4 w[D / 8];
+  float am = 0.f;
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i) {
+    w[i] = src ? *reinterpret_cast<const uint4*>(src + 8 * i) : make_uint4(0, 0, 0, 0);
+    const uint32_t a[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 f = bf2_to_f2(a[j]);
+      am = fmaxf(am, fabsf(f.x) < INFINITY ? fabsf(f.x) : 0.f);
+      am = fmaxf(am, fabsf(f.y) < INFINITY ? fabsf(f.y) : 0.f);
+    }
+  }
+  // 2^e with am / 2^e in [2^13, 2^14): bf16's 8 bits are exact in f16 down to
+  // 2^-30 of the row's largest value
+  int e = (int)(__float_as_uint(am) >> 23) - 127 - 13;
+  e = e < -100 ? -100 : e;
+  const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i) {
+    const uint32_t a[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+    uint32_t b[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 f = bf2_to_f2(a[j]);   // f - f is 0, or NaN where f is not finite
+      b[j] = f2_to_h2((f.x + (f.x - f.x)) * inv, (f.y + (f.y - f.y)) * inv);
+    }
+    *reinterpret_cast<uint4*>(tile + (i >> 3) * (128 * 128) + r * 128 + (((i & 7) ^ (r & 7)) << 4)) =
+        make_uint4(b[0], b[1], b[2], b[3]);
+  }
+  return __uint_as_float((uint32_t)(e + 127) << 23);
+}
+
+template <int D>
+__global__ void __maxnreg__(kRegs8) kv8_doc_tc(const Doc8Params p) {
+  using C = Cfg8<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  __shared__ uint32_t tmem_base_sh;
+  __shared__ int abort_sh;
+  volatile int* abort_flag = &abort_sh;
+  uint64_t* bar = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  uint64_t* raw_full = bar;
+  uint64_t* raw_empty = raw_full + C::NR;
+  uint64_t* f_full = raw_empty + C::NR;
+  uint64_t* f_empty = f_full + C::NF;
+  uint64_t* q_full = f_empty + C::NF;
+  uint64_t* s_full = q_full + 2;
+  uint64_t* p_full = s_full + 2;
+  uint64_t* o_done = p_full + 2;
+  uint64_t* drain = o_done + 2;
+  // per tile and 16 keys: key scale, log2 of the value scale, 1 / value scale,
+  // keys that are there
+  float4* info = reinterpret_cast<float4*>(smem + C::OFF_INFO);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int cta = blockIdx.x;
+  const int64_t t_begin = plan_tile_begin(p.plan, cta);
+  const int64_t t_end = plan_tile_begin(p.plan, cta + 1);
+  int32_t* status = p.L.status;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::NR; ++i) {
+      mbar_init(raw_full + i, 1);
+      mbar_init(raw_empty + i, 128);
+    }
+    for (int i = 0; i < C::NF; ++i) {
+      mbar_init(f_full + i, 128);
+      mbar_init(f_empty + i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(q_full + i, 128);
+      mbar_init(s_full + i, 1);
+      mbar_init(p_full + i, 128);
+      mbar_init(o_done + i, 1);
+    }
+    mbar_init(drain, 1);
+    abort_sh = 0;
+    fence_mbar_init();
+  }
+  if (warp == 2) {
+    tmem_alloc(&tmem_base_sh, C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base_sh;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ loader ----
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCtl));
+    const int page = p.L.page, ppt = kBN / page;   // pages per tile: one a lane
+    const int groups = page >> 4;
+    int64_t t = t_begin;
+    Seg8 s;
+    int ht = 0, kt = 0;
+    bool ok = true;
+    auto fetch = [&](int h, int j, int& pg, float& ks, float& vs) {
+      pg = -1;
+      ks = vs = 1.f;
+      const int i = j * ppt + lane;
+      if (lane < ppt && (int64_t)i * page < p.doc_len) {
+        pg = page_of(p.L.doc_table[i], p.L.n_pages);
+        if (pg >= 0) {
+          ks = p.L.k_scale[(int64_t)pg * p.L.H + h];
+          vs = p.L.v_scale[(int64_t)pg * p.L.H + h];
+        } else {
+          set_status(status, PP_DEV_BAD_PAGE);
+        }
+      }
+    };
+    while (ok && next_seg8(p, t, t_end, cta, s)) {
+      int pg, pg2 = -1;
+      float ks, vs, ks2 = 1.f, vs2 = 1.f;
+      fetch(s.h, s.j0, pg, ks, vs);
+      for (int j = s.j0; ok && j < s.j0 + s.n; ++j, ++kt) {
+        if (j + 1 < s.j0 + s.n) fetch(s.h, j + 1, pg2, ks2, vs2);   // a tile ahead
+        const int left = p.doc_len - (j * ppt + lane) * page;
+        const int n = pg >= 0 ? (left < page ? left : page) : 0;   // keys of this lane's page
+        const uint32_t bytes = (uint32_t)n * D;
+        uint32_t total = bytes;
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+        total = __shfl_sync(0xffffffffu, total, 0);   // lanes 0..7 hold all pages of a tile
+        const int64_t at = ((int64_t)(pg < 0 ? 0 : pg) * p.L.H + s.h) * page * D;
+        for (int kv = 0; kv < 2; ++kv, ++ht) {
+          const int sl = ht % C::NR, f = ht / C::NR;
+          if (f > 0 &&
+              !(ok = warp_wait(raw_empty + sl, (f - 1) & 1, abort_flag, p.wait_limit, status)))
+            break;
+          if (kv == 0 && lane < ppt) {
+            for (int gq = 0; gq < groups; ++gq) {
+              int c = n - gq * 16;
+              c = c < 0 ? 0 : c > 16 ? 16 : c;
+              info[(kt % kInfo) * 8 + lane * groups + gq] =
+                  c > 0 ? make_float4(ks, (float)((int)(__float_as_uint(vs) >> 23) - 127), 1.f / vs,
+                                      __int_as_float(c))
+                        : make_float4(1.f, -INFINITY, 0.f, __int_as_float(0));
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive_expect_tx(raw_full + sl, total);
+          __syncwarp();
+          if (bytes && !(p.inject_timeout && ht == 0))   // test hook: this copy never lands
+            bulk_load(smem + C::OFF_R + sl * C::RAW + lane * page * D, (kv ? p.L.v : p.L.k) + at,
+                      bytes, raw_full + sl);
+        }
+        pg = pg2;
+        ks = ks2;
+        vs = vs2;
+      }
+    }
+    if (!ok && lane == 0) {
+      // Drain: wait (bounded, abort flag ignored) for the copies still in flight.
+      for (int back = 1; back <= C::NR && ht - back >= 0; ++back) {
+        const int k2 = ht - back;
+        if (p.inject_timeout && k2 == 0) continue;
+        volatile int never = 0;
+        mbar_wait(raw_full + k2 % C::NR, (k2 / C::NR) & 1, &never, p.wait_limit, nullptr);
+      }
+    }
+  } else if (warp == 1) {
+    // -------------------------------------------------------- MMA issuer ----
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCtl));
+    constexpr uint32_t IDESC_QK = idesc_f16_f32(128, kBN, 0);
+    constexpr uint32_t IDESC_PV = idesc_f16_f32(128, D, 1);
+    const uint64_t dQ = smem_desc_sw128(smem_u32(smem), 16, 1024);
+    const uint64_t dK = smem_desc_sw128(smem_u32(smem + C::OFF_F), 16, 1024);
+    const uint64_t dV = smem_desc_sw128(smem_u32(smem + C::OFF_F), C::BOX, 1024);
+    auto issue_qk = [&](int st, int slot) {
+      const uint32_t d_t = tmem + C::T_S + (uint32_t)(st * kBN);
+      const uint64_t a0 = dQ + (uint64_t)((st * C::TILE) >> 4);
+      const uint64_t b0 = dK + (uint64_t)((slot * C::TILE) >> 4);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint64_t off = (uint64_t)(((kk >> 2) * C::BOX + (kk & 3) * 32) >> 4);
+        if (elect_one()) mma_ss(d_t, a0 + off, b0 + off, IDESC_QK, kk > 0 ? 1u : 0u);
+      }
+    };
+    auto issue_pv = [&](int st, int slot, bool acc) {
+      const uint32_t d_t = tmem + (uint32_t)(st * D);
+      const uint32_t a_t = tmem + C::T_S + (uint32_t)(st * kBN);
+      const uint64_t b0 = dV + (uint64_t)((slot * C::TILE) >> 4);
+#pragma unroll
+      for (int kk = 0; kk < kBN / 16; ++kk)
+        if (elect_one())
+          mma_ts(d_t, a_t + kk * 8, b0 + (uint64_t)((kk * 16 * 128) >> 4), IDESC_PV,
+                 (acc || kk > 0) ? 1u : 0u);
+    };
+    auto commit = [&](uint64_t* b) {
+      if (elect_one()) tc_commit(b);
+      __syncwarp();
+    };
+    auto wait_f = [&](int half) {
+      return warp_wait(f_full + half % C::NF, (half / C::NF) & 1, abort_flag, p.wait_limit, status);
+    };
+    int64_t t = t_begin;
+    Seg8 s;
+    int t0 = 0, nseg = 0;
+    uint32_t pf_ph = 0;
+    bool ok = true;
+    while (ok && next_seg8(p, t, t_end, cta, s)) {
+      const int step = s.two ? 1 : 2;
+      for (int st = 0; ok && st < 2; ++st) {
+        if (!(ok = warp_wait(q_full + st, nseg & 1, abort_flag, p.wait_limit, status))) break;
+        const int tile = s.two ? 0 : st;
+        if (tile >= s.n) continue;
+        const int half = 2 * (t0 + tile);
+        if (!(ok = wait_f(half))) break;
+        tc_fence_after();
+        issue_qk(st, half % C::NF);
+        commit(s_full + st);
+        if (!s.two || st == 1) commit(f_empty + half % C::NF);
+      }
+      const int steps = s.two ? 2 * s.n : s.n;
+      for (int i = 0; ok && i < steps; ++i) {
+        const int st = i & 1, tile = s.two ? i >> 1 : i;
+        const int hv = 2 * (t0 + tile) + 1;
+        if (!(ok = wait_f(hv))) break;
+        if (!(ok = warp_wait(p_full + st, (pf_ph >> st) & 1, abort_flag, p.wait_limit, status))) break;
+        pf_ph ^= 1u << st;
+        tc_fence_after();
+        issue_pv(st, hv % C::NF, tile >= step);
+        if (!s.two || st == 1) commit(f_empty + hv % C::NF);
+        if (tile + step < s.n) {
+          // S is overwritten behind the product that reads P from it: the MMA
+          // pipe runs in issue order
+          const int hk = 2 * (t0 + tile + step);
+          if (!(ok = wait_f(hk))) break;
+          tc_fence_after();
+          issue_qk(st, hk % C::NF);
+          commit(s_full + st);
+          if (!s.two || st == 1) commit(f_empty + hk % C::NF);
+        } else {
+          commit(o_done + st);
+        }
+      }
+      t0 += s.n;
+      ++nseg;
+    }
+    if (!ok) {
+      commit(drain);
+      if (lane == 0) {
+        volatile int never = 0;
+        mbar_wait(drain, 0, &never, p.wait_limit, nullptr);
+      }
+    }
+  } else if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCtl));
+  } else if (warp < 8) {
+    // --------------------------------------------------------- converter ----
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConv));
+    constexpr int UR = D / 16;              // 16-byte units of a stored row
+    constexpr int IT = 128 * UR / 128;      // units a thread
+    const int tid = threadIdx.x - 128;
+    const int u = tid % UR;
+    // a row's eight (four) units by neighbouring threads; the two 16-byte
+    // halves are written in the order that keeps eight threads in eight banks
+    const int o0 = (D == 128 && u >= 4) ? 1 : 0;
+    int64_t t = t_begin;
+    Seg8 s;
+    int ht = 0, kt = 0;
+    bool ok = true;
+    while (ok && next_seg8(p, t, t_end, cta, s)) {
+      for (int j = 0; ok && j < s.n; ++j, ++kt) {
+        for (int kv = 0; kv < 2; ++kv, ++ht) {
+          const int sr = ht % C::NR, sf = ht % C::NF;
+          if (!(ok = warp_wait(raw_full + sr, (ht / C::NR) & 1, abort_flag, p.wait_limit, status)))
+            break;
+          if (ht >= C::NF && !(ok = warp_wait(f_empty + sf, (ht / C::NF - 1) & 1, abort_flag,
+                                              p.wait_limit, status)))
+            break;
+          const uint8_t* src = smem + C::OFF_R + sr * C::RAW;
+          uint8_t* dst = smem + C::OFF_F + sf * C::TILE + (u / 4) * C::BOX;
+          uint4 w[IT];
+#pragma unroll
+          for (int i = 0; i < IT; ++i) w[i] = *reinterpret_cast<const uint4*>(src + (i * 128 + tid) * 16);
+#pragma unroll
+          for (int i = 0; i < IT; ++i) {
+            const int r = (i * 128 + tid) / UR;
+            const int there = __float_as_int(info[(kt % kInfo) * 8 + (r >> 4)].w);
+            if ((r & 15) >= there) w[i] = make_uint4(0, 0, 0, 0);   // not loaded, or stale
+            uint4 h[2];
+            h[0] = make_uint4(e4m3x2_to_h2(w[i].x), e4m3x2_hi_to_h2(w[i].x), e4m3x2_to_h2(w[i].y),
+                              e4m3x2_hi_to_h2(w[i].y));
+            h[1] = make_uint4(e4m3x2_to_h2(w[i].z), e4m3x2_hi_to_h2(w[i].z), e4m3x2_to_h2(w[i].w),
+                              e4m3x2_hi_to_h2(w[i].w));
+            uint8_t* row = dst + r * 128;
+            const int ua = (u % 4) * 2;
+            const uint4 ha = o0 ? h[1] : h[0], hb = o0 ? h[0] : h[1];
+            *reinterpret_cast<uint4*>(row + (((ua + o0) ^ (r & 7)) << 4)) = ha;
+            *reinterpret_cast<uint4*>(row + (((ua + 1 - o0) ^ (r & 7)) << 4)) = hb;
+          }
+          // behind the stores, which need the loaded values: with the arrival right
+          // behind the loads the next copy was seen to overtake them
+          mbar_arrive(raw_empty + sr);
+          fence_proxy_async();
+          mbar_arrive(f_full + sf);
+        }
+      }
+    }
+  } else {
+    // ----------------------------------------------------------- softmax ----
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
+    const int st = (warp - 8) >> 2;
+    const int wq = warp & 3;                 // TMEM lane quarter of this warp
+    const int rt = wq * 32 + lane;           // row of the M tile
+    const uint32_t t_lane = tmem + ((uint32_t)(wq * 32) << 16);
+    const uint32_t t_S = t_lane + C::T_S + (uint32_t)(st * kBN);
+    const uint32_t t_O = t_lane + (uint32_t)(st * D);
+    int64_t t = t_begin;
+    Seg8 s;
+    uint32_t s_ph = 0, od_ph = 0;
+    int t0 = 0;
+    bool ok = true;
+    while (ok && next_seg8(p, t, t_end, cta, s)) {
+      const int step = s.two ? 1 : 2, first = s.two ? 0 : st;
+      const int row = s.gi * kGroupRows + (s.two ? st * 128 : 0) + rt;
+      const bool valid = row < p.rows;
+      // (the previous run's last S has been seen: no MMA reads this tile of Q any more)
+      const uint16_t* src = nullptr;
+      if (valid) {
+        const int qr = row / p.g;
+        src = p.q + (int64_t)qr * p.q_ld + (int64_t)(s.h * p.g + row - qr * p.g) * D;
+      }
+      const float qs = load_query_row<D>(smem + st * C::TILE, src, rt) * p.sl2;
+      fence_proxy_async();
+      mbar_arrive(q_full + st);
+      float m = -INFINITY, l = 0.f;
+      for (int tile = first; tile < s.n; tile += step) {
+        if (!(ok = warp_wait(s_full + st, s_ph, abort_flag, p.wait_limit, status))) break;
+        s_ph ^= 1;
+        tc_fence_after();
+        uint32_t r[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(t_S + c * 32, r[c]);
+        tmem_ld_wait();
+        const float4* inf = info + ((t0 + tile) % kInfo) * 8;
+        const int kvalid = p.doc_len - (s.j0 + tile) * kBN;
+        if (kvalid < kBN) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (c * 32 + e >= kvalid) r[c][e] = __float_as_uint(-INFINITY);
+        }
+        // row maximum of w, 16 keys of one page at a time
+        float mx = -INFINITY;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const uint32_t* x = &r[q >> 1][(q & 1) * 16];
+          auto f = [&](int i) { return __uint_as_float(x[i]); };
+          float y0 = fmax3_nan(f(0), f(1), f(2)), y1 = fmax3_nan(f(3), f(4), f(5));
+          float y2 = fmax3_nan(f(6), f(7), f(8)), y3 = fmax3_nan(f(9), f(10), f(11));
+          y0 = fmax3_nan(y0, f(12), f(13));
+          y1 = fmax3_nan(y1, f(14), f(15));
+          y0 = fmax3_nan(y0, y1, y2);
+          y0 = fmax3_nan(y0, y3, y3);
+          const float4 in = inf[q];
+          const float z = fmaf(y0, in.x * qs, in.y);
+          mx = fmax3_nan(mx, z, z);
+        }
+        const float m_new = fmaxf(m, mx);      // (a NaN leaves m and spoils l below)
+        // Lazy rescale: keep a stale maximum unless the new one exceeds it by
+        // more than 2^8 (probabilities then stay below 256).
+        const bool need = m_new > m + 8.f;
+        const float m_old = m;
+        if (need) {
+          l *= ex2_mufu(m - m_new);
+          m = m_new;
+        }
+        const float mneg = m == -INFINITY ? 0.f : -m;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float4 in = inf[c * 4 + q];
+            const float a = in.x * qs, b = in.y + mneg;
+            const float2 av = make_float2(a, a), bv = make_float2(b, b);
+            float2 rs[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              const uint32_t* x = &r[c * 2 + (q >> 1)][(q & 1) * 16 + e];
+              const float2 w = ffma2(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), av, bv);
+              float2 pv;
+              if (use_poly(q * 8 + (e >> 1))) {
+                pv = ex2_poly2(w);
+              } else {
+                pv.x = ex2_mufu(w.x);
+                pv.y = ex2_mufu(w.y);
+              }
+              rs[(e >> 1) & 1] = fadd2(rs[(e >> 1) & 1], pv);
+              pk[q * 8 + (e >> 1)] = f2_to_h2(pv.x, pv.y);
+            }
+            const float2 r2 = fadd2(rs[0], rs[1]);
+            l = fmaf(r2.x + r2.y, in.z, l);
+          }
+          tmem_st32(t_S + c * 32, pk);
+        }
+        if (mx != mx) l = mx;
+        // O rescale for rows whose maximum moved (rare).  The product of this
+        // stream's tile before is complete: it was issued ahead of this S.
+        if (tile > first && __any_sync(0xffffffffu, need)) {
+          const float f = need ? ex2_mufu(m_old - m) : 1.f;
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(t_O + c * 32, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st32(t_O + c * 32, o);
+          }
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(p_full + st);
+      }
+      if (!ok) break;
+      const int64_t prow = ((int64_t)s.u * p.plan.max_chunks + s.chunk) * kGroupRows + st * 128 + rt;
+      if (first < s.n) {
+        if (!(ok = warp_wait(o_done + st, od_ph, abort_flag, p.wait_limit, status))) break;
+        od_ph ^= 1;
+        tc_fence_after();
+        float4* dst = reinterpret_cast<float4*>(p.doc_o + prow * D);
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld32(t_O + c * 32, o);
+          tmem_ld_wait();
+          if (valid) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              dst[(c * 32 + e) / 4] =
+                  make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]),
+                              __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
+          }
+        }
+        tc_fence_before();
+      }
+      // a NaN row keeps a finite maximum so that the merge does not skip it
+      if (valid)
+        reinterpret_cast<float2*>(p.doc_ml)[prow] = make_float2(l != l && m == -INFINITY ? 0.f : m, l);
+      t0 += s.n;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+template <int D>
+cudaError_t launch(const Doc8Params& p, cudaStream_t st) {
+  using C = Cfg8<D>;
+  // Once per device: allow the dynamic shared memory, and check that the
+  // kernel was built with the register count the split assumes (with fewer the
+  // softmax warps' increase would wait forever).
+  static std::atomic<uint64_t> ready{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(ready.load() & bit)) {
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, kv8_doc_tc<D>);
+    if (e != cudaSuccess) return e;
+    if (fa.numRegs != kRegs8) return cudaErrorInvalidConfiguration;
+    e = cudaFuncSetAttribute(kv8_doc_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(bit);
+  }
+  kv8_doc_tc<D><<<p.plan.C, kThreads8, C::SMEM, st>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_kv8_doc(const pp_kv8_layer& L, int doc_len, const uint16_t* q, int64_t q_ld,
+                           int Hq, int rows, float scale, const SplitPlan& plan,
+                           const Partials& part, long long wait_limit, int inject_timeout,
+                           cudaStream_t st) {
+  Doc8Params p{};
+  p.L = L;
+  p.q = q; p.q_ld = q_ld;
+  p.g = Hq / L.H;
+  p.rows = rows * p.g;
+  p.doc_len = doc_len;
+  p.plan = plan;
+  p.sl2 = scale * kLog2e;
+  p.doc_o = part.doc_o; p.doc_ml = part.doc_ml;
+  p.wait_limit = wait_limit;
+  p.inject_timeout = inject_timeout;
+  return L.d == 128 ? launch<128>(p, st) : launch<64>(p, st);
+}
+
+}  // namespace pp

@@ -329,3 +329,32 @@ def test_serving_run():
         act = [i for i in range(P) if (i + t) % 5]
         step([i + 1 for i in act], [N + have[i] for i in act], m.kv8_decode_attn)
     assert m.kv8_device_status(layer) == 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_injected_timeout_reports_status_and_recovers(d):
+    """A copy of the document pass that never lands: its waits run out, the call
+    ends, the status says so, and the next call is right."""
+    m = pp()
+    N, P = 3000, 150
+    layer, doc, segs = make_cache(2, d, 16, N, [9] * P, seed=13)
+    sid, pos = list(range(1, P + 1)), [N + 8] * P
+    q = queries(P, 2, d, 1)
+    s, p = ids(sid, pos)
+    opt = m.Options(debug_inject_timeout=1, wait_limit_log2=22)
+    m.kv8_decode_attn(layer, N, q, s, p, 0.1, opt=opt)
+    torch.cuda.synchronize()
+    assert m.kv8_device_status(layer) & m.PP_DEV_TIMEOUT
+    m.kv8_reset(layer)
+    run(layer, doc, segs, N, sid, pos, 1, "decode")
+    assert m.kv8_device_status(layer) == 0
+
+
+@pytest.mark.parametrize("splits", [1, 2, 5, 40, 1000])
+def test_any_split_of_the_document_gives_the_same(splits):
+    m = pp()
+    N, P = 2100, 90
+    layer, doc, segs = make_cache(2, 128, 64, N, [9] * P, seed=14)
+    sid, pos = list(range(1, P + 1)), [N + 8] * P
+    run(layer, doc, segs, N, sid, pos, 1, "decode", opt=m.Options(splits=splits))
+    run(layer, doc, segs, N, sid, pos, 5, "decode", opt=m.Options(splits=splits))
