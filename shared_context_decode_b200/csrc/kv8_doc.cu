@@ -18,13 +18,17 @@
 // when a row group has at most 128 rows, one M tile with even tiles on one
 // stream and odd tiles on the other (two partial results).  While one stream's
 // softmax runs, the tensor core works for the other; a converted tile serves
-// both M tiles.  Warp roles (512 threads):
+// both M tiles.  Warp roles (768 threads):
 //   warp 0       loader: bulk copies of page chunks to shared memory, page
 //                tables and scales
 //   warp 1       MMA issuer          warp 2   TMEM allocator
 //   warps 4-7    e4m3 -> f16 into the MMA's 128-byte-swizzled layout
-//   warps 8-15   softmax, one thread a row; queries to f16; partial results
-// TMEM: O_0 | O_1 | S_0 | S_1, P over the first 64 columns of its S.
+//   warps 8-23   softmax, eight a stream: a thread takes 64 of a row's 128 keys and
+//                shares its maximum with the one that has the others; queries to
+//                f16; partial results
+// TMEM: O_0 | O_1 | S_0 | S_1, P over the first 32 columns of each half of its S.
+// Bound: the latency of the softmax warps' instruction stream, not a pipe; with
+// one thread a row (eight warps, 128 keys) a tile took 4750 cycles.
 //
 // Every wait is bounded: on expiry the kernel sets PP_DEV_TIMEOUT, raises a
 // CTA-wide abort flag, drains its own copies and MMAs (bounded), frees TMEM
@@ -37,13 +41,19 @@
 namespace pp {
 namespace {
 
-// Register split: launched with 128 a thread (512 * 128 = 65536); the control
-// warps drop to 56, the converters to 96, the softmax warps rise to 176.
-constexpr int kThreads8 = 512;
-constexpr int kRegs8 = 128, kRegsCtl = 56, kRegsConv = 96, kRegsSoft = 176;
-static_assert(128 * kRegsCtl + 128 * kRegsConv + 256 * kRegsSoft <= kThreads8 * kRegs8,
+// Register split: launched with 80 a thread (768 * 80 = 61440); the control
+// warps drop to 56, the converters to 72, the softmax warps rise to 88.
+constexpr int kThreads8 = 768;
+constexpr int kRegs8 = 80, kRegsCtl = 56, kRegsConv = 72, kRegsSoft = 88;
+static_assert(128 * kRegsCtl + 128 * kRegsConv + 512 * kRegsSoft <= kThreads8 * kRegs8,
               "register split");
-constexpr int kInfo = 8;   // tiles of page scales kept; the loader runs at most 5 ahead
+#ifndef POLY
+#define POLY(i) use_poly(i)
+#endif
+// Tiles of page scales kept (the loader runs at most 6 ahead of the softmax):
+// for every 16 keys the key scale and the value scale's logarithm, -inf where
+// there are no keys; [8]: whether any of the tile's keys are not there.
+constexpr int kInfo = 8, kInfoLd = 9;
 
 struct Doc8Params {
   pp_kv8_layer L;
@@ -71,14 +81,15 @@ struct Cfg8 {
   static constexpr int OFF_F = 2 * TILE;
   static constexpr int OFF_R = OFF_F + NF * TILE;
   static constexpr int OFF_INFO = OFF_R + NR * RAW;
-  static constexpr int OFF_BAR = OFF_INFO + kInfo * 8 * 16;
+  static constexpr int OFF_SHARE = OFF_INFO + kInfo * kInfoLd * 8;
+  static constexpr int OFF_BAR = OFF_SHARE + 2 * 2 * 128 * 4;
   // raw_full[NR], raw_empty[NR], f_full[NF], f_empty[NF], q_full[2], s_full[2],
-  // p_full[2], o_done[2], drain
-  static constexpr int NBAR = 2 * NR + 2 * NF + 9;
-  static constexpr int USED = OFF_BAR + NBAR * 8;
-  // +1 KB for 1024-byte alignment; at least 120 KB so one CTA owns an SM's TMEM
-  static constexpr int SMEM = (USED + 1024) > 120 * 1024 ? (USED + 1024) : 120 * 1024;
-  static_assert(SMEM + 64 <= 227 * 1024, "shared memory above the per-CTA limit");
+  // p_full[2], o_done[2], pair[8], drain
+  static constexpr int NBAR = 2 * NR + 2 * NF + 17;
+  static constexpr int USED = OFF_BAR + NBAR * 8 + 8;   // TMEM base and abort flag last
+  // at least 120 KB so one CTA owns an SM's TMEM
+  static constexpr int SMEM = USED > 120 * 1024 ? USED : 120 * 1024;
+  static_assert(SMEM <= 227 * 1024, "shared memory above the per-CTA limit");
   static constexpr uint32_t T_S = 2 * D, TMEM_COLS = 512;
   static_assert(T_S + 2 * kBN <= TMEM_COLS, "TMEM budget");
 };
@@ -105,6 +116,14 @@ __device__ __forceinline__ bool next_seg8(const Doc8Params& p, int64_t& t, int64
   return true;
 }
 
+// One arrival for a warp whose lanes have all done what the barrier stands for.
+// (An arrival by every lane is an atomic on one address 32 times over: with
+// those, barriers alone took 1.7 us of a tile's 3.6.)
+__device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
+
 // max of three, NaN if any is NaN
 __device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
   float d;
@@ -112,16 +131,40 @@ __device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
   return d;
 }
 
-// One row of queries to f16 in the swizzled tile; returns the power of two the
-// stored row stands for.  A NaN or infinity becomes NaN.
+// 16-byte unit c of row r in a tile of 128-byte-swizzled rows of 64 f16.
+__device__ __forceinline__ uint4* unit_at(uint8_t* tile, int r, int c) {
+  return reinterpret_cast<uint4*>(tile + (c >> 3) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
+
+// Sixteen rows of queries (from pair `row0` on) to f16 in rows r0 .. r0 + 15 of
+// the swizzled tile; scale[r]: the power of two row r stands for, times sl2.  The
+// rows come in coalesced through their own place in the tile, then two lanes
+// take a row.  A NaN or infinity becomes NaN.
 template <int D>
-__device__ __forceinline__ float load_query_row(uint8_t* tile, const uint16_t* src, int r) {
-  uint4 w[D / 8];
-  float am = 0.f;
+__device__ __forceinline__ void load_queries(const Doc8Params& p, uint8_t* tile, float* scale,
+                                             int r0, int row0, int h, int lane) {
+  constexpr int U = D / 8, RP = 32 / U, B = 16 / RP;   // units a row, rows a pass, passes
+  const uint16_t* head = p.q + (int64_t)h * p.g * D + (lane % U) * 8;
+  uint4 w[B];
 #pragma unroll
-  for (int i = 0; i < D / 8; ++i) {
-    w[i] = src ? *reinterpret_cast<const uint4*>(src + 8 * i) : make_uint4(0, 0, 0, 0);
-    const uint32_t a[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+  for (int i = 0; i < B; ++i) {
+    const int row = row0 + i * RP + lane / U;
+    w[i] = make_uint4(0, 0, 0, 0);
+    if (row < p.rows) {
+      const int qr = p.g == 1 ? row : row / p.g;
+      w[i] = __ldg(reinterpret_cast<const uint4*>(head + (int64_t)qr * p.q_ld +
+                                                  (int64_t)(row - qr * p.g) * D));
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < B; ++i) *unit_at(tile, r0 + i * RP + lane / U, lane % U) = w[i];
+  __syncwarp();
+  const int r = r0 + (lane & 15), c0 = (lane >> 4) * (U / 2);
+  float am = 0.f;
+#pragma unroll 2
+  for (int i = 0; i < U / 2; ++i) {
+    const uint4 x = *unit_at(tile, r, c0 + i);
+    const uint32_t a[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const float2 f = bf2_to_f2(a[j]);
@@ -129,35 +172,37 @@ __device__ __forceinline__ float load_query_row(uint8_t* tile, const uint16_t* s
       am = fmaxf(am, fabsf(f.y) < INFINITY ? fabsf(f.y) : 0.f);
     }
   }
+  am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 16));
   // 2^e with am / 2^e in [2^13, 2^14): bf16's 8 bits are exact in f16 down to
   // 2^-30 of the row's largest value
   int e = (int)(__float_as_uint(am) >> 23) - 127 - 13;
   e = e < -100 ? -100 : e;
   const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
-#pragma unroll
-  for (int i = 0; i < D / 8; ++i) {
-    const uint32_t a[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll 2
+  for (int i = 0; i < U / 2; ++i) {
+    const uint4 x = *unit_at(tile, r, c0 + i);
+    const uint32_t a[4] = {x.x, x.y, x.z, x.w};
     uint32_t b[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const float2 f = bf2_to_f2(a[j]);   // f - f is 0, or NaN where f is not finite
       b[j] = f2_to_h2((f.x + (f.x - f.x)) * inv, (f.y + (f.y - f.y)) * inv);
     }
-    *reinterpret_cast<uint4*>(tile + (i >> 3) * (128 * 128) + r * 128 + (((i & 7) ^ (r & 7)) << 4)) =
-        make_uint4(b[0], b[1], b[2], b[3]);
+    *unit_at(tile, r, c0 + i) = make_uint4(b[0], b[1], b[2], b[3]);
   }
-  return __uint_as_float((uint32_t)(e + 127) << 23);
+  if (lane < 16) scale[r] = __uint_as_float((uint32_t)(e + 127) << 23) * p.sl2;
 }
 
 template <int D>
 __global__ void __maxnreg__(kRegs8) kv8_doc_tc(const Doc8Params p) {
   using C = Cfg8<D>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~uintptr_t(1023));
-  __shared__ uint32_t tmem_base_sh;
-  __shared__ int abort_sh;
-  volatile int* abort_flag = &abort_sh;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  volatile int* abort_flag = reinterpret_cast<int*>(smem + C::OFF_BAR + C::NBAR * 8 + 4);
+  uint32_t* tmem_base = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + C::NBAR * 8);
+  if (smem_u32(smem) & 1023) {     // (the swizzled tiles need it; never seen)
+    set_status(p.L.status, PP_DEV_TIMEOUT);
+    return;
+  }
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* raw_full = bar;
   uint64_t* raw_empty = raw_full + C::NR;
@@ -167,10 +212,10 @@ __global__ void __maxnreg__(kRegs8) kv8_doc_tc(const Doc8Params p) {
   uint64_t* s_full = q_full + 2;
   uint64_t* p_full = s_full + 2;
   uint64_t* o_done = p_full + 2;
-  uint64_t* drain = o_done + 2;
-  // per tile and 16 keys: key scale, log2 of the value scale, 1 / value scale,
-  // keys that are there
-  float4* info = reinterpret_cast<float4*>(smem + C::OFF_INFO);
+  uint64_t* pair = o_done + 2;   // two warps that share rows
+  uint64_t* drain = pair + 8;
+  float(*share)[2][128] = reinterpret_cast<float(*)[2][128]>(smem + C::OFF_SHARE);  // [stream][half][row]
+  float2* info = reinterpret_cast<float2*>(smem + C::OFF_INFO);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cta = blockIdx.x;
@@ -181,62 +226,79 @@ __global__ void __maxnreg__(kRegs8) kv8_doc_tc(const Doc8Params p) {
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::NR; ++i) {
       mbar_init(raw_full + i, 1);
-      mbar_init(raw_empty + i, 128);
+      mbar_init(raw_empty + i, 4);
     }
     for (int i = 0; i < C::NF; ++i) {
-      mbar_init(f_full + i, 128);
+      mbar_init(f_full + i, 4);
       mbar_init(f_empty + i, 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(q_full + i, 128);
+      mbar_init(q_full + i, 8);
       mbar_init(s_full + i, 1);
-      mbar_init(p_full + i, 128);
+      mbar_init(p_full + i, 8);
       mbar_init(o_done + i, 1);
     }
+    for (int i = 0; i < 8; ++i) mbar_init(pair + i, 2);
     mbar_init(drain, 1);
-    abort_sh = 0;
+    *abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == 2) {
-    tmem_alloc(&tmem_base_sh, C::TMEM_COLS);
+    tmem_alloc(tmem_base, C::TMEM_COLS);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tmem_base_sh;
+  const uint32_t tmem = *tmem_base;
 
   if (warp == 0) {
     // ------------------------------------------------------------ loader ----
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCtl));
-    const int page = p.L.page, ppt = kBN / page;   // pages per tile: one a lane
+    const int page = p.L.page, ppt = kBN / page;   // pages per tile
     const int groups = page >> 4;
+    const int per = 32 / ppt;                      // tiles per batch of 32 pages, a lane each
     int64_t t = t_begin;
     Seg8 s;
     int ht = 0, kt = 0;
     bool ok = true;
-    auto fetch = [&](int h, int j, int& pg, float& ks, float& vs) {
-      pg = -1;
+    // Table entries are loaded two batches ahead, scales one, so that neither
+    // dependent load stands between two tiles' copies.
+    auto entry = [&](int b) {   // page b * 32 + lane of the document
+      const int64_t i = (int64_t)b * 32 + lane;
+      return i * page < p.doc_len ? p.L.doc_table[i] : -1;
+    };
+    auto scales = [&](int h, int pg, float& ks, float& vs) {
       ks = vs = 1.f;
-      const int i = j * ppt + lane;
-      if (lane < ppt && (int64_t)i * page < p.doc_len) {
-        pg = page_of(p.L.doc_table[i], p.L.n_pages);
-        if (pg >= 0) {
-          ks = p.L.k_scale[(int64_t)pg * p.L.H + h];
-          vs = p.L.v_scale[(int64_t)pg * p.L.H + h];
-        } else {
-          set_status(status, PP_DEV_BAD_PAGE);
-        }
+      if (pg >= 0) {
+        ks = p.L.k_scale[(int64_t)pg * p.L.H + h];
+        vs = p.L.v_scale[(int64_t)pg * p.L.H + h];
       }
     };
     while (ok && next_seg8(p, t, t_end, cta, s)) {
-      int pg, pg2 = -1;
-      float ks, vs, ks2 = 1.f, vs2 = 1.f;
-      fetch(s.h, s.j0, pg, ks, vs);
+      int b = s.j0 / per;
+      int pg0 = page_of(entry(b), p.L.n_pages), e1 = entry(b + 1);
+      float ks0, vs0, ks1, vs1;
+      scales(s.h, pg0, ks0, vs0);
+      int pg1 = page_of(e1, p.L.n_pages);
+      scales(s.h, pg1, ks1, vs1);
+      e1 = entry(b + 2);
       for (int j = s.j0; ok && j < s.j0 + s.n; ++j, ++kt) {
-        if (j + 1 < s.j0 + s.n) fetch(s.h, j + 1, pg2, ks2, vs2);   // a tile ahead
-        const int left = p.doc_len - (j * ppt + lane) * page;
-        const int n = pg >= 0 ? (left < page ? left : page) : 0;   // keys of this lane's page
+        if (j / per != b) {
+          b = j / per;
+          pg0 = pg1; ks0 = ks1; vs0 = vs1;
+          pg1 = page_of(e1, p.L.n_pages);
+          scales(s.h, pg1, ks1, vs1);
+          e1 = entry(b + 2);
+        }
+        const int from = (j % per) * ppt + (lane & 7);    // lanes 0 .. ppt-1 take the tile's pages
+        const int pg = __shfl_sync(0xffffffffu, pg0, from & 31);
+        const float ks = __shfl_sync(0xffffffffu, ks0, from & 31);
+        const float vs = __shfl_sync(0xffffffffu, vs0, from & 31);
+        const int64_t left = lane < ppt ? p.doc_len - ((int64_t)j * ppt + lane) * page : 0;
+        if (left > 0 && pg < 0) set_status(status, PP_DEV_BAD_PAGE);
+        // keys of this lane's page
+        const int n = left > 0 && pg >= 0 ? (int)(left < page ? left : page) : 0;
         const uint32_t bytes = (uint32_t)n * D;
         uint32_t total = bytes;
 #pragma unroll
@@ -250,14 +312,13 @@ __global__ void __maxnreg__(kRegs8) kv8_doc_tc(const Doc8Params p) {
             break;
           if (kv == 0 && lane < ppt) {
             for (int gq = 0; gq < groups; ++gq) {
-              int c = n - gq * 16;
-              c = c < 0 ? 0 : c > 16 ? 16 : c;
-              info[(kt % kInfo) * 8 + lane * groups + gq] =
-                  c > 0 ? make_float4(ks, (float)((int)(__float_as_uint(vs) >> 23) - 127), 1.f / vs,
-                                      __int_as_float(c))
-                        : make_float4(1.f, -INFINITY, 0.f, __int_as_float(0));
+              info[(kt % kInfo) * kInfoLd + lane * groups + gq] =
+                  n > gq * 16 ? make_float2(ks, (float)((int)(__float_as_uint(vs) >> 23) - 127))
+                              : make_float2(1.f, -INFINITY);
             }
           }
+          if (kv == 0 && lane == 0)
+            info[(kt % kInfo) * kInfoLd + 8].x = total < (uint32_t)(kBN * D) ? 1.f : 0.f;
           __syncwarp();
           if (lane == 0) mbar_arrive_expect_tx(raw_full + sl, total);
           __syncwarp();
@@ -265,9 +326,6 @@ __global__ void __maxnreg__(kRegs8) kv8_doc_tc(const Doc8Params p) {
             bulk_load(smem + C::OFF_R + sl * C::RAW + lane * page * D, (kv ? p.L.v : p.L.k) + at,
                       bytes, raw_full + sl);
         }
-        pg = pg2;
-        ks = ks2;
-        vs = vs2;
       }
     }
     if (!ok && lane == 0) {
@@ -284,6 +342,7 @@ __global__ void __maxnreg__(kRegs8) kv8_doc_tc(const Doc8Params p) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCtl));
     constexpr uint32_t IDESC_QK = idesc_f16_f32(128, kBN, 0);
     constexpr uint32_t IDESC_PV = idesc_f16_f32(128, D, 1);
+    const uint32_t on = elect_one() ? 1u : 0u;   // one lane issues, always the same
     const uint64_t dQ = smem_desc_sw128(smem_u32(smem), 16, 1024);
     const uint64_t dK = smem_desc_sw128(smem_u32(smem + C::OFF_F), 16, 1024);
     const uint64_t dV = smem_desc_sw128(smem_u32(smem + C::OFF_F), C::BOX, 1024);
@@ -294,7 +353,7 @@ __global__ void __maxnreg__(kRegs8) kv8_doc_tc(const Doc8Params p) {
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         const uint64_t off = (uint64_t)(((kk >> 2) * C::BOX + (kk & 3) * 32) >> 4);
-        if (elect_one()) mma_ss(d_t, a0 + off, b0 + off, IDESC_QK, kk > 0 ? 1u : 0u);
+        mma_ss_if(on, d_t, a0 + off, b0 + off, IDESC_QK, kk > 0 ? 1u : 0u);
       }
     };
     auto issue_pv = [&](int st, int slot, bool acc) {
@@ -303,14 +362,10 @@ __global__ void __maxnreg__(kRegs8) kv8_doc_tc(const Doc8Params p) {
       const uint64_t b0 = dV + (uint64_t)((slot * C::TILE) >> 4);
 #pragma unroll
       for (int kk = 0; kk < kBN / 16; ++kk)
-        if (elect_one())
-          mma_ts(d_t, a_t + kk * 8, b0 + (uint64_t)((kk * 16 * 128) >> 4), IDESC_PV,
-                 (acc || kk > 0) ? 1u : 0u);
+        mma_ts_if(on, d_t, a_t + (kk & 3) * 8 + (kk >> 2) * (kBN / 2), b0 + (uint64_t)((kk * 16 * 128) >> 4), IDESC_PV,
+                  (acc || kk > 0) ? 1u : 0u);
     };
-    auto commit = [&](uint64_t* b) {
-      if (elect_one()) tc_commit(b);
-      __syncwarp();
-    };
+    auto commit = [&](uint64_t* b) { tc_commit_if(on, b); };
     auto wait_f = [&](int half) {
       return warp_wait(f_full + half % C::NF, (half / C::NF) & 1, abort_flag, p.wait_limit, status);
     };
@@ -370,13 +425,19 @@ __global__ void __maxnreg__(kRegs8) kv8_doc_tc(const Doc8Params p) {
   } else if (warp < 8) {
     // --------------------------------------------------------- converter ----
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConv));
-    constexpr int UR = D / 16;              // 16-byte units of a stored row
-    constexpr int IT = 128 * UR / 128;      // units a thread
+    // A thread takes 16-byte unit u (16 dims) of every RS-th row from r0 on.  The
+    // eight threads that access shared memory together take two rows, with u
+    // dealt out so that their loads and both of their stores meet 32 different
+    // banks.  RS is a multiple of 8: the swizzle is the same for all rows.
+    constexpr int UR = D / 16, RS = 128 / UR, IT = 128 / RS;
     const int tid = threadIdx.x - 128;
-    const int u = tid % UR;
-    // a row's eight (four) units by neighbouring threads; the two 16-byte
-    // halves are written in the order that keeps eight threads in eight banks
-    const int o0 = (D == 128 && u >= 4) ? 1 : 0;
+    const int sub = tid & 7;
+    const int u = D == 128 ? sub : sub & 3;
+    const int r0 = D == 128 ? (tid >> 4) * 2 + ((sub >> 2) ^ ((tid >> 3) & 1)) : tid >> 2;
+    const int src0 = r0 * D + u * 16;
+    const int ua = (u & 3) * 2;
+    const int dst0 = (u >> 2) * C::BOX + r0 * 128 + ((ua ^ (r0 & 7)) << 4);
+    const int dst1 = (u >> 2) * C::BOX + r0 * 128 + (((ua + 1) ^ (r0 & 7)) << 4);
     int64_t t = t_begin;
     Seg8 s;
     int ht = 0, kt = 0;
@@ -390,44 +451,58 @@ __global__ void __maxnreg__(kRegs8) kv8_doc_tc(const Doc8Params p) {
           if (ht >= C::NF && !(ok = warp_wait(f_empty + sf, (ht / C::NF - 1) & 1, abort_flag,
                                               p.wait_limit, status)))
             break;
-          const uint8_t* src = smem + C::OFF_R + sr * C::RAW;
-          uint8_t* dst = smem + C::OFF_F + sf * C::TILE + (u / 4) * C::BOX;
+          const uint8_t* src = smem + C::OFF_R + sr * C::RAW + src0;
+          uint8_t* dst = smem + C::OFF_F + sf * C::TILE;
           uint4 w[IT];
 #pragma unroll
-          for (int i = 0; i < IT; ++i) w[i] = *reinterpret_cast<const uint4*>(src + (i * 128 + tid) * 16);
+          for (int i = 0; i < IT; ++i) w[i] = *reinterpret_cast<const uint4*>(src + i * RS * D);
+          const float2* inf = info + (kt % kInfo) * kInfoLd;
+          if (inf[8].x != 0.f) {      // some keys are not there: zeros for them (rare)
+            const int there = p.doc_len - (s.j0 + j) * kBN;
+#pragma unroll
+            for (int i = 0; i < IT; ++i) {
+              const int r = r0 + i * RS;
+              if (r >= there || inf[r >> 4].y == -INFINITY) w[i] = make_uint4(0, 0, 0, 0);
+            }
+          }
 #pragma unroll
           for (int i = 0; i < IT; ++i) {
-            const int r = (i * 128 + tid) / UR;
-            const int there = __float_as_int(info[(kt % kInfo) * 8 + (r >> 4)].w);
-            if ((r & 15) >= there) w[i] = make_uint4(0, 0, 0, 0);   // not loaded, or stale
-            uint4 h[2];
-            h[0] = make_uint4(e4m3x2_to_h2(w[i].x), e4m3x2_hi_to_h2(w[i].x), e4m3x2_to_h2(w[i].y),
-                              e4m3x2_hi_to_h2(w[i].y));
-            h[1] = make_uint4(e4m3x2_to_h2(w[i].z), e4m3x2_hi_to_h2(w[i].z), e4m3x2_to_h2(w[i].w),
-                              e4m3x2_hi_to_h2(w[i].w));
-            uint8_t* row = dst + r * 128;
-            const int ua = (u % 4) * 2;
-            const uint4 ha = o0 ? h[1] : h[0], hb = o0 ? h[0] : h[1];
-            *reinterpret_cast<uint4*>(row + (((ua + o0) ^ (r & 7)) << 4)) = ha;
-            *reinterpret_cast<uint4*>(row + (((ua + 1 - o0) ^ (r & 7)) << 4)) = hb;
+            *reinterpret_cast<uint4*>(dst + dst0 + i * RS * 128) =
+                make_uint4(e4m3x2_to_h2(w[i].x), e4m3x2_hi_to_h2(w[i].x), e4m3x2_to_h2(w[i].y),
+                           e4m3x2_hi_to_h2(w[i].y));
+            *reinterpret_cast<uint4*>(dst + dst1 + i * RS * 128) =
+                make_uint4(e4m3x2_to_h2(w[i].z), e4m3x2_hi_to_h2(w[i].z), e4m3x2_to_h2(w[i].w),
+                           e4m3x2_hi_to_h2(w[i].w));
           }
           // behind the stores, which need the loaded values: with the arrival right
           // behind the loads the next copy was seen to overtake them
-          mbar_arrive(raw_empty + sr);
           fence_proxy_async();
-          mbar_arrive(f_full + sf);
+          warp_arrive(raw_empty + sr, lane);
+          warp_arrive(f_full + sf, lane);
         }
       }
     }
   } else {
     // ----------------------------------------------------------- softmax ----
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
-    const int st = (warp - 8) >> 2;
+    const int st = (warp - 8) >> 3, half = ((warp - 8) >> 2) & 1;
     const int wq = warp & 3;                 // TMEM lane quarter of this warp
     const int rt = wq * 32 + lane;           // row of the M tile
     const uint32_t t_lane = tmem + ((uint32_t)(wq * 32) << 16);
-    const uint32_t t_S = t_lane + C::T_S + (uint32_t)(st * kBN);
-    const uint32_t t_O = t_lane + (uint32_t)(st * D);
+    const uint32_t t_S = t_lane + C::T_S + (uint32_t)(st * kBN + half * (kBN / 2));
+    const uint32_t t_O = t_lane + (uint32_t)(st * D + half * (D / 2));   // this half's share of O
+    uint8_t* tq = smem + st * C::TILE;
+    uint64_t* pb = pair + st * 4 + wq;
+    uint32_t pr_ph = 0;
+    // x of the thread that has the row's other keys
+    auto swap_half = [&](float x, float& other) -> bool {
+      share[st][half][rt] = x;
+      warp_arrive(pb, lane);
+      const bool got = warp_wait(pb, pr_ph, abort_flag, p.wait_limit, status);
+      pr_ph ^= 1;
+      other = share[st][half ^ 1][rt];
+      return got;
+    };
     int64_t t = t_begin;
     Seg8 s;
     uint32_t s_ph = 0, od_ph = 0;
@@ -436,50 +511,58 @@ __global__ void __maxnreg__(kRegs8) kv8_doc_tc(const Doc8Params p) {
     while (ok && next_seg8(p, t, t_end, cta, s)) {
       const int step = s.two ? 1 : 2, first = s.two ? 0 : st;
       const int row = s.gi * kGroupRows + (s.two ? st * 128 : 0) + rt;
-      const bool valid = row < p.rows;
       // (the previous run's last S has been seen: no MMA reads this tile of Q any more)
-      const uint16_t* src = nullptr;
-      if (valid) {
-        const int qr = row / p.g;
-        src = p.q + (int64_t)qr * p.q_ld + (int64_t)(s.h * p.g + row - qr * p.g) * D;
-      }
-      const float qs = load_query_row<D>(smem + st * C::TILE, src, rt) * p.sl2;
+      load_queries<D>(p, tq, &share[st][0][0], wq * 32 + half * 16, row - lane + half * 16, s.h, lane);
       fence_proxy_async();
-      mbar_arrive(q_full + st);
+      warp_arrive(q_full + st, lane);
+      warp_arrive(pb, lane);
+      if (!(ok = warp_wait(pb, pr_ph, abort_flag, p.wait_limit, status))) break;
+      pr_ph ^= 1;
+      const float qs = share[st][0][rt];
+      // (both have read the scales before one writes over them: a swap's value is
+      // read by the other warp before this one passes its next barrier)
+      warp_arrive(pb, lane);
+      if (!(ok = warp_wait(pb, pr_ph, abort_flag, p.wait_limit, status))) break;
+      pr_ph ^= 1;
       float m = -INFINITY, l = 0.f;
       for (int tile = first; tile < s.n; tile += step) {
         if (!(ok = warp_wait(s_full + st, s_ph, abort_flag, p.wait_limit, status))) break;
         s_ph ^= 1;
+        const float2* inf = info + ((t0 + tile) % kInfo) * kInfoLd + half * 4;
         tc_fence_after();
-        uint32_t r[4][32];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(t_S + c * 32, r[c]);
-        tmem_ld_wait();
-        const float4* inf = info + ((t0 + tile) % kInfo) * 8;
-        const int kvalid = p.doc_len - (s.j0 + tile) * kBN;
-        if (kvalid < kBN) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
+        // Two passes over S in TMEM, 32 columns at a time: the maximum, then the
+        // exponentials.
+        const int kvalid = p.doc_len - (s.j0 + tile) * kBN - half * (kBN / 2);
+        auto load32 = [&](uint32_t (&x)[32], int c) {
+          tmem_ld32(t_S + c * 32, x);
+          tmem_ld_wait();
+          if (kvalid < kBN / 2) {
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              if (c * 32 + e >= kvalid) r[c][e] = __float_as_uint(-INFINITY);
-        }
-        // row maximum of w, 16 keys of one page at a time
+              if (c * 32 + e >= kvalid) x[e] = __float_as_uint(-INFINITY);
+          }
+        };
         float mx = -INFINITY;
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c) {
+          uint32_t x[32];
+          load32(x, c);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const uint32_t* x = &r[q >> 1][(q & 1) * 16];
-          auto f = [&](int i) { return __uint_as_float(x[i]); };
-          float y0 = fmax3_nan(f(0), f(1), f(2)), y1 = fmax3_nan(f(3), f(4), f(5));
-          float y2 = fmax3_nan(f(6), f(7), f(8)), y3 = fmax3_nan(f(9), f(10), f(11));
-          y0 = fmax3_nan(y0, f(12), f(13));
-          y1 = fmax3_nan(y1, f(14), f(15));
-          y0 = fmax3_nan(y0, y1, y2);
-          y0 = fmax3_nan(y0, y3, y3);
-          const float4 in = inf[q];
-          const float z = fmaf(y0, in.x * qs, in.y);
-          mx = fmax3_nan(mx, z, z);
+          for (int q = 0; q < 2; ++q) {
+            const float2 in = inf[c * 2 + q];
+            auto f = [&](int i) { return __uint_as_float(x[q * 16 + i]); };
+            float y0 = fmax3_nan(f(0), f(1), f(2)), y1 = fmax3_nan(f(3), f(4), f(5));
+            float y2 = fmax3_nan(f(6), f(7), f(8)), y3 = fmax3_nan(f(9), f(10), f(11));
+            y0 = fmax3_nan(y0, f(12), f(13));
+            y1 = fmax3_nan(y1, f(14), f(15));
+            y0 = fmax3_nan(y0, y1, y2);
+            const float z = fmaf(fmax3_nan(y0, y3, y3), in.x * qs, in.y);
+            mx = fmax3_nan(mx, z, z);
+          }
         }
+        float mo;
+        if (!(ok = swap_half(mx, mo))) break;
+        mx = fmax3_nan(mx, mo, mo);
         const float m_new = fmaxf(m, mx);      // (a NaN leaves m and spoils l below)
         // Lazy rescale: keep a stale maximum unless the new one exceeds it by
         // more than 2^8 (probabilities then stay below 256).
@@ -490,21 +573,23 @@ __global__ void __maxnreg__(kRegs8) kv8_doc_tc(const Doc8Params p) {
           m = m_new;
         }
         const float mneg = m == -INFINITY ? 0.f : -m;
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < 2; ++c) {
-          uint32_t pk[32];
+          uint32_t x[32], pk[16];
+          load32(x, c);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const float4 in = inf[c * 4 + q];
+          for (int q = 0; q < 2; ++q) {
+            const float2 in = inf[c * 2 + q];
             const float a = in.x * qs, b = in.y + mneg;
+            const float rv = in.y == -INFINITY ? 0.f : ex2_mufu(-in.y);   // 1 / value scale
             const float2 av = make_float2(a, a), bv = make_float2(b, b);
             float2 rs[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
             for (int e = 0; e < 16; e += 2) {
-              const uint32_t* x = &r[c * 2 + (q >> 1)][(q & 1) * 16 + e];
-              const float2 w = ffma2(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), av, bv);
+              const float2 w = ffma2(make_float2(__uint_as_float(x[q * 16 + e]),
+                                                 __uint_as_float(x[q * 16 + e + 1])), av, bv);
               float2 pv;
-              if (use_poly(q * 8 + (e >> 1))) {
+              if (POLY(q * 8 + (e >> 1))) {
                 pv = ex2_poly2(w);
               } else {
                 pv.x = ex2_mufu(w.x);
@@ -514,17 +599,17 @@ __global__ void __maxnreg__(kRegs8) kv8_doc_tc(const Doc8Params p) {
               pk[q * 8 + (e >> 1)] = f2_to_h2(pv.x, pv.y);
             }
             const float2 r2 = fadd2(rs[0], rs[1]);
-            l = fmaf(r2.x + r2.y, in.z, l);
+            l = fmaf(r2.x + r2.y, rv, l);
           }
-          tmem_st32(t_S + c * 32, pk);
+          tmem_st16(t_S + c * 16, pk);   // over columns that have been read
         }
         if (mx != mx) l = mx;
         // O rescale for rows whose maximum moved (rare).  The product of this
         // stream's tile before is complete: it was issued ahead of this S.
         if (tile > first && __any_sync(0xffffffffu, need)) {
           const float f = need ? ex2_mufu(m_old - m) : 1.f;
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
+#pragma unroll 1
+          for (int c = 0; c < D / 64; ++c) {
             uint32_t o[32];
             tmem_ld32(t_O + c * 32, o);
             tmem_ld_wait();
@@ -535,7 +620,7 @@ __global__ void __maxnreg__(kRegs8) kv8_doc_tc(const Doc8Params p) {
         }
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(p_full + st);
+        warp_arrive(p_full + st, lane);
       }
       if (!ok) break;
       const int64_t prow = ((int64_t)s.u * p.plan.max_chunks + s.chunk) * kGroupRows + st * 128 + rt;
@@ -543,25 +628,47 @@ __global__ void __maxnreg__(kRegs8) kv8_doc_tc(const Doc8Params p) {
         if (!(ok = warp_wait(o_done + st, od_ph, abort_flag, p.wait_limit, status))) break;
         od_ph ^= 1;
         tc_fence_after();
-        float4* dst = reinterpret_cast<float4*>(p.doc_o + prow * D);
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
+        // through the rows' place in the query tile (a box of it, or half of each
+        // row, for each half), so that rows go out in whole sectors
+        constexpr int U = D / 16, RP = 32 / U;
+        float* dst = p.doc_o + (prow - lane) * D + half * (D / 2);
+        const int n_rows = p.rows - (row - lane);
+#pragma unroll 1
+        for (int c = 0; c < D / 64; ++c) {
           uint32_t o[32];
           tmem_ld32(t_O + c * 32, o);
           tmem_ld_wait();
-          if (valid) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              dst[(c * 32 + e) / 4] =
-                  make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]),
-                              __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
+          for (int k = 0; k < 8 / U; ++k) {
+#pragma unroll
+            for (int e = 0; e < U; ++e) {
+              const int i = 4 * (k * U + e);
+              *unit_at(tq, rt, half * U + e) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+            }
+            __syncwarp();
+            uint4 w[RP == 4 ? 8 : 4];
+#pragma unroll
+            for (int i = 0; i < 32 / RP; ++i)
+              w[i] = *unit_at(tq, wq * 32 + i * RP + lane / U, half * U + lane % U);
+#pragma unroll
+            for (int i = 0; i < 32 / RP; ++i)
+              if (i * RP + lane / U < n_rows)
+                *reinterpret_cast<uint4*>(dst + (i * RP + lane / U) * D + c * 32 + k * U * 4 +
+                                          (lane % U) * 4) = w[i];
+            __syncwarp();
           }
         }
         tc_fence_before();
       }
+      float lo;
+      if (!(ok = swap_half(l, lo))) break;
+      l = half == 0 ? l + lo : lo + l;
       // a NaN row keeps a finite maximum so that the merge does not skip it
-      if (valid)
+      if (half == 0 && row < p.rows)
         reinterpret_cast<float2*>(p.doc_ml)[prow] = make_float2(l != l && m == -INFINITY ? 0.f : m, l);
+      warp_arrive(pb, lane);     // lo is read: the next run's scales may go over it
+      if (!(ok = warp_wait(pb, pr_ph, abort_flag, p.wait_limit, status))) break;
+      pr_ph ^= 1;
       t0 += s.n;
     }
   }
