@@ -15,18 +15,24 @@
 // transposed, S^T = K Q^T and O^T = V^T P^T, so the 16-wide mma dimension is
 // the keys' and the values', and the 8-wide one the few rows.  A lane reads a
 // key's contiguous 32 bytes (values: 16 bytes of four keys); which dims and
-// keys an mma index stands for is free as long as both operands agree, so the
-// loads need no shuffling through shared memory.  e4m3 -> f16 is exact; queries
-// are scaled by a power of two into f16's range; P^T goes from the
-// accumulators to the operand by a transposing move.
+// keys an mma index stands for is free as long as both operands agree, so no
+// value is shuffled.  e4m3 -> f16 is exact; queries are scaled by a power of
+// two into f16's range; P^T goes from the accumulators to the operand by a
+// transposing move.
 //
-// WAYS warps share an item, each a contiguous range of its 16-key chunks; the
-// partials meet in shared memory, where each row's (m, l, O) are joined with
-// the document pass's.  Bound: HBM for decode (one read of every segment).
+// A warp brings 16 keys (K and V, 4 KB) at a time into its own ring in shared
+// memory with 16-byte asynchronous copies, two chunks ahead; what bounds the
+// pass is latency, so 16 (12 with two tiles of rows) warps share an SM.  WAYS
+// warps share an item, each a contiguous range of its chunks; the partials meet
+// in shared memory (over the rings), where each row's (m, l, O) are joined with
+// the document pass's: the lanes take the partials' maxima and sums, the warp
+// then adds the partials' rows with their weights known.
 #include <atomic>
+#include <type_traits>
 
 #include "kv8.cuh"
 #include "internal.h"
+#include "warp_mma.cuh"
 
 namespace pp {
 namespace {
@@ -75,30 +81,33 @@ struct State {
   float o[NT][D / 16][4];  // O^T: [tile][dim pair j][2 rows x 2 dims]
 };
 
-// The chunk's stored bytes of one warp: two keys' 32 (16) bytes and four
-// values' 16 (8) bytes a lane.
+// ---- the warp's ring: a stage holds 16 keys' rows, then their values'
 template <int D>
-struct Chunk {
-  uint32_t k[2][D / 16];
-  uint32_t v[4][D / 32];
+struct Ring {
+  static constexpr int ST = D == 128 ? 3 : 4;         // stages
+  static constexpr int HALF = 16 * D, STAGE = 2 * HALF;
+  static constexpr int BYTES = ST * STAGE;
 };
 
+// Byte offset of 16-byte unit u of row `row`; units are XOR-ed with the row (two
+// rows of 64 bytes to a line) so that eight lanes' reads meet 32 banks.
 template <int D>
-__device__ __forceinline__ void load_chunk(Chunk<D>& ch, const uint8_t* kb, const uint8_t* vb,
-                                           int r, int c) {
+__device__ __forceinline__ uint32_t unit_off(int row, int u) {
+  if constexpr (D == 128) return (uint32_t)(row * 128 + ((u ^ (row & 7)) << 4));
+  const int line = row >> 1;
+  return (uint32_t)(line * 128 + ((((row & 1) * 4 + u) ^ ((line & 3) * 2)) << 4));
+}
+
+template <int D>
+__device__ __forceinline__ void fetch_chunk(uint32_t stage, const uint8_t* kb, const uint8_t* vb,
+                                            int lane) {
+  constexpr int U = D / 16;
 #pragma unroll
-  for (int a = 0; a < 2; ++a)
-#pragma unroll
-    for (int i = 0; i < D / 64; ++i)
-      *reinterpret_cast<uint4*>(&ch.k[a][4 * i]) = __ldg(
-          reinterpret_cast<const uint4*>(kb + (r + 8 * a) * D + c * (D / 4) + 16 * i));
-#pragma unroll
-  for (int a = 0; a < 4; ++a) {
-    const uint8_t* at = vb + (2 * c + (a & 1) + 8 * (a >> 1)) * D + r * (D / 8);
-    if constexpr (D == 128)
-      *reinterpret_cast<uint4*>(&ch.v[a][0]) = __ldg(reinterpret_cast<const uint4*>(at));
-    else
-      *reinterpret_cast<uint2*>(&ch.v[a][0]) = __ldg(reinterpret_cast<const uint2*>(at));
+  for (int i = 0; i < 16 * U / 32; ++i) {
+    const int x = lane + 32 * i;
+    const uint32_t at = stage + unit_off<D>(x / U, x % U);
+    cp_async16(at, kb + x * 16, 16);
+    cp_async16(at + Ring<D>::HALF, vb + x * 16, 16);
   }
 }
 
@@ -107,7 +116,7 @@ __device__ __forceinline__ void load_chunk(Chunk<D>& ch, const uint8_t* kb, cons
 // held before, so its values are taken as 0 (0 * NaN would spoil the sum).
 template <int D, int NT>
 __device__ __forceinline__ void chunk_step(State<D, NT>& st, const uint32_t (&qf)[NT][D / 8],
-                                           Chunk<D>& ch, int t0, const int (&lim)[NT][2],
+                                           const uint8_t* stage, int t0, const int (&lim)[NT][2],
                                            int t_max, int t_min, const float (&qs)[NT][2],
                                            float ks, float vs, int r, int c) {
   float s[NT][4];
@@ -115,10 +124,17 @@ __device__ __forceinline__ void chunk_step(State<D, NT>& st, const uint32_t (&qf
   for (int t = 0; t < NT; ++t)
 #pragma unroll
     for (int e = 0; e < 4; ++e) s[t][e] = 0.f;
+  uint32_t kx[2][D / 16];
+#pragma unroll
+  for (int a = 0; a < 2; ++a)
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i)
+      *reinterpret_cast<uint4*>(&kx[a][4 * i]) = *reinterpret_cast<const uint4*>(
+          stage + unit_off<D>(r + 8 * a, c * (D / 64) + i));
 #pragma unroll
   for (int kk = 0; kk < D / 16; ++kk) {
-    const uint32_t a0 = e4m3x2_to_h2(ch.k[0][kk]), a2 = e4m3x2_hi_to_h2(ch.k[0][kk]);
-    const uint32_t a1 = e4m3x2_to_h2(ch.k[1][kk]), a3 = e4m3x2_hi_to_h2(ch.k[1][kk]);
+    const uint32_t a0 = e4m3x2_to_h2(kx[0][kk]), a2 = e4m3x2_hi_to_h2(kx[0][kk]);
+    const uint32_t a1 = e4m3x2_to_h2(kx[1][kk]), a3 = e4m3x2_hi_to_h2(kx[1][kk]);
 #pragma unroll
     for (int t = 0; t < NT; ++t) mma_f16(s[t], a0, a1, a2, a3, qf[t][2 * kk], qf[t][2 * kk + 1]);
   }
@@ -175,20 +191,32 @@ __device__ __forceinline__ void chunk_step(State<D, NT>& st, const uint32_t (&qf
     pb[t][0] = transpose8(f2_to_h2(pr[0], pr[1]));
     pb[t][1] = transpose8(f2_to_h2(pr[2], pr[3]));
   }
+  uint32_t vx[4][D / 32];
+#pragma unroll
+  for (int a = 0; a < 4; ++a) {
+    const int row = 2 * c + (a & 1) + 8 * (a >> 1);
+    const uint8_t* at = stage + Ring<D>::HALF;
+    if constexpr (D == 128)
+      *reinterpret_cast<uint4*>(&vx[a][0]) =
+          *reinterpret_cast<const uint4*>(at + unit_off<D>(row, r));
+    else
+      *reinterpret_cast<uint2*>(&vx[a][0]) =
+          *reinterpret_cast<const uint2*>(at + unit_off<D>(row, r >> 1) + (r & 1) * 8);
+  }
   if (t0 + 15 > t_max) {
 #pragma unroll
     for (int a = 0; a < 4; ++a)
       if (t0 + 2 * c + (a & 1) + 8 * (a >> 1) > t_max)
 #pragma unroll
-        for (int w = 0; w < D / 32; ++w) ch.v[a][w] = 0u;
+        for (int w = 0; w < D / 32; ++w) vx[a][w] = 0u;
   }
 #pragma unroll
   for (int w = 0; w < D / 32; ++w) {      // 4 bytes of each value row: dims 4w .. 4w + 3 of the lane's
     uint32_t x[4][2];
 #pragma unroll
     for (int a = 0; a < 4; ++a) {
-      x[a][0] = e4m3x2_to_h2(ch.v[a][w]);
-      x[a][1] = e4m3x2_hi_to_h2(ch.v[a][w]);
+      x[a][0] = e4m3x2_to_h2(vx[a][w]);
+      x[a][1] = e4m3x2_hi_to_h2(vx[a][w]);
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -201,13 +229,14 @@ __device__ __forceinline__ void chunk_step(State<D, NT>& st, const uint32_t (&qf
 }
 
 // Chunks [c0, c1) of one token sequence (page table `tab`): 32 table entries
-// and scales are fetched at a time, a chunk's bytes one chunk ahead.
+// and scales are fetched at a time.
 template <int D, int NT>
 __device__ __forceinline__ void scan(State<D, NT>& st, const uint32_t (&qf)[NT][D / 8],
                                      const Attn8Params& p, const int32_t* tab, int h, int c0,
                                      int c1, const int (&lim)[NT][2], int t_max, int t_min,
-                                     const float (&qs)[NT][2], int lane) {
-  const int r = lane >> 2, c = lane & 3;
+                                     const float (&qs)[NT][2], uint8_t* ring, int lane) {
+  constexpr int ST = Ring<D>::ST;
+  const uint32_t ring_u = smem_u32(ring);
   const int lper = p.lper, per = 1 << lper;   // chunks per page: 1, 2, 4, 8
   for (int b = c0; b < c1; b += 32) {
     const int n = min(32, c1 - b);
@@ -215,31 +244,34 @@ __device__ __forceinline__ void scan(State<D, NT>& st, const uint32_t (&qf)[NT][
     float ks = 1.f, vs = 1.f;
     if (lane < n) {
       pg = page_of(tab[(b + lane) >> lper], p.L.n_pages);
-      if (pg >= 0) {
-        ks = p.L.k_scale[(int64_t)pg * p.L.H + h];
-        vs = p.L.v_scale[(int64_t)pg * p.L.H + h];
-      } else {
-        set_status(p.L.status, PP_DEV_BAD_PAGE);
-      }
+      if (pg < 0) set_status(p.L.status, PP_DEV_BAD_PAGE);
     }
-    auto base = [&](int j, int& pgj) -> int64_t {
-      pgj = __shfl_sync(0xffffffffu, pg, j);
-      return (((int64_t)(pgj < 0 ? 0 : pgj) * p.L.H + h) * p.L.page + ((b + j) & (per - 1)) * 16) * D;
-    };
-    Chunk<D> cur, nxt;
-    int pgc = -1, pgn = -1;
-    int64_t at = base(0, pgc);
-    if (pgc >= 0) load_chunk<D>(cur, p.L.k + at, p.L.v + at, r, c);
-    for (int j = 0; j < n; ++j) {
-      if (j + 1 < n) {
-        at = base(j + 1, pgn);
-        if (pgn >= 0) load_chunk<D>(nxt, p.L.k + at, p.L.v + at, r, c);
+    auto fetch = [&](int j) {
+      const int pgj = __shfl_sync(0xffffffffu, pg, j);
+      if (pgj >= 0) {
+        const int64_t at =
+            (((int64_t)pgj * p.L.H + h) * p.L.page + ((b + j) & (per - 1)) * 16) * D;
+        fetch_chunk<D>(ring_u + (j % ST) * Ring<D>::STAGE, p.L.k + at, p.L.v + at, lane);
       }
+    };
+#pragma unroll
+    for (int j = 0; j < ST - 1; ++j) {
+      if (j < n) fetch(j);
+      asm volatile("cp.async.commit_group;\n" ::: "memory");
+    }
+    if (pg >= 0) {
+      ks = p.L.k_scale[(int64_t)pg * p.L.H + h];
+      vs = p.L.v_scale[(int64_t)pg * p.L.H + h];
+    }
+    for (int j = 0; j < n; ++j) {
+      if (j + ST - 1 < n) fetch(j + ST - 1);
+      asm volatile("cp.async.commit_group;\ncp.async.wait_group %0;\n" ::"n"(ST - 1) : "memory");
+      __syncwarp();
       const float ksj = __shfl_sync(0xffffffffu, ks, j), vsj = __shfl_sync(0xffffffffu, vs, j);
-      if (pgc >= 0)
-        chunk_step<D, NT>(st, qf, cur, (b + j) * 16, lim, t_max, t_min, qs, ksj, vsj, r, c);
-      cur = nxt;
-      pgc = pgn;
+      if (__shfl_sync(0xffffffffu, pg, j) >= 0)
+        chunk_step<D, NT>(st, qf, ring + (j % ST) * Ring<D>::STAGE, (b + j) * 16, lim, t_max, t_min,
+                          qs, ksj, vsj, lane >> 2, lane & 3);
+      __syncwarp();
     }
   }
 }
@@ -252,18 +284,42 @@ __device__ __forceinline__ void part_of(int n, int w, int ways, int& c0, int& c1
 
 constexpr int kMaxWays = 8;   // warps of a CTA, and of an item, at most
 
+// A warp's shared memory: its ring, and over it, when the keys are done, its
+// partial result: (m, l) of its rows, then O, rows of D + 4 floats.
 template <int D, int NT>
-__global__ void __launch_bounds__(kMaxWays * 32) kv8_attn(const Attn8Params p) {
-  constexpr int ROWS = 8 * NT, LD = D + 4;
-  extern __shared__ float sm[];
+struct Smem8 {
+  static constexpr int ROWS = 8 * NT, LD = D + 4;
+  static constexpr int PART = ROWS * (LD + 2) * 4;
+  static constexpr int WARP = PART > Ring<D>::BYTES ? (PART + 127) / 128 * 128 : Ring<D>::BYTES;
+};
+
+// Partial j of a row's document partials: slot of the row's (m, l) and O.
+struct DocRow {
+  int64_t slot;   // of the first
+  int n;          // partials
+  int two;        // a row group of one M tile: two a chunk, 128 rows apart
+  __device__ __forceinline__ int64_t at(int j) const {
+    return two ? slot + (int64_t)(j >> 1) * kGroupRows + (j & 1) * 128
+               : slot + (int64_t)j * kGroupRows;
+  }
+};
+
+// Four warps a block, and eight where that many share an item.
+template <int D, int NT, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, (NT == 1 ? 16 : 12) / WARPS)
+    kv8_attn(const Attn8Params p) {
+  using M = Smem8<D, NT>;
+  constexpr int LD = M::LD;
+  extern __shared__ __align__(128) uint8_t sm[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r = lane >> 2, c = lane & 3;
   const int per_cta = (blockDim.x >> 5) / p.ways;
   const int64_t item = (int64_t)blockIdx.x * per_cta + warp / p.ways;
   const int way = warp % p.ways;
   const bool live = item < p.n_items;
-  float* my_o = sm + (int64_t)warp * ROWS * LD;
-  float* my_ml = sm + (int64_t)(blockDim.x >> 5) * ROWS * LD + warp * ROWS * 2;
+  uint8_t* ring = sm + warp * M::WARP;
+  float* my_ml = reinterpret_cast<float*>(ring);
+  float* my_o = my_ml + 2 * M::ROWS;
   int r0 = 0, kvh = 0, hb = 0, nh = 1, nrow = 0;
   if (live) {
     const int x = (int)(item % (p.L.H * p.gt));
@@ -350,7 +406,8 @@ __global__ void __launch_bounds__(kMaxWays * 32) kv8_attn(const Attn8Params p) {
 #pragma unroll
         for (int a = 0; a < 2; ++a) all &= t * 8 + 2 * c + a >= n_pairs || sidr[t][a] != 0;
       const int t_min = __all_sync(0xffffffffu, all) ? p.doc_len - 1 : -1;
-      scan<D, NT>(st, qf, p, p.L.doc_table, kvh, c0, c1, dl, p.doc_len - 1, t_min, qs, lane);
+      scan<D, NT>(st, qf, p, p.L.doc_table, kvh, c0, c1, dl, p.doc_len - 1, t_min, qs, ring,
+                  lane);
     }
     // ---- segments: one pass per stretch of rows of one stream
     for (int ra = 0; ra < nrow;) {
@@ -380,11 +437,13 @@ __global__ void __launch_bounds__(kMaxWays * 32) kv8_attn(const Attn8Params p) {
         int c0, c1;
         part_of((hi + 16) >> 4, way, p.ways, c0, c1);
         scan<D, NT>(st, qf, p, p.L.seg_table + (int64_t)(s - 1) * p.L.seg_pages, kvh, c0, c1, lm,
-                    hi, lo, qs, lane);
+                    hi, lo, qs, ring, lane);
       }
       ra = rb;
     }
-    // ---- this warp's partial to shared memory, row by row
+    // ---- this warp's partial to shared memory, row by row, over the ring
+    asm volatile("cp.async.wait_group 0;\n" ::: "memory");
+    __syncwarp();
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -393,6 +452,7 @@ __global__ void __launch_bounds__(kMaxWays * 32) kv8_attn(const Attn8Params p) {
 #pragma unroll
         for (int o2 = 4; o2 < 32; o2 <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o2);
         const int n2 = t * 8 + 2 * c + a;
+        if (n2 >= n_pairs) continue;
         if (r == 0) {
           my_ml[2 * n2] = st.m[t][a];
           my_ml[2 * n2 + 1] = l;
@@ -405,78 +465,136 @@ __global__ void __launch_bounds__(kMaxWays * 32) kv8_attn(const Attn8Params p) {
   }
   if (p.ways > 1) __syncthreads(); else __syncwarp();
   if (!live) return;
-  // ---- merge: the item's warps take its rows in turn, a lane E dims
+  // ---- merge: the item's warps take its rows in turn, a lane E dims.  Lane n
+  // finds where pair n's document partials are.
   constexpr int E = D / 32;
-  const int w0 = warp - way;
-  const float* it_o = sm + (int64_t)w0 * ROWS * LD;
-  const float* it_ml = sm + (int64_t)(blockDim.x >> 5) * ROWS * LD + w0 * ROWS * 2;
-  for (int n = way; n < nrow * nh; n += p.ways) {
+  DocRow dr{0, 0, 0};
+  int q_live = 0;
+  if (lane < nrow * nh) {
+    const int row = r0 + lane / nh;
+    q_live = stream_query(p.q_sid[row], p.L.P_max) ? 1 : 0;
+    if (p.has_doc && q_live) {
+      const int64_t pair = (int64_t)row * p.g + hb + lane % nh;
+      const int u = kvh * p.plan.G + (int)(pair / kGroupRows);
+      const int64_t ub = plan_unit_begin(p.plan, u);
+      dr.two = (int64_t)p.rows * p.g - pair / kGroupRows * kGroupRows <= 128;
+      dr.n = (plan_cta_of(p.plan, ub + p.plan.T - 1) - plan_cta_of(p.plan, ub) + 1) << dr.two;
+      dr.slot = (int64_t)u * p.plan.max_chunks * kGroupRows + pair % kGroupRows;
+    }
+  }
+  const uint8_t* it = sm + (warp - way) * M::WARP;
+  auto row_of = [&](int n) {
+    DocRow d;
+    d.slot = __shfl_sync(0xffffffffu, dr.slot, n);
+    d.n = __shfl_sync(0xffffffffu, dr.n, n);
+    d.two = __shfl_sync(0xffffffffu, dr.two, n);
+    return d;
+  };
+  using Vec = typename std::conditional<E == 4, float4, float2>::type;
+  auto doc_vec = [&](int64_t slot) {
+    return __ldg(reinterpret_cast<const Vec*>(p.doc_o + slot * D) + lane);
+  };
+  auto lane_ml = [&](const DocRow& d, int n, int j) {    // (m, l) of the row's partial j
+    if (j < p.ways)
+      return *reinterpret_cast<const float2*>(it + j * M::WARP + n * 8);
+    if (j - p.ways < d.n)
+      return __ldg(reinterpret_cast<const float2*>(p.doc_ml) + d.at(j - p.ways));
+    return make_float2(-INFINITY, 0.f);
+  };
+  // the next row's maxima and first document row are on their way while one is joined
+  const int n_all = nrow * nh;
+  DocRow nd = row_of(way < n_all ? way : 0);
+  float2 nml = make_float2(-INFINITY, 0.f);
+  Vec nv{};
+  if (way < n_all) {
+    nml = lane_ml(nd, way, lane);
+    if (nd.n) nv = doc_vec(nd.slot);
+  }
+  for (int n = way; n < n_all; n += p.ways) {
     const int row = r0 + n / nh, head = kvh * p.g + hb + n % nh;
-    const bool query = stream_query(p.q_sid[row], p.L.P_max);
+    const DocRow d = nd;
+    const float2 ml0 = nml;
+    const Vec v0 = nv;
+    const int n2 = n + p.ways;
+    nd = row_of(n2 < n_all ? n2 : 0);
+    if (n2 < n_all) {
+      nml = lane_ml(nd, n2, lane);
+      if (nd.n) nv = doc_vec(nd.slot);
+    }
+    const bool query = __shfl_sync(0xffffffffu, q_live, n) != 0;
     float m = -INFINITY, l = 0.f, acc[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
-    auto fold_in = [&](float m2, float l2, const float* src) {
-      if (m2 == -INFINITY) return;        // saw no key
-      const float mm = fmaxf(m, m2);
-      const float x = m == -INFINITY ? 0.f : ex2_mufu(m - mm), y = ex2_mufu(m2 - mm);
-      l = l * x + l2 * y;
+    const int cnt = query ? p.ways + d.n : 0;
+    for (int b = 0; b < cnt; b += 32) {
+      const float2 ml = b == 0 ? ml0 : lane_ml(d, n, b + lane);
+      float mm = ml.x;
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] = acc[e] * x + src[lane * E + e] * y;
+      for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+      mm = fmaxf(mm, m);
+      if (mm == -INFINITY) continue;      // none of them saw a key
+      const float x = m == -INFINITY ? 0.f : ex2_mufu(m - mm);
+      // (of a partial that saw no key nothing is read: its O may hold anything)
+      const float y = ml.x == -INFINITY ? 0.f : ex2_mufu(ml.x - mm);
+      const uint32_t saw = __ballot_sync(0xffffffffu, ml.x != -INFINITY);
+      float ls = ml.x == -INFINITY ? 0.f : ml.y * y;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
+      l = l * x + ls;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] *= x;
       m = mm;
-    };
-    if (query) {
-      for (int w = 0; w < p.ways; ++w)
-        fold_in(it_ml[(w * ROWS + n) * 2], it_ml[(w * ROWS + n) * 2 + 1],
-                it_o + (w * ROWS + n) * LD);
-      if (p.has_doc) {
-        const int64_t dr = (int64_t)row * p.g + hb + n % nh;
-        const int u = kvh * p.plan.G + (int)(dr / kGroupRows);
-        const int64_t ub = plan_unit_begin(p.plan, u);
-        const int d0 = plan_cta_of(p.plan, ub);
-        const int d1 = plan_cta_of(p.plan, ub + p.plan.T - 1);
-        const int64_t sl0 = (int64_t)u * p.plan.max_chunks * kGroupRows + dr % kGroupRows;
-        // a row group of one M tile has two partials a chunk, 128 rows apart
-        const bool two = (int64_t)p.rows * p.g - dr / kGroupRows * kGroupRows <= 128;
-        for (int d = d0; d <= d1; ++d) {
-          const int64_t sl = sl0 + (int64_t)(d - d0) * kGroupRows;
-          const float2 ml = *reinterpret_cast<const float2*>(p.doc_ml + sl * 2);
-          fold_in(ml.x, ml.y, p.doc_o + sl * D);
-          if (two) {
-            const float2 m2 = *reinterpret_cast<const float2*>(p.doc_ml + (sl + 128) * 2);
-            fold_in(m2.x, m2.y, p.doc_o + (sl + 128) * D);
-          }
-        }
+      const int nb = min(32, cnt - b);
+#pragma unroll 4
+      for (int j = 0; j < nb; ++j) {
+        const float yj = __shfl_sync(0xffffffffu, y, j);
+        if (!(saw >> j & 1)) continue;
+        Vec v;
+        if (b + j < p.ways)
+          v = reinterpret_cast<const Vec*>(it + j * M::WARP + M::ROWS * 8 + n * LD * 4)[lane];
+        else
+          v = b + j == p.ways ? v0 : doc_vec(d.at(b + j - p.ways));
+        const float* f = reinterpret_cast<const float*>(&v);
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(f[e], yj, acc[e]);
       }
     }
-    const bool any = query && m != -INFINITY;
+    const bool any = m != -INFINITY;
     const float inv = any ? 1.f / l : 0.f;
-    uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + ((int64_t)row * p.Hq + head) * D + lane * E);
+    uint32_t w[E / 2];
 #pragma unroll
-    for (int e = 0; e < E; e += 2) dst[e / 2] = any ? f2_to_bf2(acc[e] * inv, acc[e + 1] * inv) : 0u;
+    for (int e = 0; e < E; e += 2) w[e / 2] = any ? f2_to_bf2(acc[e] * inv, acc[e + 1] * inv) : 0u;
+    uint16_t* dst = p.o + ((int64_t)row * p.Hq + head) * D + lane * E;
+    if constexpr (E == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint32_t*>(dst) = w[0];
     if (p.lse && lane == 0)
       p.lse[(int64_t)row * p.Hq + head] = any ? (m + log2f(l)) * kLn2 : -INFINITY;
   }
 }
 
-template <int D, int NT>
-cudaError_t launch(const Attn8Params& p, int warps, cudaStream_t st) {
-  const int smem = warps * 8 * NT * (D + 4 + 2) * (int)sizeof(float);
+template <int D, int NT, int WARPS>
+cudaError_t launch_as(const Attn8Params& p, cudaStream_t st) {
+  constexpr int SMEM = WARPS * Smem8<D, NT>::WARP;
   static std::atomic<uint64_t> ready{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const uint64_t bit = 1ull << (dev & 63);
   if (!(ready.load() & bit)) {
-    e = cudaFuncSetAttribute(kv8_attn<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kMaxWays * 8 * NT * (D + 6) * (int)sizeof(float));
+    e = cudaFuncSetAttribute(kv8_attn<D, NT, WARPS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             SMEM);
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit);
   }
-  const int per = warps / p.ways;
+  const int per = WARPS / p.ways;
   const int64_t grid = ((int64_t)p.n_items + per - 1) / per;
-  kv8_attn<D, NT><<<(unsigned)grid, warps * 32, smem, st>>>(p);
+  kv8_attn<D, NT, WARPS><<<(unsigned)grid, WARPS * 32, SMEM, st>>>(p);
   return cudaGetLastError();
+}
+
+template <int D, int NT>
+cudaError_t launch(const Attn8Params& p, cudaStream_t st) {
+  return p.ways > 4 ? launch_as<D, NT, 8>(p, st) : launch_as<D, NT, 4>(p, st);
 }
 
 }  // namespace
@@ -518,10 +636,8 @@ cudaError_t launch_kv8_attn(const pp_kv8_layer& L, int doc_len, const uint16_t* 
     ways *= 2;
   p.ways = ways;
   p.lper = L.page == 16 ? 0 : L.page == 32 ? 1 : L.page == 64 ? 2 : 3;
-  const int warps = ways > 4 ? ways : 4;
-  if (L.d == 128)
-    return most == 8 ? launch<128, 1>(p, warps, st) : launch<128, 2>(p, warps, st);
-  return most == 8 ? launch<64, 1>(p, warps, st) : launch<64, 2>(p, warps, st);
+  if (L.d == 128) return most == 8 ? launch<128, 1>(p, st) : launch<128, 2>(p, st);
+  return most == 8 ? launch<64, 1>(p, st) : launch<64, 2>(p, st);
 }
 
 }  // namespace pp
