@@ -304,6 +304,28 @@ struct DocRow {
   }
 };
 
+// Where the document partials of (query row `row`, query head kvh * g + hq) are.
+__device__ __forceinline__ DocRow doc_row(const Attn8Params& p, int row, int kvh, int hq) {
+  const int64_t pair = (int64_t)row * p.g + hq;
+  const int u = kvh * p.plan.G + (int)(pair / kGroupRows);
+  const int64_t ub = plan_unit_begin(p.plan, u);
+  DocRow d;
+  d.two = (int64_t)p.rows * p.g - pair / kGroupRows * kGroupRows <= 128;
+  d.n = (plan_cta_of(p.plan, ub + p.plan.T - 1) - plan_cta_of(p.plan, ub) + 1) << d.two;
+  d.slot = (int64_t)u * p.plan.max_chunks * kGroupRows + pair % kGroupRows;
+  return d;
+}
+
+// A lane's share of row n = 2c + a of tile t of a partial: dims (D/8) r ..
+template <int D>
+__device__ __forceinline__ void load_part(float (&x)[D / 8], const float* row, int r) {
+#pragma unroll
+  for (int i = 0; i < D / 8; i += 4) {
+    const float4 v = __ldg(reinterpret_cast<const float4*>(row + r * (D / 8) + i));
+    x[i] = v.x; x[i + 1] = v.y; x[i + 2] = v.z; x[i + 3] = v.w;
+  }
+}
+
 // Four warps a block, and eight where that many share an item.
 template <int D, int NT, int WARPS>
 __global__ void __launch_bounds__(WARPS * 32, (NT == 1 ? 16 : 12) / WARPS)
@@ -389,6 +411,36 @@ __global__ void __launch_bounds__(WARPS * 32, (NT == 1 ? 16 : 12) / WARPS)
         for (int j = 0; j < D / 16; ++j) st.o[t][j][a] = st.o[t][j][2 + a] = 0.f;
       }
     }
+    // ---- rows that a warp has to itself start from their first document partial
+    DocRow dr2[NT][2];
+    if (NT > 1 && p.has_doc && p.ways == 1) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        // lane n (of the tile's 8) finds pair n's partials
+        DocRow d{0, 0, 0};
+        const int n = t * 8 + (lane & 7);
+        if (n < n_pairs && stream_query(p.q_sid[r0 + n / nh], p.L.P_max))
+          d = doc_row(p, r0 + n / nh, kvh, hb + n % nh);
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+          dr2[t][a].slot = __shfl_sync(0xffffffffu, d.slot, 2 * c + a);
+          dr2[t][a].n = __shfl_sync(0xffffffffu, d.n, 2 * c + a);
+          dr2[t][a].two = __shfl_sync(0xffffffffu, d.two, 2 * c + a);
+          if (dr2[t][a].n == 0) continue;
+          const float2 ml = __ldg(reinterpret_cast<const float2*>(p.doc_ml) + dr2[t][a].slot);
+          if (ml.x == -INFINITY) continue;     // saw no key: its O may hold anything
+          float x[D / 8];
+          load_part<D>(x, p.doc_o + dr2[t][a].slot * D, r);
+          st.m[t][a] = ml.x;
+          st.l[t][a] = r == 0 ? ml.y : 0.f;
+#pragma unroll
+          for (int j = 0; j < D / 16; ++j) {
+            st.o[t][j][a] = x[2 * j];
+            st.o[t][j][2 + a] = x[2 * j + 1];
+          }
+        }
+      }
+    }
     // ---- document
     if (p.doc_len > 0) {
       int dl[NT][2];
@@ -441,6 +493,48 @@ __global__ void __launch_bounds__(WARPS * 32, (NT == 1 ? 16 : 12) / WARPS)
       }
       ra = rb;
     }
+    if (NT > 1 && p.ways == 1) {
+      // ---- the further document partials, and out
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+          float m = st.m[t][a], l = st.l[t][a];
+#pragma unroll
+          for (int o2 = 4; o2 < 32; o2 <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o2);
+          const int n2 = t * 8 + 2 * c + a;
+          if (n2 >= n_pairs) continue;
+          for (int k = 1; p.has_doc && k < dr2[t][a].n; ++k) {
+            const int64_t sl = dr2[t][a].at(k);
+            const float2 ml = __ldg(reinterpret_cast<const float2*>(p.doc_ml) + sl);
+            if (ml.x == -INFINITY) continue;
+            float x[D / 8];
+            load_part<D>(x, p.doc_o + sl * D, r);
+            const float mm = fmaxf(m, ml.x);
+            const float f = m == -INFINITY ? 0.f : ex2_mufu(m - mm), y = ex2_mufu(ml.x - mm);
+            l = l * f + ml.y * y;
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) {
+              st.o[t][j][a] = st.o[t][j][a] * f + x[2 * j] * y;
+              st.o[t][j][2 + a] = st.o[t][j][2 + a] * f + x[2 * j + 1] * y;
+            }
+            m = mm;
+          }
+          const bool any = sidr[t][a] != 0 && m != -INFINITY;
+          const float inv = any ? 1.f / l : 0.f;
+          uint32_t w[D / 16];
+#pragma unroll
+          for (int j = 0; j < D / 16; ++j)
+            w[j] = any ? f2_to_bf2(st.o[t][j][a] * inv, st.o[t][j][2 + a] * inv) : 0u;
+          const int64_t at = (int64_t)(r0 + n2 / nh) * p.Hq + kvh * p.g + hb + n2 % nh;
+#pragma unroll
+          for (int j = 0; j < D / 16; j += 4)
+            *reinterpret_cast<uint4*>(p.o + at * D + r * (D / 8) + 2 * j) =
+                make_uint4(w[j], w[j + 1], w[j + 2], w[j + 3]);
+          if (p.lse && r == 0) p.lse[at] = any ? (m + log2f(l)) * kLn2 : -INFINITY;
+        }
+      return;
+    }
     // ---- this warp's partial to shared memory, row by row, over the ring
     asm volatile("cp.async.wait_group 0;\n" ::: "memory");
     __syncwarp();
@@ -474,12 +568,7 @@ __global__ void __launch_bounds__(WARPS * 32, (NT == 1 ? 16 : 12) / WARPS)
     const int row = r0 + lane / nh;
     q_live = stream_query(p.q_sid[row], p.L.P_max) ? 1 : 0;
     if (p.has_doc && q_live) {
-      const int64_t pair = (int64_t)row * p.g + hb + lane % nh;
-      const int u = kvh * p.plan.G + (int)(pair / kGroupRows);
-      const int64_t ub = plan_unit_begin(p.plan, u);
-      dr.two = (int64_t)p.rows * p.g - pair / kGroupRows * kGroupRows <= 128;
-      dr.n = (plan_cta_of(p.plan, ub + p.plan.T - 1) - plan_cta_of(p.plan, ub) + 1) << dr.two;
-      dr.slot = (int64_t)u * p.plan.max_chunks * kGroupRows + pair % kGroupRows;
+      dr = doc_row(p, row, kvh, hb + lane % nh);
     }
   }
   const uint8_t* it = sm + (warp - way) * M::WARP;
@@ -626,13 +715,12 @@ cudaError_t launch_kv8_attn(const pp_kv8_layer& L, int doc_len, const uint16_t* 
   p.plan = plan;
   p.doc_o = part.doc_o; p.doc_ml = part.doc_ml;
   p.o = o; p.lse = lse;
-  // Warps per item: enough to fill the GPU when items are few, and a long
-  // segment cut so that one item is not a CTA's whole tail; at least four
-  // chunks a warp.
+  // Warps per item: enough to fill the GPU when items are few (they share the
+  // item's merge too, however short its keys), and a long segment cut so that
+  // one item is not a CTA's whole tail.
   const int64_t chunks = (int64_t)L.seg_pages * L.page / 16 + (p.doc_len + 15) / 16;
   int ways = 1;
-  while (ways < kMaxWays && chunks / (2 * ways) >= 4 &&
-         (items * ways < 12LL * num_sms || (ways < 4 && chunks / ways > 16)))
+  while (ways < kMaxWays && (items * ways < 12LL * num_sms || (ways < 4 && chunks / ways > 16)))
     ways *= 2;
   p.ways = ways;
   p.lper = L.page == 16 ? 0 : L.page == 32 ? 1 : L.page == 64 ? 2 : 3;
