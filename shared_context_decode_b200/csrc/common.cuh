@@ -114,10 +114,8 @@ __device__ __forceinline__ float ex2_mufu(float x) {
 // clamped at -126 (2^f can be just below 1, exponent field 126, so n >= -126
 // keeps the field >= 0): -inf and underflow give at most 2^-125, zero for
 // every use here.  Valid for x <= 64.
-__device__ __forceinline__ float2 ex2_poly2(float2 x) {
+__device__ __forceinline__ float2 ex2_poly2_clamped(float2 x) {
   constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23
-  x.x = fmaxf(x.x, -126.f);
-  x.y = fmaxf(x.y, -126.f);
   const float2 t = fadd2_rm(x, make_float2(kMagic, kMagic));
   const float2 n = fadd2(t, make_float2(-kMagic, -kMagic));
   const float2 f = fadd2(x, make_float2(-n.x, -n.y));
@@ -129,6 +127,16 @@ __device__ __forceinline__ float2 ex2_poly2(float2 x) {
   r.x = __int_as_float(__float_as_int(p.x) + (__float_as_int(t.x) << 23));
   r.y = __int_as_float(__float_as_int(p.y) + (__float_as_int(t.y) << 23));
   return r;
+}
+__device__ __forceinline__ float2 ex2_poly2(float2 x) {
+  return ex2_poly2_clamped(make_float2(fmaxf(x.x, -126.f), fmaxf(x.y, -126.f)));
+}
+// The same, but a NaN gives a huge number (0x7f7fffff: the canonical NaN's bits
+// plus the exponent a NaN leaves) and not 2^-126.
+__device__ __forceinline__ float2 ex2_poly2_nan(float2 x) {
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(x.x) : "f"(-126.f));
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(x.y) : "f"(-126.f));
+  return ex2_poly2_clamped(x);
 }
 
 // Softmax exponentials: pairs p with p % 5 in {1, 3} go to the FMA-pipe

@@ -5,8 +5,11 @@
 //     S = Q X^T                   X the stored keys, S fp32 in TMEM
 //     w = S a + log2 vs           a = query scale * page's key scale, log2 domain
 //     P = 2^(w - M) as f16,  l += P / vs,  O += P Y     Y the stored values
-// with M the running maximum (raised only when it would grow by 2^8), so a
-// page's value scale vs rides in the exponent and no value is multiplied.
+// with M a reference for the row's maximum, so a page's value scale vs rides in
+// the exponent and no value is multiplied.  M is the maximum of a run's first
+// tile, and stays while a tile's sum of P stays below 2^12: then no P passes
+// f16's range, and no pass over S for its maximum is needed.  A tile whose sum
+// is larger raises M to its maximum, rescales O and l and is taken again (rare).
 // Both products are f16 tcgen05 MMAs: e4m3 -> f16 is exact, queries are scaled
 // into f16's range by a power of two a row (bf16's 8 bits fit f16's 11), and P
 // keeps 2^-11 of its value.  (Products of e4m3 operands would need queries and
@@ -18,17 +21,13 @@
 // when a row group has at most 128 rows, one M tile with even tiles on one
 // stream and odd tiles on the other (two partial results).  While one stream's
 // softmax runs, the tensor core works for the other; a converted tile serves
-// both M tiles.  Warp roles (768 threads):
+// both M tiles.  Warp roles (512 threads):
 //   warp 0       loader: bulk copies of page chunks to shared memory, page
 //                tables and scales
 //   warp 1       MMA issuer          warp 2   TMEM allocator
 //   warps 4-7    e4m3 -> f16 into the MMA's 128-byte-swizzled layout
-//   warps 8-23   softmax, eight a stream: a thread takes 64 of a row's 128 keys and
-//                shares its maximum with the one that has the others; queries to
-//                f16; partial results
-// TMEM: O_0 | O_1 | S_0 | S_1, P over the first 32 columns of each half of its S.
-// Bound: the latency of the softmax warps' instruction stream, not a pipe; with
-// one thread a row (eight warps, 128 keys) a tile took 4750 cycles.
+//   warps 8-15   softmax, one thread a row; queries to f16; partial results
+// TMEM: O_0 | O_1 | S_0 | S_1, P over the first 64 columns of its S.
 //
 // Every wait is bounded: on expiry the kernel sets PP_DEV_TIMEOUT, raises a
 // CTA-wide abort flag, drains its own copies and MMAs (bounded), frees TMEM
@@ -41,15 +40,12 @@
 namespace pp {
 namespace {
 
-// Register split: launched with 80 a thread (768 * 80 = 61440); the control
-// warps drop to 56, the converters to 72, the softmax warps rise to 88.
-constexpr int kThreads8 = 768;
-constexpr int kRegs8 = 80, kRegsCtl = 56, kRegsConv = 72, kRegsSoft = 88;
-static_assert(128 * kRegsCtl + 128 * kRegsConv + 512 * kRegsSoft <= kThreads8 * kRegs8,
+// Register split: launched with 128 a thread (512 * 128 = 65536); the control
+// warps drop to 56, the converters to 72, the softmax warps rise to 192.
+constexpr int kThreads8 = 512;
+constexpr int kRegs8 = 128, kRegsCtl = 56, kRegsConv = 72, kRegsSoft = 192;
+static_assert(128 * kRegsCtl + 128 * kRegsConv + 256 * kRegsSoft <= kThreads8 * kRegs8,
               "register split");
-#ifndef POLY
-#define POLY(i) use_poly(i)
-#endif
 // Tiles of page scales kept (the loader runs at most 6 ahead of the softmax):
 // for every 16 keys the key scale and the value scale's logarithm, -inf where
 // there are no keys; [8]: whether any of the tile's keys are not there.
@@ -81,11 +77,11 @@ struct Cfg8 {
   static constexpr int OFF_F = 2 * TILE;
   static constexpr int OFF_R = OFF_F + NF * TILE;
   static constexpr int OFF_INFO = OFF_R + NR * RAW;
-  static constexpr int OFF_SHARE = OFF_INFO + kInfo * kInfoLd * 8;
-  static constexpr int OFF_BAR = OFF_SHARE + 2 * 2 * 128 * 4;
+  static constexpr int OFF_SCALE = OFF_INFO + kInfo * kInfoLd * 8;
+  static constexpr int OFF_BAR = OFF_SCALE + 2 * 128 * 4;
   // raw_full[NR], raw_empty[NR], f_full[NF], f_empty[NF], q_full[2], s_full[2],
-  // p_full[2], o_done[2], pair[8], drain
-  static constexpr int NBAR = 2 * NR + 2 * NF + 17;
+  // p_full[2], o_done[2], drain
+  static constexpr int NBAR = 2 * NR + 2 * NF + 9;
   static constexpr int USED = OFF_BAR + NBAR * 8 + 8;   // TMEM base and abort flag last
   // at least 120 KB so one CTA owns an SM's TMEM
   static constexpr int SMEM = USED > 120 * 1024 ? USED : 120 * 1024;
@@ -122,13 +118,6 @@ __device__ __forceinline__ bool next_seg8(const Doc8Params& p, int64_t& t, int64
 __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
   __syncwarp();
   if (lane == 0) mbar_arrive(bar);
-}
-
-// max of three, NaN if any is NaN
-__device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
-  float d;
-  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
 }
 
 // 16-byte unit c of row r in a tile of 128-byte-swizzled rows of 64 f16.
@@ -191,6 +180,7 @@ __device__ __forceinline__ void load_queries(const Doc8Params& p, uint8_t* tile,
     *unit_at(tile, r, c0 + i) = make_uint4(b[0], b[1], b[2], b[3]);
   }
   if (lane < 16) scale[r] = __uint_as_float((uint32_t)(e + 127) << 23) * p.sl2;
+  __syncwarp();
 }
 
 template <int D>
@@ -212,9 +202,8 @@ __global__ void __maxnreg__(kRegs8) kv8_doc_tc(const Doc8Params p) {
   uint64_t* s_full = q_full + 2;
   uint64_t* p_full = s_full + 2;
   uint64_t* o_done = p_full + 2;
-  uint64_t* pair = o_done + 2;   // two warps that share rows
-  uint64_t* drain = pair + 8;
-  float(*share)[2][128] = reinterpret_cast<float(*)[2][128]>(smem + C::OFF_SHARE);  // [stream][half][row]
+  uint64_t* drain = o_done + 2;
+  float* scale = reinterpret_cast<float*>(smem + C::OFF_SCALE);   // [stream][row]
   float2* info = reinterpret_cast<float2*>(smem + C::OFF_INFO);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -233,12 +222,11 @@ __global__ void __maxnreg__(kRegs8) kv8_doc_tc(const Doc8Params p) {
       mbar_init(f_empty + i, 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(q_full + i, 8);
+      mbar_init(q_full + i, 4);
       mbar_init(s_full + i, 1);
-      mbar_init(p_full + i, 8);
+      mbar_init(p_full + i, 4);
       mbar_init(o_done + i, 1);
     }
-    for (int i = 0; i < 8; ++i) mbar_init(pair + i, 2);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -362,7 +350,7 @@ __global__ void __maxnreg__(kRegs8) kv8_doc_tc(const Doc8Params p) {
       const uint64_t b0 = dV + (uint64_t)((slot * C::TILE) >> 4);
 #pragma unroll
       for (int kk = 0; kk < kBN / 16; ++kk)
-        mma_ts_if(on, d_t, a_t + (kk & 3) * 8 + (kk >> 2) * (kBN / 2), b0 + (uint64_t)((kk * 16 * 128) >> 4), IDESC_PV,
+        mma_ts_if(on, d_t, a_t + kk * 8, b0 + (uint64_t)((kk * 16 * 128) >> 4), IDESC_PV,
                   (acc || kk > 0) ? 1u : 0u);
     };
     auto commit = [&](uint64_t* b) { tc_commit_if(on, b); };
@@ -485,24 +473,13 @@ __global__ void __maxnreg__(kRegs8) kv8_doc_tc(const Doc8Params p) {
   } else {
     // ----------------------------------------------------------- softmax ----
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
-    const int st = (warp - 8) >> 3, half = ((warp - 8) >> 2) & 1;
+    const int st = (warp - 8) >> 2;
     const int wq = warp & 3;                 // TMEM lane quarter of this warp
     const int rt = wq * 32 + lane;           // row of the M tile
     const uint32_t t_lane = tmem + ((uint32_t)(wq * 32) << 16);
-    const uint32_t t_S = t_lane + C::T_S + (uint32_t)(st * kBN + half * (kBN / 2));
-    const uint32_t t_O = t_lane + (uint32_t)(st * D + half * (D / 2));   // this half's share of O
+    const uint32_t t_S = t_lane + C::T_S + (uint32_t)(st * kBN);
+    const uint32_t t_O = t_lane + (uint32_t)(st * D);
     uint8_t* tq = smem + st * C::TILE;
-    uint64_t* pb = pair + st * 4 + wq;
-    uint32_t pr_ph = 0;
-    // x of the thread that has the row's other keys
-    auto swap_half = [&](float x, float& other) -> bool {
-      share[st][half][rt] = x;
-      warp_arrive(pb, lane);
-      const bool got = warp_wait(pb, pr_ph, abort_flag, p.wait_limit, status);
-      pr_ph ^= 1;
-      other = share[st][half ^ 1][rt];
-      return got;
-    };
     int64_t t = t_begin;
     Seg8 s;
     uint32_t s_ph = 0, od_ph = 0;
@@ -512,112 +489,123 @@ __global__ void __maxnreg__(kRegs8) kv8_doc_tc(const Doc8Params p) {
       const int step = s.two ? 1 : 2, first = s.two ? 0 : st;
       const int row = s.gi * kGroupRows + (s.two ? st * 128 : 0) + rt;
       // (the previous run's last S has been seen: no MMA reads this tile of Q any more)
-      load_queries<D>(p, tq, &share[st][0][0], wq * 32 + half * 16, row - lane + half * 16, s.h, lane);
+#pragma unroll 1
+      for (int i = 0; i < 32; i += 16)
+        load_queries<D>(p, tq, scale + st * 128, wq * 32 + i, row - lane + i, s.h, lane);
       fence_proxy_async();
       warp_arrive(q_full + st, lane);
-      warp_arrive(pb, lane);
-      if (!(ok = warp_wait(pb, pr_ph, abort_flag, p.wait_limit, status))) break;
-      pr_ph ^= 1;
-      const float qs = share[st][0][rt];
-      // (both have read the scales before one writes over them: a swap's value is
-      // read by the other warp before this one passes its next barrier)
-      warp_arrive(pb, lane);
-      if (!(ok = warp_wait(pb, pr_ph, abort_flag, p.wait_limit, status))) break;
-      pr_ph ^= 1;
-      float m = -INFINITY, l = 0.f;
+      const float qs = scale[st * 128 + rt];
+      float m = 0.f, l = 0.f;
+      bool none = true;                        // no key so far
       for (int tile = first; tile < s.n; tile += step) {
+        const float2* inf = info + ((t0 + tile) % kInfo) * kInfoLd;
         if (!(ok = warp_wait(s_full + st, s_ph, abort_flag, p.wait_limit, status))) break;
         s_ph ^= 1;
-        const float2* inf = info + ((t0 + tile) % kInfo) * kInfoLd + half * 4;
         tc_fence_after();
-        // Two passes over S in TMEM, 32 columns at a time: the maximum, then the
-        // exponentials.
-        const int kvalid = p.doc_len - (s.j0 + tile) * kBN - half * (kBN / 2);
-        auto load32 = [&](uint32_t (&x)[32], int c) {
-          tmem_ld32(t_S + c * 32, x);
-          tmem_ld_wait();
-          if (kvalid < kBN / 2) {
+        const int kvalid = p.doc_len - (s.j0 + tile) * kBN;
+        auto mask = [&](uint32_t (&x)[32], int c) {
+          if (kvalid < kBN) {
 #pragma unroll
             for (int e = 0; e < 32; ++e)
               if (c * 32 + e >= kvalid) x[e] = __float_as_uint(-INFINITY);
           }
         };
-        float mx = -INFINITY;
+        // the row's maximum of w
+        auto maximum = [&]() {
+          float mx = -INFINITY;
 #pragma unroll 1
-        for (int c = 0; c < 2; ++c) {
-          uint32_t x[32];
-          load32(x, c);
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const float2 in = inf[c * 2 + q];
-            auto f = [&](int i) { return __uint_as_float(x[q * 16 + i]); };
-            float y0 = fmax3_nan(f(0), f(1), f(2)), y1 = fmax3_nan(f(3), f(4), f(5));
-            float y2 = fmax3_nan(f(6), f(7), f(8)), y3 = fmax3_nan(f(9), f(10), f(11));
-            y0 = fmax3_nan(y0, f(12), f(13));
-            y1 = fmax3_nan(y1, f(14), f(15));
-            y0 = fmax3_nan(y0, y1, y2);
-            const float z = fmaf(fmax3_nan(y0, y3, y3), in.x * qs, in.y);
-            mx = fmax3_nan(mx, z, z);
-          }
-        }
-        float mo;
-        if (!(ok = swap_half(mx, mo))) break;
-        mx = fmax3_nan(mx, mo, mo);
-        const float m_new = fmaxf(m, mx);      // (a NaN leaves m and spoils l below)
-        // Lazy rescale: keep a stale maximum unless the new one exceeds it by
-        // more than 2^8 (probabilities then stay below 256).
-        const bool need = m_new > m + 8.f;
-        const float m_old = m;
-        if (need) {
-          l *= ex2_mufu(m - m_new);
-          m = m_new;
-        }
-        const float mneg = m == -INFINITY ? 0.f : -m;
-#pragma unroll 1
-        for (int c = 0; c < 2; ++c) {
-          uint32_t x[32], pk[16];
-          load32(x, c);
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const float2 in = inf[c * 2 + q];
-            const float a = in.x * qs, b = in.y + mneg;
-            const float rv = in.y == -INFINITY ? 0.f : ex2_mufu(-in.y);   // 1 / value scale
-            const float2 av = make_float2(a, a), bv = make_float2(b, b);
-            float2 rs[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-            for (int e = 0; e < 16; e += 2) {
-              const float2 w = ffma2(make_float2(__uint_as_float(x[q * 16 + e]),
-                                                 __uint_as_float(x[q * 16 + e + 1])), av, bv);
-              float2 pv;
-              if (POLY(q * 8 + (e >> 1))) {
-                pv = ex2_poly2(w);
-              } else {
-                pv.x = ex2_mufu(w.x);
-                pv.y = ex2_mufu(w.y);
-              }
-              rs[(e >> 1) & 1] = fadd2(rs[(e >> 1) & 1], pv);
-              pk[q * 8 + (e >> 1)] = f2_to_h2(pv.x, pv.y);
-            }
-            const float2 r2 = fadd2(rs[0], rs[1]);
-            l = fmaf(r2.x + r2.y, rv, l);
-          }
-          tmem_st16(t_S + c * 16, pk);   // over columns that have been read
-        }
-        if (mx != mx) l = mx;
-        // O rescale for rows whose maximum moved (rare).  The product of this
-        // stream's tile before is complete: it was issued ahead of this S.
-        if (tile > first && __any_sync(0xffffffffu, need)) {
-          const float f = need ? ex2_mufu(m_old - m) : 1.f;
-#pragma unroll 1
-          for (int c = 0; c < D / 64; ++c) {
-            uint32_t o[32];
-            tmem_ld32(t_O + c * 32, o);
+          for (int c = 0; c < 4; ++c) {
+            uint32_t x[32];
+            tmem_ld32(t_S + c * 32, x);
             tmem_ld_wait();
+            mask(x, c);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-            tmem_st32(t_O + c * 32, o);
+            for (int q = 0; q < 2; ++q) {
+              const float2 in = inf[c * 2 + q];
+              float y = __uint_as_float(x[q * 16]);
+#pragma unroll
+              for (int e = 1; e < 16; ++e) y = fmaxf(y, __uint_as_float(x[q * 16 + e]));
+              mx = fmaxf(mx, fmaf(y, in.x * qs, in.y));
+            }
           }
+          return mx;
+        };
+        uint32_t pk[64];
+        float lt, sum;
+        // P of the tile, its sum, and the sum over the value scales
+        auto exponentials = [&]() {
+          lt = sum = 0.f;
+          uint32_t r[2][32];
+          tmem_ld32(t_S, r[0]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            tmem_ld_wait();
+            if (c < 3) tmem_ld32(t_S + (c + 1) * 32, r[(c + 1) & 1]);
+            uint32_t (&x)[32] = r[c & 1];
+            mask(x, c);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const float2 in = inf[c * 2 + q];
+              const float a = in.x * qs, b = in.y - m;
+              const float rv = in.y == -INFINITY ? 0.f : ex2_mufu(-in.y);   // 1 / value scale
+              const float2 av = make_float2(a, a), bv = make_float2(b, b);
+              float2 rs[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+              for (int e = 0; e < 16; e += 2) {
+                const float2 w = ffma2(make_float2(__uint_as_float(x[q * 16 + e]),
+                                                   __uint_as_float(x[q * 16 + e + 1])), av, bv);
+                // a quarter on the FMA pipe: MUFU alone took 104 us where this takes
+                // 88 (256 rows, 32 heads, 16384 keys), 2 in 5 the same 88
+                const float2 pv = (e >> 1) % 4 == 2 ? ex2_poly2_nan(w)
+                                                    : make_float2(ex2_mufu(w.x), ex2_mufu(w.y));
+                rs[(e >> 1) & 1] = fadd2(rs[(e >> 1) & 1], pv);
+                pk[c * 16 + q * 8 + (e >> 1)] = f2_to_h2(pv.x, pv.y);
+              }
+              const float2 r2 = fadd2(rs[0], rs[1]);
+              const float r1 = r2.x + r2.y;
+              sum += r1;
+              lt = fmaf(r1, rv, lt);
+            }
+          }
+        };
+        // Rows without a reference yet, or whose sum says that it is too low, take
+        // their maximum first (the warp does, for all its rows; the others keep
+        // theirs).  The product of this stream's tile before is complete: it was
+        // issued ahead of this S.
+        sum = 0.f;
+        bool raise = __any_sync(0xffffffffu, none);
+        for (int tries = 0;; ++tries) {
+          if (raise) {
+            const float mx = maximum();
+            const bool move = none ? mx != -INFINITY : sum > 4096.f;
+            const float f = !move ? 1.f : none ? 0.f : ex2_mufu(m - mx);
+            if (move) {
+              m = mx;
+              l *= f;
+              none = false;
+            }
+            if (tile > first) {
+#pragma unroll 1
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                tmem_ld32(t_O + c * 32, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tmem_st32(t_O + c * 32, o);
+              }
+            }
+          }
+          exponentials();
+          if (tries == 2 || !__any_sync(0xffffffffu, sum > 4096.f)) break;
+          raise = true;
         }
+        // A NaN score: the sum is NaN, or, from the polynomial, still huge.
+        if (sum > 4096.f || sum != sum) lt = __int_as_float(0x7fffffff);
+        none = none && lt == lt;
+        l += lt;
+        tmem_st32(t_S, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
+        tmem_st32(t_S + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
         tmem_st_wait();
         tc_fence_before();
         warp_arrive(p_full + st, lane);
@@ -628,47 +616,33 @@ __global__ void __maxnreg__(kRegs8) kv8_doc_tc(const Doc8Params p) {
         if (!(ok = warp_wait(o_done + st, od_ph, abort_flag, p.wait_limit, status))) break;
         od_ph ^= 1;
         tc_fence_after();
-        // through the rows' place in the query tile (a box of it, or half of each
-        // row, for each half), so that rows go out in whole sectors
-        constexpr int U = D / 16, RP = 32 / U;
-        float* dst = p.doc_o + (prow - lane) * D + half * (D / 2);
+        // through the rows' place in the query tile, so that rows go out in whole
+        // sectors
+        float* dst = p.doc_o + (prow - lane) * D;
         const int n_rows = p.rows - (row - lane);
 #pragma unroll 1
-        for (int c = 0; c < D / 64; ++c) {
+        for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
           tmem_ld32(t_O + c * 32, o);
           tmem_ld_wait();
 #pragma unroll
-          for (int k = 0; k < 8 / U; ++k) {
+          for (int e = 0; e < 8; ++e)
+            *unit_at(tq, rt, e) = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          __syncwarp();
+          uint4 w[8];
 #pragma unroll
-            for (int e = 0; e < U; ++e) {
-              const int i = 4 * (k * U + e);
-              *unit_at(tq, rt, half * U + e) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
-            }
-            __syncwarp();
-            uint4 w[RP == 4 ? 8 : 4];
+          for (int i = 0; i < 8; ++i) w[i] = *unit_at(tq, wq * 32 + i * 4 + (lane >> 3), lane & 7);
 #pragma unroll
-            for (int i = 0; i < 32 / RP; ++i)
-              w[i] = *unit_at(tq, wq * 32 + i * RP + lane / U, half * U + lane % U);
-#pragma unroll
-            for (int i = 0; i < 32 / RP; ++i)
-              if (i * RP + lane / U < n_rows)
-                *reinterpret_cast<uint4*>(dst + (i * RP + lane / U) * D + c * 32 + k * U * 4 +
-                                          (lane % U) * 4) = w[i];
-            __syncwarp();
-          }
+          for (int i = 0; i < 8; ++i)
+            if (i * 4 + (lane >> 3) < n_rows)
+              *reinterpret_cast<uint4*>(dst + (i * 4 + (lane >> 3)) * D + c * 32 + (lane & 7) * 4) = w[i];
+          __syncwarp();
         }
         tc_fence_before();
       }
-      float lo;
-      if (!(ok = swap_half(l, lo))) break;
-      l = half == 0 ? l + lo : lo + l;
       // a NaN row keeps a finite maximum so that the merge does not skip it
-      if (half == 0 && row < p.rows)
-        reinterpret_cast<float2*>(p.doc_ml)[prow] = make_float2(l != l && m == -INFINITY ? 0.f : m, l);
-      warp_arrive(pb, lane);     // lo is read: the next run's scales may go over it
-      if (!(ok = warp_wait(pb, pr_ph, abort_flag, p.wait_limit, status))) break;
-      pr_ph ^= 1;
+      if (row < p.rows)
+        reinterpret_cast<float2*>(p.doc_ml)[prow] = make_float2(none ? -INFINITY : m, l);
       t0 += s.n;
     }
   }
