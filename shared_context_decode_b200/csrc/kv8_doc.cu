@@ -498,18 +498,24 @@ __global__ void __maxnreg__(kRegs8) kv8_doc_tc(const Doc8Params p) {
       float m = 0.f, l = 0.f;
       bool none = true;                        // no key so far
       for (int tile = first; tile < s.n; tile += step) {
-        const float2* inf = info + ((t0 + tile) % kInfo) * kInfoLd;
         if (!(ok = warp_wait(s_full + st, s_ph, abort_flag, p.wait_limit, status))) break;
         s_ph ^= 1;
+        const float2* inf = info + ((t0 + tile) % kInfo) * kInfoLd;
         tc_fence_after();
         const int kvalid = p.doc_len - (s.j0 + tile) * kBN;
-        auto mask = [&](uint32_t (&x)[32], int c) {
-          if (kvalid < kBN) {
+        if (kvalid < kBN) {              // the document's last tile: hide what is behind it
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t x[32];
+            tmem_ld32(t_S + c * 32, x);
+            tmem_ld_wait();
 #pragma unroll
             for (int e = 0; e < 32; ++e)
               if (c * 32 + e >= kvalid) x[e] = __float_as_uint(-INFINITY);
+            tmem_st32(t_S + c * 32, x);
           }
-        };
+          tmem_st_wait();
+        }
         // the row's maximum of w
         auto maximum = [&]() {
           float mx = -INFINITY;
@@ -518,7 +524,6 @@ __global__ void __maxnreg__(kRegs8) kv8_doc_tc(const Doc8Params p) {
             uint32_t x[32];
             tmem_ld32(t_S + c * 32, x);
             tmem_ld_wait();
-            mask(x, c);
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
               const float2 in = inf[c * 2 + q];
@@ -536,18 +541,23 @@ __global__ void __maxnreg__(kRegs8) kv8_doc_tc(const Doc8Params p) {
         auto exponentials = [&]() {
           lt = sum = 0.f;
           uint32_t r[2][32];
+          float2 in[2][2];                 // scales of 2 x 16 keys, and of the next
+          in[0][0] = inf[0];
+          in[0][1] = inf[1];
           tmem_ld32(t_S, r[0]);
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             tmem_ld_wait();
-            if (c < 3) tmem_ld32(t_S + (c + 1) * 32, r[(c + 1) & 1]);
+            if (c < 3) {
+              tmem_ld32(t_S + (c + 1) * 32, r[(c + 1) & 1]);
+              in[(c + 1) & 1][0] = inf[c * 2 + 2];
+              in[(c + 1) & 1][1] = inf[c * 2 + 3];
+            }
             uint32_t (&x)[32] = r[c & 1];
-            mask(x, c);
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-              const float2 in = inf[c * 2 + q];
-              const float a = in.x * qs, b = in.y - m;
-              const float rv = in.y == -INFINITY ? 0.f : ex2_mufu(-in.y);   // 1 / value scale
+              const float a = in[c & 1][q].x * qs, g = in[c & 1][q].y, b = g - m;
+              const float rv = g == -INFINITY ? 0.f : ex2_mufu(-g);   // 1 / value scale
               const float2 av = make_float2(a, a), bv = make_float2(b, b);
               float2 rs[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
