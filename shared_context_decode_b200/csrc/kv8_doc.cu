@@ -36,6 +36,7 @@
 
 #include "kv8.cuh"
 #include "internal.h"
+#include "warp_mma.cuh"
 
 namespace pp {
 namespace {
@@ -59,6 +60,7 @@ struct Doc8Params {
   int rows;     // (query row, query head) pairs of a key head
   int doc_len;
   SplitPlan plan;
+  int tiles;    // plan.W
   float sl2;
   float* doc_o;
   float* doc_ml;
@@ -77,8 +79,7 @@ struct Cfg8 {
   static constexpr int OFF_F = 2 * TILE;
   static constexpr int OFF_R = OFF_F + NF * TILE;
   static constexpr int OFF_INFO = OFF_R + NR * RAW;
-  static constexpr int OFF_SCALE = OFF_INFO + kInfo * kInfoLd * 8;
-  static constexpr int OFF_BAR = OFF_SCALE + 2 * 128 * 4;
+  static constexpr int OFF_BAR = OFF_INFO + kInfo * kInfoLd * 8;
   // raw_full[NR], raw_empty[NR], f_full[NF], f_empty[NF], q_full[2], s_full[2],
   // p_full[2], o_done[2], drain
   static constexpr int NBAR = 2 * NR + 2 * NF + 9;
@@ -90,25 +91,42 @@ struct Cfg8 {
   static_assert(T_S + 2 * kBN <= TMEM_COLS, "TMEM budget");
 };
 
-// A run of tiles of one (key head, row group).
+// A run of tiles of one unit, (key head, row group).  Tiles are counted in 32
+// bits (the host sees to it), and only a CTA's first run divides: 64-bit
+// divisions at every role's start took 3600 cycles.
 struct Seg8 {
-  int u, h, gi, j0, n, chunk;
+  int u, h, gi, j0, n;
   bool two;     // two M tiles; else one, its tiles dealt out to the streams
 };
-__device__ __forceinline__ bool next_seg8(const Doc8Params& p, int64_t& t, int64_t t_end, int cta,
-                                          Seg8& s) {
-  if (t >= t_end) return false;
-  int j;
-  plan_locate(p.plan, t, s.u, j);
-  s.h = s.u / p.plan.G;
-  s.gi = s.u - s.h * p.plan.G;
-  const int64_t ub = plan_unit_begin(p.plan, s.u);
-  const int64_t ue = ub + p.plan.T;
-  s.j0 = j;
-  s.n = (int)((ue < t_end ? ue : t_end) - t);
-  s.chunk = cta - plan_cta_of(p.plan, ub);
+struct Runs8 {
+  int t, t_end, u, h, gi;
+};
+__device__ __forceinline__ Runs8 first_run8(const Doc8Params& p, int cta) {
+  Runs8 r;
+  const int q = p.tiles / p.plan.C, m = p.tiles - q * p.plan.C;   // floor(cta W / C)
+  r.t = cta * q + cta * m / p.plan.C;
+  r.t_end = (cta + 1) * q + (cta + 1) * m / p.plan.C;
+  r.u = r.t / p.plan.T;
+  r.h = r.u / p.plan.G;
+  r.gi = r.u - r.h * p.plan.G;
+  return r;
+}
+__device__ __forceinline__ bool next_seg8(const Doc8Params& p, Runs8& r, Seg8& s) {
+  if (r.t >= r.t_end) return false;
+  s.u = r.u;
+  s.h = r.h;
+  s.gi = r.gi;
+  s.j0 = r.t - r.u * p.plan.T;
+  s.n = min(p.plan.T - s.j0, r.t_end - r.t);
   s.two = p.rows - s.gi * kGroupRows > 128;
-  t += s.n;
+  r.t += s.n;
+  if (s.j0 + s.n == p.plan.T) {
+    ++r.u;
+    if (++r.gi == p.plan.G) {
+      r.gi = 0;
+      ++r.h;
+    }
+  }
   return true;
 }
 
@@ -125,34 +143,30 @@ __device__ __forceinline__ uint4* unit_at(uint8_t* tile, int r, int c) {
   return reinterpret_cast<uint4*>(tile + (c >> 3) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
 
-// Sixteen rows of queries (from pair `row0` on) to f16 in rows r0 .. r0 + 15 of
-// the swizzled tile; scale[r]: the power of two row r stands for, times sl2.  The
-// rows come in coalesced through their own place in the tile, then two lanes
-// take a row.  A NaN or infinity becomes NaN.
+// A warp's 32 rows of queries (from pair `row0` on) to f16 in rows r0 .. r0 + 31
+// of the swizzled tile, each a power of two smaller; returns that of the lane's
+// row.  The rows come in whole, through their own place in the tile.  A NaN or
+// infinity becomes NaN.
 template <int D>
-__device__ __forceinline__ void load_queries(const Doc8Params& p, uint8_t* tile, float* scale,
-                                             int r0, int row0, int h, int lane) {
-  constexpr int U = D / 8, RP = 32 / U, B = 16 / RP;   // units a row, rows a pass, passes
+__device__ __forceinline__ float load_queries(const Doc8Params& p, uint8_t* tile, int r0, int row0,
+                                              int h, int lane) {
+  constexpr int U = D / 8, RP = 32 / U;   // units a row, rows a pass
   const uint16_t* head = p.q + (int64_t)h * p.g * D + (lane % U) * 8;
-  uint4 w[B];
-#pragma unroll
-  for (int i = 0; i < B; ++i) {
-    const int row = row0 + i * RP + lane / U;
-    w[i] = make_uint4(0, 0, 0, 0);
-    if (row < p.rows) {
-      const int qr = p.g == 1 ? row : row / p.g;
-      w[i] = __ldg(reinterpret_cast<const uint4*>(head + (int64_t)qr * p.q_ld +
-                                                  (int64_t)(row - qr * p.g) * D));
-    }
+#pragma unroll 4
+  for (int i = 0; i < 32; i += RP) {
+    const int row = row0 + i + lane / U;
+    const int at = row < p.rows ? row : 0;
+    const int qr = p.g == 1 ? at : at / p.g;
+    cp_async16(smem_u32(unit_at(tile, r0 + i + lane / U, lane % U)),
+               head + (int64_t)qr * p.q_ld + (int64_t)(at - qr * p.g) * D, row < p.rows ? 16 : 0);
   }
-#pragma unroll
-  for (int i = 0; i < B; ++i) *unit_at(tile, r0 + i * RP + lane / U, lane % U) = w[i];
+  cp_async_wait_all();
   __syncwarp();
-  const int r = r0 + (lane & 15), c0 = (lane >> 4) * (U / 2);
+  const int r = r0 + lane;
   float am = 0.f;
-#pragma unroll 2
-  for (int i = 0; i < U / 2; ++i) {
-    const uint4 x = *unit_at(tile, r, c0 + i);
+#pragma unroll 4
+  for (int i = 0; i < U; ++i) {
+    const uint4 x = *unit_at(tile, r, i);
     const uint32_t a[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -161,15 +175,14 @@ __device__ __forceinline__ void load_queries(const Doc8Params& p, uint8_t* tile,
       am = fmaxf(am, fabsf(f.y) < INFINITY ? fabsf(f.y) : 0.f);
     }
   }
-  am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 16));
   // 2^e with am / 2^e in [2^13, 2^14): bf16's 8 bits are exact in f16 down to
   // 2^-30 of the row's largest value
   int e = (int)(__float_as_uint(am) >> 23) - 127 - 13;
   e = e < -100 ? -100 : e;
   const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
-#pragma unroll 2
-  for (int i = 0; i < U / 2; ++i) {
-    const uint4 x = *unit_at(tile, r, c0 + i);
+#pragma unroll 4
+  for (int i = 0; i < U; ++i) {
+    const uint4 x = *unit_at(tile, r, i);
     const uint32_t a[4] = {x.x, x.y, x.z, x.w};
     uint32_t b[4];
 #pragma unroll
@@ -177,10 +190,9 @@ __device__ __forceinline__ void load_queries(const Doc8Params& p, uint8_t* tile,
       const float2 f = bf2_to_f2(a[j]);   // f - f is 0, or NaN where f is not finite
       b[j] = f2_to_h2((f.x + (f.x - f.x)) * inv, (f.y + (f.y - f.y)) * inv);
     }
-    *unit_at(tile, r, c0 + i) = make_uint4(b[0], b[1], b[2], b[3]);
+    *unit_at(tile, r, i) = make_uint4(b[0], b[1], b[2], b[3]);
   }
-  if (lane < 16) scale[r] = __uint_as_float((uint32_t)(e + 127) << 23) * p.sl2;
-  __syncwarp();
+  return __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
 template <int D>
@@ -203,13 +215,11 @@ __global__ void __maxnreg__(kRegs8) kv8_doc_tc(const Doc8Params p) {
   uint64_t* p_full = s_full + 2;
   uint64_t* o_done = p_full + 2;
   uint64_t* drain = o_done + 2;
-  float* scale = reinterpret_cast<float*>(smem + C::OFF_SCALE);   // [stream][row]
   float2* info = reinterpret_cast<float2*>(smem + C::OFF_INFO);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cta = blockIdx.x;
-  const int64_t t_begin = plan_tile_begin(p.plan, cta);
-  const int64_t t_end = plan_tile_begin(p.plan, cta + 1);
+  const Runs8 runs = first_run8(p, cta);
   int32_t* status = p.L.status;
 
   if (threadIdx.x == 0) {
@@ -246,7 +256,7 @@ __global__ void __maxnreg__(kRegs8) kv8_doc_tc(const Doc8Params p) {
     const int page = p.L.page, ppt = kBN / page;   // pages per tile
     const int groups = page >> 4;
     const int per = 32 / ppt;                      // tiles per batch of 32 pages, a lane each
-    int64_t t = t_begin;
+    Runs8 t = runs;
     Seg8 s;
     int ht = 0, kt = 0;
     bool ok = true;
@@ -263,7 +273,7 @@ __global__ void __maxnreg__(kRegs8) kv8_doc_tc(const Doc8Params p) {
         vs = p.L.v_scale[(int64_t)pg * p.L.H + h];
       }
     };
-    while (ok && next_seg8(p, t, t_end, cta, s)) {
+    while (ok && next_seg8(p, t, s)) {
       int b = s.j0 / per;
       int pg0 = page_of(entry(b), p.L.n_pages), e1 = entry(b + 1);
       float ks0, vs0, ks1, vs1;
@@ -357,12 +367,12 @@ __global__ void __maxnreg__(kRegs8) kv8_doc_tc(const Doc8Params p) {
     auto wait_f = [&](int half) {
       return warp_wait(f_full + half % C::NF, (half / C::NF) & 1, abort_flag, p.wait_limit, status);
     };
-    int64_t t = t_begin;
+    Runs8 t = runs;
     Seg8 s;
     int t0 = 0, nseg = 0;
     uint32_t pf_ph = 0;
     bool ok = true;
-    while (ok && next_seg8(p, t, t_end, cta, s)) {
+    while (ok && next_seg8(p, t, s)) {
       const int step = s.two ? 1 : 2;
       for (int st = 0; ok && st < 2; ++st) {
         if (!(ok = warp_wait(q_full + st, nseg & 1, abort_flag, p.wait_limit, status))) break;
@@ -426,11 +436,11 @@ __global__ void __maxnreg__(kRegs8) kv8_doc_tc(const Doc8Params p) {
     const int ua = (u & 3) * 2;
     const int dst0 = (u >> 2) * C::BOX + r0 * 128 + ((ua ^ (r0 & 7)) << 4);
     const int dst1 = (u >> 2) * C::BOX + r0 * 128 + (((ua + 1) ^ (r0 & 7)) << 4);
-    int64_t t = t_begin;
+    Runs8 t = runs;
     Seg8 s;
     int ht = 0, kt = 0;
     bool ok = true;
-    while (ok && next_seg8(p, t, t_end, cta, s)) {
+    while (ok && next_seg8(p, t, s)) {
       for (int j = 0; ok && j < s.n; ++j, ++kt) {
         for (int kv = 0; kv < 2; ++kv, ++ht) {
           const int sr = ht % C::NR, sf = ht % C::NF;
@@ -480,21 +490,18 @@ __global__ void __maxnreg__(kRegs8) kv8_doc_tc(const Doc8Params p) {
     const uint32_t t_S = t_lane + C::T_S + (uint32_t)(st * kBN);
     const uint32_t t_O = t_lane + (uint32_t)(st * D);
     uint8_t* tq = smem + st * C::TILE;
-    int64_t t = t_begin;
+    Runs8 t = runs;
     Seg8 s;
     uint32_t s_ph = 0, od_ph = 0;
     int t0 = 0;
     bool ok = true;
-    while (ok && next_seg8(p, t, t_end, cta, s)) {
+    while (ok && next_seg8(p, t, s)) {
       const int step = s.two ? 1 : 2, first = s.two ? 0 : st;
       const int row = s.gi * kGroupRows + (s.two ? st * 128 : 0) + rt;
       // (the previous run's last S has been seen: no MMA reads this tile of Q any more)
-#pragma unroll 1
-      for (int i = 0; i < 32; i += 16)
-        load_queries<D>(p, tq, scale + st * 128, wq * 32 + i, row - lane + i, s.h, lane);
+      const float qs = load_queries<D>(p, tq, wq * 32, row - lane, s.h, lane) * p.sl2;
       fence_proxy_async();
       warp_arrive(q_full + st, lane);
-      const float qs = scale[st * 128 + rt];
       float m = 0.f, l = 0.f;
       bool none = true;                        // no key so far
       for (int tile = first; tile < s.n; tile += step) {
@@ -621,7 +628,9 @@ __global__ void __maxnreg__(kRegs8) kv8_doc_tc(const Doc8Params p) {
         warp_arrive(p_full + st, lane);
       }
       if (!ok) break;
-      const int64_t prow = ((int64_t)s.u * p.plan.max_chunks + s.chunk) * kGroupRows + st * 128 + rt;
+      // partial of this run: the unit's first CTA has chunk 0
+      const int chunk = s.j0 == 0 ? 0 : cta - plan_cta_of(p.plan, (int64_t)s.u * p.plan.T);
+      const int64_t prow = ((int64_t)s.u * p.plan.max_chunks + chunk) * kGroupRows + st * 128 + rt;
       if (first < s.n) {
         if (!(ok = warp_wait(o_done + st, od_ph, abort_flag, p.wait_limit, status))) break;
         od_ph ^= 1;
@@ -702,6 +711,8 @@ cudaError_t launch_kv8_doc(const pp_kv8_layer& L, int doc_len, const uint16_t* q
   p.rows = rows * p.g;
   p.doc_len = doc_len;
   p.plan = plan;
+  if (plan.W > INT32_MAX) return cudaErrorInvalidValue;
+  p.tiles = (int)plan.W;
   p.sl2 = scale * kLog2e;
   p.doc_o = part.doc_o; p.doc_ml = part.doc_ml;
   p.wait_limit = wait_limit;
