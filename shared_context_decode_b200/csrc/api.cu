@@ -13,6 +13,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "kv8.cuh"
 
 namespace {
 
@@ -319,8 +320,18 @@ SplitPlan kv8_plan(int32_t rows, int32_t Hq, int32_t H, int32_t doc_len, const p
   const int ctas = (opt && opt->splits > 0) ? opt->splits : sm_count();
   const char* e = getenv("PPKV8_DOC");
   const int mode = e ? atoi(e) : 1;
-  if (mode == 0) return SplitPlan{};
-  return make_plan(rows * (Hq / H), H, doc_len, ctas);
+  if (mode == 0 || doc_len == 0) return SplitPlan{};
+  SplitPlan p{};
+  p.T = (doc_len + pp::kBN - 1) / pp::kBN + pp::kKv8Lead;
+  p.G = (rows * (Hq / H) + pp::kGroupRows - 1) / pp::kGroupRows;
+  p.units = p.G * H;
+  p.W = (int64_t)p.units * p.T;
+  p.C = (int32_t)std::min<int64_t>(std::max(ctas, 0), p.W);
+  if (p.C < 1) return SplitPlan{};
+  // a unit's steps lie in at most this many CTAs' ranges of floor(W / C) or one more
+  const int64_t least = p.W / p.C;
+  p.max_chunks = (int32_t)((p.T - 2) / least + 2);
+  return p;
 }
 
 WsLayout kv8_ws_layout(const SplitPlan& p, int d) {

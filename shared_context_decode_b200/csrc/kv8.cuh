@@ -67,10 +67,11 @@ __device__ __forceinline__ int page_of(int32_t entry, int n_pages) {
   return (uint32_t)entry < (uint32_t)n_pages ? entry : -1;
 }
 
-// Doc-pass and merge row of (query row r, query head kvh * g + j): the g query
-// heads of a key head stack as rows, r * g + j.
-struct Kv8Rows {
-  int rows, H, g;
-};
+// The document pass's split plan gives every unit this many steps ahead of its
+// tiles: what a run costs beside them (queries in, partial result out: about
+// 14000 cycles, a tile 3450), so that a CTA whose range meets a unit's border
+// gets fewer tiles.  They hold no tile: the unit's first chunk is that of the
+// CTA of step kKv8Lead.
+constexpr int kKv8Lead = 4;
 
 }  // namespace pp

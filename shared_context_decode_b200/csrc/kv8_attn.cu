@@ -311,7 +311,7 @@ __device__ __forceinline__ DocRow doc_row(const Attn8Params& p, int row, int kvh
   const int64_t ub = plan_unit_begin(p.plan, u);
   DocRow d;
   d.two = (int64_t)p.rows * p.g - pair / kGroupRows * kGroupRows <= 128;
-  d.n = (plan_cta_of(p.plan, ub + p.plan.T - 1) - plan_cta_of(p.plan, ub) + 1) << d.two;
+  d.n = (plan_cta_of(p.plan, ub + p.plan.T - 1) - plan_cta_of(p.plan, ub + kKv8Lead) + 1) << d.two;
   d.slot = (int64_t)u * p.plan.max_chunks * kGroupRows + pair % kGroupRows;
   return d;
 }

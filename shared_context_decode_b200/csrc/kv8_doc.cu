@@ -60,7 +60,7 @@ struct Doc8Params {
   int rows;     // (query row, query head) pairs of a key head
   int doc_len;
   SplitPlan plan;
-  int tiles;    // plan.W
+  int steps;    // plan.W
   float sl2;
   float* doc_o;
   float* doc_ml;
@@ -91,9 +91,10 @@ struct Cfg8 {
   static_assert(T_S + 2 * kBN <= TMEM_COLS, "TMEM budget");
 };
 
-// A run of tiles of one unit, (key head, row group).  Tiles are counted in 32
-// bits (the host sees to it), and only a CTA's first run divides: 64-bit
-// divisions at every role's start took 3600 cycles.
+// A run of tiles of one unit, (key head, row group).  The plan counts steps: a
+// unit's tiles, and kKv8Lead ahead of them for what starting a run costs.  Steps
+// are counted in 32 bits (the host sees to it), and only a CTA's first run
+// divides: 64-bit divisions at every role's start took 3600 cycles.
 struct Seg8 {
   int u, h, gi, j0, n;
   bool two;     // two M tiles; else one, its tiles dealt out to the streams
@@ -103,7 +104,7 @@ struct Runs8 {
 };
 __device__ __forceinline__ Runs8 first_run8(const Doc8Params& p, int cta) {
   Runs8 r;
-  const int q = p.tiles / p.plan.C, m = p.tiles - q * p.plan.C;   // floor(cta W / C)
+  const int q = p.steps / p.plan.C, m = p.steps - q * p.plan.C;   // floor(cta W / C)
   r.t = cta * q + cta * m / p.plan.C;
   r.t_end = (cta + 1) * q + (cta + 1) * m / p.plan.C;
   r.u = r.t / p.plan.T;
@@ -112,22 +113,26 @@ __device__ __forceinline__ Runs8 first_run8(const Doc8Params& p, int cta) {
   return r;
 }
 __device__ __forceinline__ bool next_seg8(const Doc8Params& p, Runs8& r, Seg8& s) {
-  if (r.t >= r.t_end) return false;
-  s.u = r.u;
-  s.h = r.h;
-  s.gi = r.gi;
-  s.j0 = r.t - r.u * p.plan.T;
-  s.n = min(p.plan.T - s.j0, r.t_end - r.t);
-  s.two = p.rows - s.gi * kGroupRows > 128;
-  r.t += s.n;
-  if (s.j0 + s.n == p.plan.T) {
-    ++r.u;
-    if (++r.gi == p.plan.G) {
-      r.gi = 0;
-      ++r.h;
+  while (r.t < r.t_end) {
+    s.u = r.u;
+    s.h = r.h;
+    s.gi = r.gi;
+    s.two = p.rows - s.gi * kGroupRows > 128;
+    const int v = r.t - r.u * p.plan.T;              // step of the unit
+    const int n = min(p.plan.T - v, r.t_end - r.t);
+    r.t += n;
+    if (v + n == p.plan.T) {
+      ++r.u;
+      if (++r.gi == p.plan.G) {
+        r.gi = 0;
+        ++r.h;
+      }
     }
+    s.j0 = max(0, v - kKv8Lead);
+    s.n = v + n - kKv8Lead - s.j0;
+    if (s.n > 0) return true;
   }
-  return true;
+  return false;
 }
 
 // One arrival for a warp whose lanes have all done what the barrier stands for.
@@ -163,23 +168,22 @@ __device__ __forceinline__ float load_queries(const Doc8Params& p, uint8_t* tile
   cp_async_wait_all();
   __syncwarp();
   const int r = r0 + lane;
-  float am = 0.f;
+  uint32_t am2 = 0;                       // largest magnitudes, as bits, of two columns
 #pragma unroll 4
   for (int i = 0; i < U; ++i) {
     const uint4 x = *unit_at(tile, r, i);
     const uint32_t a[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 f = bf2_to_f2(a[j]);
-      am = fmaxf(am, fabsf(f.x) < INFINITY ? fabsf(f.x) : 0.f);
-      am = fmaxf(am, fabsf(f.y) < INFINITY ? fabsf(f.y) : 0.f);
-    }
+    for (int j = 0; j < 4; ++j)
+      asm("max.u16x2 %0, %0, %1;" : "+r"(am2) : "r"(a[j] & 0x7fff7fffu));
   }
-  // 2^e with am / 2^e in [2^13, 2^14): bf16's 8 bits are exact in f16 down to
-  // 2^-30 of the row's largest value
-  int e = (int)(__float_as_uint(am) >> 23) - 127 - 13;
+  const uint32_t am = max(am2 & 0xffffu, am2 >> 16);
+  // 2^e with the largest value / 2^e in [2^13, 2^14): bf16's 8 bits are exact in
+  // f16 down to 2^-30 of it
+  int e = (int)(am >> 7) - 127 - 13;
   e = e < -100 ? -100 : e;
-  const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+  const float inv = am >= 0x7f80u ? __int_as_float(0x7fffffff)
+                                  : __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll 4
   for (int i = 0; i < U; ++i) {
     const uint4 x = *unit_at(tile, r, i);
@@ -187,8 +191,8 @@ __device__ __forceinline__ float load_queries(const Doc8Params& p, uint8_t* tile
     uint32_t b[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float2 f = bf2_to_f2(a[j]);   // f - f is 0, or NaN where f is not finite
-      b[j] = f2_to_h2((f.x + (f.x - f.x)) * inv, (f.y + (f.y - f.y)) * inv);
+      const float2 f = bf2_to_f2(a[j]);
+      b[j] = f2_to_h2(f.x * inv, f.y * inv);
     }
     *unit_at(tile, r, i) = make_uint4(b[0], b[1], b[2], b[3]);
   }
@@ -629,7 +633,8 @@ __global__ void __maxnreg__(kRegs8) kv8_doc_tc(const Doc8Params p) {
       }
       if (!ok) break;
       // partial of this run: the unit's first CTA has chunk 0
-      const int chunk = s.j0 == 0 ? 0 : cta - plan_cta_of(p.plan, (int64_t)s.u * p.plan.T);
+      const int chunk =
+          s.j0 == 0 ? 0 : cta - plan_cta_of(p.plan, (int64_t)s.u * p.plan.T + kKv8Lead);
       const int64_t prow = ((int64_t)s.u * p.plan.max_chunks + chunk) * kGroupRows + st * 128 + rt;
       if (first < s.n) {
         if (!(ok = warp_wait(o_done + st, od_ph, abort_flag, p.wait_limit, status))) break;
@@ -712,7 +717,7 @@ cudaError_t launch_kv8_doc(const pp_kv8_layer& L, int doc_len, const uint16_t* q
   p.doc_len = doc_len;
   p.plan = plan;
   if (plan.W > INT32_MAX) return cudaErrorInvalidValue;
-  p.tiles = (int)plan.W;
+  p.steps = (int)plan.W;
   p.sl2 = scale * kLog2e;
   p.doc_o = part.doc_o; p.doc_ml = part.doc_ml;
   p.wait_limit = wait_limit;
