@@ -18,13 +18,14 @@
 //
 // Bound: HBM (bf16 in, e4m3 out); a decode step's few kilobytes a row are
 // latency.
+#include <atomic>
+
 #include "kv8.cuh"
 #include "internal.h"
+#include "warp_mma.cuh"
 
 namespace pp {
 namespace {
-
-constexpr int kAppWarps = 4;
 
 struct AppendParams {
   pp_kv8_layer L;
@@ -36,13 +37,12 @@ struct AppendParams {
   const int32_t* pos;
   const float* cos_sin;              // [max_pos][rot]: rot/2 cosines, rot/2 sines
   int rot, interleaved, max_pos;     // rot 0: no rotation
-  int win;                           // rows whose leaders one CTA looks after
+  int win;                           // rows whose leaders one CTA looks after, at most 32
   int ys;                            // CTAs along y for keys and values; the rest turn queries
 };
 
 // Eight consecutive dims of a row: 16 bytes of bf16 -> floats.
-__device__ __forceinline__ void load8(const uint16_t* src, float (&x)[8]) {
-  const uint4 w = *reinterpret_cast<const uint4*>(src);
+__device__ __forceinline__ void unpack8(const uint4 w, float (&x)[8]) {
   const uint32_t a[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
@@ -77,35 +77,44 @@ __device__ __forceinline__ void load_angles(const AppendParams& p, int pos, int 
   }
 }
 
-// Rotate the lane's 8 dims.  Every product and difference is rounded by
-// itself (no fused multiply-add), the result a plain fp32 evaluation of
-// a cos - b sin gives, so which e4m3 value a rotated key rounds to does not
-// depend on the compiler's contraction.  All lanes of the warp call it.
+// Rotations of 8 dims.  Every product and difference is rounded by itself (no
+// fused multiply-add), the result a plain fp32 evaluation of a cos - b sin
+// gives, so which e4m3 value a rotated key rounds to does not depend on the
+// compiler's contraction.
+__device__ __forceinline__ void turn_pairs(const float (&cs)[8], const float (&sn)[8],
+                                           float (&x)[8]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float a = x[2 * j], b = x[2 * j + 1];
+    x[2 * j] = __fsub_rn(__fmul_rn(a, cs[j]), __fmul_rn(b, sn[j]));
+    x[2 * j + 1] = __fadd_rn(__fmul_rn(b, cs[j]), __fmul_rn(a, sn[j]));
+  }
+}
+// y: the other half's dims
+__device__ __forceinline__ void turn_halves(const float (&cs)[8], const float (&sn)[8], bool low,
+                                            float (&x)[8], const float (&y)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float c = __fmul_rn(x[e], cs[e]), s = __fmul_rn(y[e], sn[e]);
+    x[e] = low ? __fsub_rn(c, s) : __fadd_rn(c, s);
+  }
+}
+// The lane's 8 dims, the other half's by shuffle; all lanes of the warp call it.
 __device__ __forceinline__ void turn8(const AppendParams& p, int u, int lane, const float (&cs)[8],
                                       const float (&sn)[8], float (&x)[8]) {
   if (p.rot == 0) return;
   const bool in = u * 8 < p.rot;
   if (p.interleaved) {
-    if (!in) return;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float a = x[2 * j], b = x[2 * j + 1];
-      x[2 * j] = __fsub_rn(__fmul_rn(a, cs[j]), __fmul_rn(b, sn[j]));
-      x[2 * j + 1] = __fadd_rn(__fmul_rn(b, cs[j]), __fmul_rn(a, sn[j]));
-    }
+    if (in) turn_pairs(cs, sn, x);
     return;
   }
   const int hu = p.rot >> 4;                       // units of a half
   const bool low = u < hu;
   const int other = in ? (low ? lane + hu : lane - hu) : lane;
+  float y[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float y = __shfl_sync(0xffffffffu, x[e], other);
-    if (in) {
-      const float c = __fmul_rn(x[e], cs[e]), s = __fmul_rn(y, sn[e]);
-      x[e] = low ? __fsub_rn(c, s) : __fadd_rn(c, s);
-    }
-  }
+  for (int e = 0; e < 8; ++e) y[e] = __shfl_sync(0xffffffffu, x[e], other);
+  if (in) turn_halves(cs, sn, low, x, y);
 }
 
 // Largest finite magnitude of 8 values, joined to a; any non-finite: bad.
@@ -128,10 +137,10 @@ __device__ __forceinline__ uint2 quant8(const float (&x)[8], float inv) {
 }
 
 // The slots [0, n) of one head's page (n * d bytes), rounded again after its
-// scale grew: x -> rn_e4m3(x * ratio), ratio = old / new < 1.
+// scale grew: x -> rn_e4m3(x * ratio), ratio = old / new < 1; thread t of nt.
 template <int D>
-__device__ __forceinline__ void requant(uint8_t* base, int n, float ratio, int lane) {
-  for (int c = lane; c < n * (D / 16); c += 32) {
+__device__ __forceinline__ void requant(uint8_t* base, int n, float ratio, int t, int nt) {
+  for (int c = t; c < n * (D / 16); c += nt) {
     uint4* at = reinterpret_cast<uint4*>(base) + c;
     const uint4 w = *at;
     uint32_t a[4] = {w.x, w.y, w.z, w.w};
@@ -145,61 +154,17 @@ __device__ __forceinline__ void requant(uint8_t* base, int n, float ratio, int l
   }
 }
 
-// Rows [i, i + nr) of the call into slots [off, off + nr) of head h of page
-// pg, by one warp: lane = (row of the pass, 8-dim unit).
+// A lane's 8 dims of a row's key and value to slot `slot`.  All lanes call it.
 template <int D>
-__device__ __forceinline__ void write_group(const AppendParams& p, int i, int nr, int pos0, int pg,
-                                            int off, int h, int lane) {
-  constexpr int U = D / 8, RP = 32 / U;
-  const int u = lane % U, rl = lane / U;
-  const int64_t cell = (int64_t)pg * p.L.H + h;
-  uint8_t* kb = p.L.k + cell * p.L.page * D;
-  uint8_t* vb = p.L.v + cell * p.L.page * D;
-  auto load = [&](int r, float (&kx)[8], float (&vx)[8]) {
-    float cs[8], sn[8];
-    const bool ok = r < nr;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) kx[e] = vx[e] = cs[e] = sn[e] = 0.f;
-    if (ok) {
-      load8(p.k + (int64_t)(i + r) * p.k_ld + (int64_t)h * D + u * 8, kx);
-      load8(p.v + (int64_t)(i + r) * p.v_ld + (int64_t)h * D + u * 8, vx);
-      if (p.rot) load_angles(p, pos0 + r, u, cs, sn);
-    }
-    turn8(p, u, lane, cs, sn, kx);
-  };
-  float ka = 0.f, va = 0.f;
-  bool bad = false;
-  float kx[8], vx[8];
-  for (int r0 = 0; r0 < nr; r0 += RP) {
-    load(r0 + rl, kx, vx);
-    amax8(kx, ka, bad);
-    amax8(vx, va, bad);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    ka = fmaxf(ka, __shfl_xor_sync(0xffffffffu, ka, o));
-    va = fmaxf(va, __shfl_xor_sync(0xffffffffu, va, o));
-  }
-  if (__any_sync(0xffffffffu, bad) && lane == 0) set_status(p.L.status, PP_DEV_NONFINITE);
-  float ks = scale_for(ka), vs = scale_for(va);
-  if (off > 0) {
-    const float ko = p.L.k_scale[cell], vo = p.L.v_scale[cell];
-    __syncwarp();
-    if (ks > ko) requant<D>(kb, off, ko / ks, lane);
-    else ks = ko;
-    if (vs > vo) requant<D>(vb, off, vo / vs, lane);
-    else vs = vo;
-  }
-  if (lane == 0) {
-    p.L.k_scale[cell] = ks;
-    p.L.v_scale[cell] = vs;
-  }
-  const float ki = 1.f / ks, vi = 1.f / vs;
-  for (int r0 = 0; r0 < nr; r0 += RP) {
-    if (r0 > 0 || nr > RP) load(r0 + rl, kx, vx);
-    // A NaN among a row's values is kept by its key: value 0, first key
-    // element NaN.  Queries that see the row come out NaN either way, and
-    // queries that do not see it are not touched by 0 * NaN.
+__device__ __forceinline__ void put8(uint8_t* kb, uint8_t* vb, int slot, int u, bool on,
+                                     const float (&kx)[8], float (&vx)[8], float ki, float vi,
+                                     bool bad, int lane) {
+  constexpr int U = D / 8;
+  uint32_t nan_lanes = 0;
+  if (bad) {
+    // A NaN among a row's values is kept by its key: value 0, first key element
+    // NaN.  Queries that see the row come out NaN either way, and queries that
+    // do not see it are not touched by 0 * NaN.
     bool vn = false;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -207,81 +172,347 @@ __device__ __forceinline__ void write_group(const AppendParams& p, int i, int nr
       vn |= n;
       vx[e] = n ? 0.f : vx[e];
     }
-    const uint32_t nan_lanes = __ballot_sync(0xffffffffu, vn);
-    uint2 kq = quant8(kx, ki), vq = quant8(vx, vi);
-    const uint32_t mine = U == 32 ? 0xffffffffu : (((1u << U) - 1u) << (rl * U));
-    if (u == 0 && (nan_lanes & mine)) kq.x = (kq.x & ~0xffu) | 0x7fu;
-    if (r0 + rl < nr) {
-      const int64_t at = (int64_t)(off + r0 + rl) * D + u * 8;
-      *reinterpret_cast<uint2*>(kb + at) = kq;
-      *reinterpret_cast<uint2*>(vb + at) = vq;
+    nan_lanes = __ballot_sync(0xffffffffu, vn);
+  }
+  uint2 kq = quant8(kx, ki), vq = quant8(vx, vi);
+  const uint32_t mine = ((1u << U) - 1u) << (lane / U * U);
+  if (u == 0 && (nan_lanes & mine)) kq.x = (kq.x & ~0xffu) | 0x7fu;
+  if (on) {
+    const int64_t at = (int64_t)slot * D + u * 8;
+    *reinterpret_cast<uint2*>(kb + at) = kq;
+    *reinterpret_cast<uint2*>(vb + at) = vq;
+  }
+}
+
+// Sixteen rows of a head by one warp: all of them on their way to shared memory
+// at once, and kept there between the maximum and the rounding, the keys turned,
+// in 32 bits.  The loops over passes stay rolled: unrolled, the instruction
+// fetch bound the kernel.  A key row's place: D floats, the first halves of its
+// 8-dim units, then the second halves; its bf16 arrive in the upper half.
+template <int D>
+struct Stage16 {
+  static constexpr int KROW = D * 4, VROW = D * 2;
+  static constexpr int BYTES = 16 * (KROW + VROW);
+};
+
+// Rows [i, i + nr) of the call into slots [off, off + nr) of head h of page pg
+// by the `wph` warps of a head, 16 rows each; all of the block's warps call it
+// (live: this one has a head), for its one barrier.
+template <int D, int WARPS>
+__device__ __forceinline__ void write_group(const AppendParams& p, int i, int nr, int pos0, int pg,
+                                            int off, int h, bool live, int part, int wph,
+                                            float2 (&red)[WARPS], uint8_t* stage, int warp,
+                                            int lane) {
+  using S = Stage16<D>;
+  constexpr int U = D / 8, RP = 32 / U;               // units a row, rows a pass
+  const int u = lane % U, rl = lane / U;
+  const int64_t cell = (int64_t)pg * p.L.H + h;
+  uint8_t* kb = p.L.k + cell * p.L.page * D;
+  uint8_t* vb = p.L.v + cell * p.L.page * D;
+  const int r0 = part * 16;
+  const int mine = live ? min(16, nr - r0) : 0;       // rows of this warp
+  uint8_t* ks_at = stage + u * 16;                    // lane's share of key row 0
+  uint8_t* vs_at = stage + 16 * S::KROW + u * 16;
+  float ka = 0.f, ko = 0.f, vo = 0.f;
+  uint32_t va2 = 0;                                   // bf16 magnitudes, as bits, two columns
+  float odd = 0.f;                                    // NaN when a key is not finite
+  if (live && off > 0) {
+    ko = p.L.k_scale[cell];
+    vo = p.L.v_scale[cell];
+  }
+  __syncwarp();                                       // the head before is out of the stage
+  const int64_t src0 = (int64_t)(i + r0 + rl), at0 = (int64_t)h * D + u * 8;
+#pragma unroll 2
+  for (int r = rl; r < mine; r += RP) {
+    cp_async16(smem_u32(ks_at + r * S::KROW + D * 2), p.k + (src0 + r - rl) * p.k_ld + at0, 16);
+    cp_async16(smem_u32(vs_at + r * S::VROW), p.v + (src0 + r - rl) * p.v_ld + at0, 16);
+  }
+  cp_async_wait_all();
+  __syncwarp();
+  const int half = p.rot >> 4, pair = u < half ? u + half : u - half;   // units of a half
+  for (int q = 0; q < mine; q += RP) {
+    const int r = q + rl;
+    const bool on = r < mine;
+    float x[8], y[8], cs[8], sn[8];
+    if (on) {
+      unpack8(*reinterpret_cast<const uint4*>(ks_at + r * S::KROW + D * 2), x);
+      if (u * 8 < p.rot) {
+        load_angles(p, pos0 + r0 + r, u, cs, sn);
+        if (p.interleaved) {
+          turn_pairs(cs, sn, x);
+        } else {
+          unpack8(*reinterpret_cast<const uint4*>(ks_at + r * S::KROW + D * 2 + (pair - u) * 16), y);
+          turn_halves(cs, sn, u < half, x, y);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        ka = fmaxf(ka, fabsf(x[e]));
+        odd = fmaf(x[e], 0.f, odd);
+      }
+      const uint4 v = *reinterpret_cast<const uint4*>(vs_at + r * S::VROW);
+      const uint32_t a[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        asm("max.u16x2 %0, %0, %1;" : "+r"(va2) : "r"(a[c] & 0x7fff7fffu));
+    }
+    __syncwarp();                                     // every bf16 of these rows has been read
+    if (on) {
+      *reinterpret_cast<float4*>(ks_at + r * S::KROW) = make_float4(x[0], x[1], x[2], x[3]);
+      *reinterpret_cast<float4*>(ks_at + r * S::KROW + D * 2) = make_float4(x[4], x[5], x[6], x[7]);
+    }
+  }
+  const uint32_t vm = max(va2 & 0xffffu, va2 >> 16);
+  float va = __uint_as_float(vm << 16);
+  const bool bad = __any_sync(0xffffffffu, odd != 0.f || vm >= 0x7f80u);
+  auto turned = [&](int r, float (&x)[8]) {
+    const float4 a = *reinterpret_cast<const float4*>(ks_at + r * S::KROW);
+    const float4 b = *reinterpret_cast<const float4*>(ks_at + r * S::KROW + D * 2);
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+  };
+  if (bad) {                                          // rare: the largest finite ones
+    if (lane == 0) set_status(p.L.status, PP_DEV_NONFINITE);
+    ka = va = 0.f;
+    bool any = false;
+    for (int r = rl; r < mine; r += RP) {
+      float x[8];
+      turned(r, x);
+      amax8(x, ka, any);
+      unpack8(*reinterpret_cast<const uint4*>(vs_at + r * S::VROW), x);
+      amax8(x, va, any);
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    ka = fmaxf(ka, __shfl_xor_sync(0xffffffffu, ka, o));
+    va = fmaxf(va, __shfl_xor_sync(0xffffffffu, va, o));
+  }
+  // (the barrier also has every warp's look at the old scales behind it before
+  // one of them is overwritten)
+  if (lane == 0) red[warp] = make_float2(ka, va);
+  __syncthreads();
+  if (!live) return;
+  for (int w = 0; w < wph; ++w) {
+    const float2 y = red[warp - part + w];
+    ka = fmaxf(ka, y.x);
+    va = fmaxf(va, y.y);
+  }
+  float ks = scale_for(ka), vs = scale_for(va);
+  if (off > 0) {
+    if (ks > ko) requant<D>(kb, off, ko / ks, part * 32 + lane, wph * 32);
+    else ks = ko;
+    if (vs > vo) requant<D>(vb, off, vo / vs, part * 32 + lane, wph * 32);
+    else vs = vo;
+  }
+  if (part == 0 && lane == 0) {
+    p.L.k_scale[cell] = ks;
+    p.L.v_scale[cell] = vs;
+  }
+  const float ki = 1.f / ks, vi = 1.f / vs;
+#pragma unroll 2
+  for (int q = 0; q < mine; q += RP) {
+    const int r = q + rl;
+    const int rr = r < mine ? r : 0;
+    float kx[8], vx[8];
+    turned(rr, kx);
+    unpack8(*reinterpret_cast<const uint4*>(vs_at + rr * S::VROW), vx);
+    put8<D>(kb, vb, off + r0 + r, u, r < mine, kx, vx, ki, vi, bad, lane);
+  }
+}
+
+// The same for short runs (one row of a decode step): a warp takes 32 / U heads
+// side by side, U lanes each, all rows of one after another.  h: the lane's head.
+template <int D>
+__device__ __forceinline__ void write_short(const AppendParams& p, int i, int nr, int pos0, int pg,
+                                            int off, int h, bool live, int lane) {
+  constexpr int U = D / 8;
+  const int u = lane % U;
+  const int64_t cell = (int64_t)pg * p.L.H + h;
+  uint8_t* kb = p.L.k + cell * p.L.page * D;
+  uint8_t* vb = p.L.v + cell * p.L.page * D;
+  float ko = 0.f, vo = 0.f;
+  if (live && off > 0) {
+    ko = p.L.k_scale[cell];
+    vo = p.L.v_scale[cell];
+  }
+  float kx[8], vx[8], ka = 0.f, va = 0.f;
+  bool bad = false;
+  auto load = [&](int r) {
+    uint4 k = make_uint4(0, 0, 0, 0), v = k;
+    float cs[8], sn[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) cs[e] = sn[e] = 0.f;
+    if (live) {
+      k = __ldg(reinterpret_cast<const uint4*>(p.k + (int64_t)(i + r) * p.k_ld + (int64_t)h * D + u * 8));
+      v = __ldg(reinterpret_cast<const uint4*>(p.v + (int64_t)(i + r) * p.v_ld + (int64_t)h * D + u * 8));
+    }
+    if (p.rot) load_angles(p, pos0 + r, u, cs, sn);
+    unpack8(k, kx);
+    unpack8(v, vx);
+    turn8(p, u, lane, cs, sn, kx);
+  };
+  for (int r = 0; r < nr; ++r) {
+    load(r);
+    amax8(kx, ka, bad);
+    amax8(vx, va, bad);
+  }
+#pragma unroll
+  for (int o = U / 2; o > 0; o >>= 1) {
+    ka = fmaxf(ka, __shfl_xor_sync(0xffffffffu, ka, o));
+    va = fmaxf(va, __shfl_xor_sync(0xffffffffu, va, o));
+  }
+  bad = __any_sync(0xffffffffu, bad);
+  if (bad && lane == 0) set_status(p.L.status, PP_DEV_NONFINITE);
+  float ks = scale_for(ka), vs = scale_for(va);
+  if (live && off > 0) {
+    if (ks > ko) requant<D>(kb, off, ko / ks, u, U);
+    else ks = ko;
+    if (vs > vo) requant<D>(vb, off, vo / vs, u, U);
+    else vs = vo;
+  }
+  __syncwarp();
+  if (live && u == 0) {
+    p.L.k_scale[cell] = ks;
+    p.L.v_scale[cell] = vs;
+  }
+  const float ki = 1.f / ks, vi = 1.f / vs;
+  for (int r = 0; r < nr; ++r) {
+    if (nr > 1) load(r);
+    put8<D>(kb, vb, off + r, u, live, kx, vx, ki, vi, bad, lane);
+  }
+}
+
+// Of the rows before i: how many are of stream s (joined to cnt), and the last
+// that is not (joined to last); 16 bytes of ids a thread at a time.
+__device__ __forceinline__ void scan_ids(const int16_t* sid, int i, int s, int& cnt, int& last) {
+  auto one = [&](int j, int id) {
+    const bool same = id == s;
+    cnt += same ? 1 : 0;
+    last = same ? last : max(last, j);
+  };
+  const int lead = min(i, (int)((16 - (reinterpret_cast<uintptr_t>(sid) & 15)) & 15) / 2);
+  const int vecs = (i - lead) / 8;
+  for (int j = threadIdx.x; j < lead; j += blockDim.x) one(j, sid[j]);
+#pragma unroll 4
+  for (int v = threadIdx.x; v < vecs; v += blockDim.x) {
+    const int4 w = __ldg(reinterpret_cast<const int4*>(sid + lead) + v);
+    const int a[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      one(lead + v * 8 + 2 * c, (int)(int16_t)(a[c] & 0xffff));
+      one(lead + v * 8 + 2 * c + 1, a[c] >> 16);
+    }
+  }
+  for (int j = lead + vecs * 8 + threadIdx.x; j < i; j += blockDim.x) one(j, sid[j]);
+}
+
+// Turn the window's queries: a warp a row, four passes of heads in flight.
+template <int D, int WARPS>
+__device__ __forceinline__ void turn_queries(const AppendParams& p, int w0, int w1, int hb, int he,
+                                             int warp, int lane) {
+  constexpr int U = D / 8, RP = 32 / U;
+  const int u = lane % U, hl = lane / U;
+  const int row = w0 + lane;
+  const int s_l = row < w1 ? p.sid[row] : -1, ps_l = row < w1 ? p.pos[row] : -1;
+  for (int i = w0 + warp; i < w1; i += WARPS) {
+    const int s = __shfl_sync(0xffffffffu, s_l, i - w0), ps = __shfl_sync(0xffffffffu, ps_l, i - w0);
+    if (s < 0 || s > p.L.P_max || ps < 0 || (p.rot && ps >= p.max_pos)) continue;
+    float cs[8], sn[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) cs[e] = sn[e] = 0.f;
+    if (p.rot) load_angles(p, ps, u, cs, sn);
+    const uint16_t* src = p.q + (int64_t)i * p.q_ld + u * 8;
+    uint16_t* dst = p.q_out + (int64_t)i * p.qo_ld + u * 8;
+    for (int h0 = hb; h0 < he; h0 += 4 * RP) {
+      uint4 w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int h = h0 + j * RP + hl;
+        w[j] = make_uint4(0, 0, 0, 0);
+        if (h < he) w[j] = *reinterpret_cast<const uint4*>(src + (int64_t)h * D);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int h = h0 + j * RP + hl;
+        float x[8];
+        unpack8(w[j], x);
+        turn8(p, u, lane, cs, sn, x);
+        if (h < he)
+          *reinterpret_cast<uint4*>(dst + (int64_t)h * D) =
+              make_uint4(f2_to_bf2(x[0], x[1]), f2_to_bf2(x[2], x[3]), f2_to_bf2(x[4], x[5]),
+                         f2_to_bf2(x[6], x[7]));
+      }
     }
   }
 }
 
-template <int D>
-__global__ void __launch_bounds__(kAppWarps * 32) kv8_append(const AppendParams p) {
+// WARPS: 4, or 8 for pages of 128 tokens.  SHORT: for runs of about a row.
+template <int D, int WARPS, bool SHORT>
+__global__ void __launch_bounds__(WARPS * 32, (SHORT ? 32 : 24) / WARPS)
+    kv8_append(const AppendParams p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int w0 = blockIdx.x * p.win;
   const int w1 = min(p.n, w0 + p.win);
   if ((int)blockIdx.y >= p.ys) {
-    // ---- queries: rows w0 .. w1-1, this CTA's share of the heads
-    constexpr int U = D / 8, RP = 32 / U;
-    const int u = lane % U, hl = lane / U;
     const int part = blockIdx.y - p.ys, parts = gridDim.y - p.ys;
-    const int hb = p.Hq * part / parts, he = p.Hq * (part + 1) / parts;
-    for (int i = w0; i < w1; ++i) {
-      const int s = p.sid[i], ps = p.pos[i];
-      if (s < 0 || s > p.L.P_max || ps < 0 || (p.rot && ps >= p.max_pos)) continue;
-      float cs[8], sn[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) cs[e] = sn[e] = 0.f;
-      if (p.rot) load_angles(p, ps, u, cs, sn);
-      for (int h0 = hb + warp * RP; h0 < he; h0 += kAppWarps * RP) {
-        const int h = h0 + hl;
-        float x[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = 0.f;
-        if (h < he) load8(p.q + (int64_t)i * p.q_ld + (int64_t)h * D + u * 8, x);
-        turn8(p, u, lane, cs, sn, x);
-        if (h < he) {
-          uint4 r;
-          r.x = f2_to_bf2(x[0], x[1]);
-          r.y = f2_to_bf2(x[2], x[3]);
-          r.z = f2_to_bf2(x[4], x[5]);
-          r.w = f2_to_bf2(x[6], x[7]);
-          *reinterpret_cast<uint4*>(p.q_out + (int64_t)i * p.qo_ld + (int64_t)h * D + u * 8) = r;
-        }
-      }
-    }
+    turn_queries<D, WARPS>(p, w0, w1, p.Hq * part / parts, p.Hq * (part + 1) / parts, warp, lane);
     return;
   }
-  __shared__ int red_cnt[kAppWarps], red_last[kAppWarps];
+  __shared__ int red_cnt[WARPS], red_last[WARPS];
+  extern __shared__ __align__(16) uint8_t stage[];
+  __shared__ float2 red[2][WARPS];
   const int page = p.L.page;
+  const int wph = SHORT ? 1 : page >> 4;            // warps a head
+  const int hpp = SHORT ? WARPS * 256 / D : WARPS / wph;   // heads a pass
   const int hb = p.L.H * (int)blockIdx.y / p.ys, he = p.L.H * ((int)blockIdx.y + 1) / p.ys;
-  for (int i = w0; i < w1; ++i) {       // every branch down to the warps' heads is CTA-uniform
-    const int s = p.sid[i], ps = p.pos[i];
-    if (s < 0) continue;
-    const bool first_cta = blockIdx.y == 0 && threadIdx.x == 0;
-    if (s > p.L.P_max) {
-      if (first_cta) set_status(p.L.status, PP_DEV_BAD_STREAM);
-      continue;
+  // every warp looks at the window's rows, a lane each (at most 32)
+  const int row = w0 + lane;
+  int s_l = -1, ps_l = -1, err = 0;
+  bool lead = false;
+  if (row < w1) {
+    s_l = p.sid[row];
+    ps_l = p.pos[row];
+    if (s_l > p.L.P_max) {
+      err = PP_DEV_BAD_STREAM;
+    } else if (s_l >= 0) {
+      const int slot = s_l == 0 ? ps_l : ps_l - p.L.pos0;
+      if (ps_l < 0 || slot < 0)
+        err = s_l == 0 ? PP_DEV_DOC_OUT_OF_RANGE : PP_DEV_BAD_POSITION;
+      else    // a row that follows its neighbour within a page is not a leader
+        lead = row == 0 || slot % page == 0 || p.sid[row - 1] != s_l || p.pos[row - 1] != ps_l - 1;
     }
+  }
+  const bool first_cta = blockIdx.y == 0 && warp == 0;
+  if (first_cta && err) set_status(p.L.status, err);
+  uint32_t leaders = __ballot_sync(0xffffffffu, lead);
+  int buf = 0;
+  while (leaders) {                     // the same in every warp
+    const int l = __ffs(leaders) - 1;
+    leaders &= leaders - 1;
+    const int i = w0 + l;
+    const int s = __shfl_sync(0xffffffffu, s_l, l), ps = __shfl_sync(0xffffffffu, ps_l, l);
     const int slot = s == 0 ? ps : ps - p.L.pos0;
-    if (ps < 0 || slot < 0) {
-      if (first_cta) set_status(p.L.status, s == 0 ? PP_DEV_DOC_OUT_OF_RANGE : PP_DEV_BAD_POSITION);
-      continue;
+    const int off = slot % page, seg = slot / page;
+    int pg = -1;
+    const bool fits = seg < (s == 0 ? p.L.doc_pages : p.L.seg_pages);
+    if (fits)
+      pg = page_of(s == 0 ? p.L.doc_table[seg]
+                          : p.L.seg_table[(int64_t)(s - 1) * p.L.seg_pages + seg], p.L.n_pages);
+    // rows of the run that fall into this page
+    const int most = min(page - off, p.n - i);
+    int nr = 1;
+    for (int r0 = 1; r0 < most; r0 += 32) {
+      const int r = r0 + lane;
+      const bool in = r < most && p.sid[i + r] == s && (int64_t)p.pos[i + r] == (int64_t)ps + r;
+      const uint32_t m = __ballot_sync(0xffffffffu, in);
+      nr = r0 + (m == 0xffffffffu ? 32 : __ffs(~m) - 1);
+      if (m != 0xffffffffu) break;
     }
-    const int off = slot % page;
-    if (i > 0 && off != 0 && p.sid[i - 1] == s && p.pos[i - 1] == ps - 1) continue;  // not a leader
     // The stream's run must be its only one and its positions consecutive:
     // count the earlier rows of the stream and find the last row of another.
     int cnt = 0, last = -1;
-    for (int j = threadIdx.x; j < i; j += blockDim.x) {
-      const bool same = p.sid[j] == s;
-      cnt += same ? 1 : 0;
-      last = same ? last : j;
-    }
+    scan_ids(p.sid, i, s, cnt, last);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       cnt += __shfl_xor_sync(0xffffffffu, cnt, o);
@@ -296,48 +527,52 @@ __global__ void __launch_bounds__(kAppWarps * 32) kv8_append(const AppendParams 
     cnt = 0;
     last = -1;
 #pragma unroll
-    for (int w = 0; w < kAppWarps; ++w) {
+    for (int w = 0; w < WARPS; ++w) {
       cnt += red_cnt[w];
       last = max(last, red_last[w]);
     }
     const int a = last + 1;             // first row of the run
-    if (cnt != i - a || (int64_t)ps - p.pos[a] != i - a) {
-      if (first_cta) set_status(p.L.status, PP_DEV_ROW_ORDER);
-      continue;
+    if (cnt != i - a || (int64_t)ps - p.pos[a] != i - a) err = PP_DEV_ROW_ORDER;
+    else if (!fits) err = s == 0 ? PP_DEV_DOC_OUT_OF_RANGE : PP_DEV_SEGMENT_OVERFLOW;
+    else if (pg < 0) err = PP_DEV_BAD_PAGE;
+    else err = p.rot && ps + nr > p.max_pos ? PP_DEV_BAD_POSITION : 0;   // past the angle table
+    if (err && first_cta && lane == 0) set_status(p.L.status, err);
+    if (err == PP_DEV_BAD_POSITION) nr = p.max_pos - ps;
+    else if (err) continue;
+    if (nr <= 0) continue;
+    for (int h0 = hb; h0 < he; h0 += hpp) {
+      if constexpr (SHORT) {
+        const int h = h0 + warp * (256 / D) + lane / (D / 8);
+        write_short<D>(p, i, nr, ps, pg, off, h < he ? h : hb, h < he, lane);
+      } else {
+        const int h = h0 + warp / wph;
+        write_group<D, WARPS>(p, i, nr, ps, pg, off, h, h < he, warp % wph, wph, red[buf],
+                              stage + warp * Stage16<D>::BYTES, warp, lane);
+        buf ^= 1;
+      }
     }
-    const int seg = slot / page;
-    if (seg >= (s == 0 ? p.L.doc_pages : p.L.seg_pages)) {
-      if (first_cta)
-        set_status(p.L.status, s == 0 ? PP_DEV_DOC_OUT_OF_RANGE : PP_DEV_SEGMENT_OVERFLOW);
-      continue;
-    }
-    const int pg = page_of(s == 0 ? p.L.doc_table[seg]
-                                  : p.L.seg_table[(int64_t)(s - 1) * p.L.seg_pages + seg],
-                           p.L.n_pages);
-    if (pg < 0) {
-      if (first_cta) set_status(p.L.status, PP_DEV_BAD_PAGE);
-      continue;
-    }
-    // rows of the run that fall into this page
-    const int most = min(page - off, p.n - i);
-    int nr = 1;
-    for (int r0 = 1; r0 < most; r0 += 32) {
-      const int r = r0 + lane;
-      const bool in = r < most && p.sid[i + r] == s && (int64_t)p.pos[i + r] == (int64_t)ps + r;
-      const uint32_t m = __ballot_sync(0xffffffffu, in);
-      nr = r0 + (m == 0xffffffffu ? 32 : __ffs(~m) - 1);
-      if (m != 0xffffffffu) break;
-    }
-    if (p.rot && ps + nr > p.max_pos) {   // positions past the angle table
-      if (first_cta) set_status(p.L.status, PP_DEV_BAD_POSITION);
-      nr = p.max_pos - ps;
-      if (nr <= 0) continue;
-    }
-    for (int h = hb + warp; h < he; h += kAppWarps) write_group<D>(p, i, nr, ps, pg, off, h, lane);
   }
 }
 
 __global__ void kv8_clear_status(int32_t* status) { *status = 0; }
+
+template <int D, int WARPS, bool SHORT>
+cudaError_t start(const AppendParams& p, dim3 grid, cudaStream_t st) {
+  constexpr int SMEM = SHORT ? 0 : WARPS * Stage16<D>::BYTES;
+  static std::atomic<uint64_t> ready{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (SMEM > 0 && !(ready.load() & bit)) {
+    e = cudaFuncSetAttribute(kv8_append<D, WARPS, SHORT>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(bit);
+  }
+  kv8_append<D, WARPS, SHORT><<<grid, WARPS * 32, SMEM, st>>>(p);
+  return cudaGetLastError();
+}
 
 }  // namespace
 
@@ -364,17 +599,34 @@ cudaError_t launch_kv8_append(const pp_kv8_layer& L, const uint16_t* k, int64_t 
     p.interleaved = rope->interleaved;
     p.max_pos = rope->max_pos;
   }
-  // Four warps' heads a CTA; rows by themselves while that keeps the grid
-  // within a few waves, else windows of rows (most rows of a long run are not
-  // leaders, and a CTA that only finds that out costs a launch slot).
-  p.ys = (L.H + kAppWarps - 1) / kAppWarps;
+  // A CTA looks after a window of rows for a share of the heads.  Windows are
+  // long (most rows of a long run are no leaders, and a CTA that only finds
+  // that out costs a launch slot) and shares small, as far as the grid stays
+  // between a few CTAs an SM and about 64.
+  // A stream has one run a call, so more rows than streams means long runs.
+  // (One row by a warp of the long form: a decode step of 256 streams, 32 heads
+  // took 54 us; questions by the short form 159 us.)
+  const bool brief = n <= L.P_max;
+  const int warps = !brief && L.page == 128 ? 8 : 4;
+  const int hpp = brief ? warps * 256 / L.d : warps / (L.page >> 4);
+  const int passes = (L.H + hpp - 1) / hpp;
   p.win = 1;
-  while (p.win < 16 && (int64_t)((n + p.win - 1) / p.win) * p.ys > 64LL * num_sms) p.win *= 2;
-  const int qs = q ? (Hq + 15) / 16 : 0;
-  const dim3 grid((n + p.win - 1) / p.win, p.ys + qs);
-  if (L.d == 128) kv8_append<128><<<grid, kAppWarps * 32, 0, st>>>(p);
-  else kv8_append<64><<<grid, kAppWarps * 32, 0, st>>>(p);
-  return cudaGetLastError();
+  while (p.win < 32 && (int64_t)((n + p.win - 1) / p.win) * passes > 32LL * num_sms) p.win *= 2;
+  const int64_t wins = (n + p.win - 1) / p.win;
+  // scanning the ids before a leader is the share's fixed cost: fewer shares
+  // for long calls
+  p.ys = passes;
+  while (p.ys > 1 && wins * (p.ys / 2) >= 16LL * num_sms) p.ys = (p.ys + 1) / 2;
+  int qs = q ? (Hq + 15) / 16 : 0;
+  if (q && p.win > 4) qs = (Hq + 31) / 32;
+  const dim3 grid((unsigned)wins, p.ys + qs);
+  if (L.d == 128)
+    return brief        ? start<128, 4, true>(p, grid, st)
+           : warps == 8 ? start<128, 8, false>(p, grid, st)
+                        : start<128, 4, false>(p, grid, st);
+  return brief        ? start<64, 4, true>(p, grid, st)
+         : warps == 8 ? start<64, 8, false>(p, grid, st)
+                      : start<64, 4, false>(p, grid, st);
 }
 
 }  // namespace pp
