@@ -8,7 +8,6 @@ fallback of any kind.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -449,6 +448,7 @@ class KV8Layer:
         if dev.type == "cuda" and dev.index is None:
             dev = torch.device("cuda", torch.cuda.current_device())
         self.device = dev
+        self.index = -1 if dev.type == "cpu" else dev.index
         self.H, self.d, self.page, self.n_pages = H, d, page, n_pages
         self.P_max, self.seg_pages, self.doc_pages, self.pos0 = P_max, seg_pages, doc_pages, pos0
 
@@ -492,6 +492,7 @@ class Rope:
             raise ValueError("Rope: cos_sin must be [max_pos, dim]")
         _want(cos_sin, torch.float32, "cos_sin", cos_sin.device)
         self.cos_sin, self.interleaved = cos_sin, bool(interleaved)
+        self.index = cos_sin.get_device()
         self.max_pos, self.dim = cos_sin.shape
         self.struct = RopeStruct(self.dim, int(self.interleaved), self.max_pos, 0,
                                  cos_sin.data_ptr())
@@ -507,15 +508,26 @@ class Rope:
                    interleaved)
 
 
-def _rows(t: torch.Tensor, name: str, n: int, heads: int, d: int, device) -> int:
+# The 8-bit calls launch kernels of a few microseconds, so their checks take the
+# short way: one test of everything, and the messages only when it fails.
+_BF16, _I16, _I32, _F32, _U8 = (torch.bfloat16, torch.int16, torch.int32, torch.float32,
+                                torch.uint8)
+
+
+def _rows(t: torch.Tensor, name: str, n: int, heads: int, d: int, layer) -> int:
     """Checks rows [n, heads, d] bf16 whose heads are packed and whose rows may
     be strided; returns the elements between rows."""
+    if isinstance(t, torch.Tensor) and t.dtype is _BF16 and t.get_device() == layer.index and \
+            t.shape == (n, heads, d):
+        s0, s1, s2 = t.stride()
+        if s2 == 1 and s1 == d and s0 >= heads * d and s0 % 8 == 0:
+            return s0
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.dtype != _BF16:
+        raise TypeError(f"{name} must be {_BF16}, got {t.dtype}")
+    if t.device != layer.device:
+        raise ValueError(f"{name} must be on {layer.device}, got {t.device}")
     if t.shape != (n, heads, d):
         raise ValueError(f"{name} must be [{n}, {heads}, {d}], got {list(t.shape)}")
     s0, s1, s2 = t.stride()
@@ -527,16 +539,30 @@ def _rows(t: torch.Tensor, name: str, n: int, heads: int, d: int, device) -> int
     return s0
 
 
-def _on(device):
-    """The device a call launches on, made current where it is not."""
-    return contextlib.nullcontext() if torch.cuda.current_device() == device.index \
-        else torch.cuda.device(device)
+def _want8(t: torch.Tensor, dtype, name: str, layer):
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == layer.index and
+            t.is_contiguous()):
+        _want(t, dtype, name, layer.device)
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _call8(fn, name: str, layer, *args):
+    """fn(layer, *args, stream) on the layer's device and its current stream."""
+    cur = torch.cuda.current_device()
+    if cur != layer.index:
+        with torch.cuda.device(layer.index):
+            return _call8(fn, name, layer, *args)
+    stream = _raw_stream(cur) if _raw_stream else torch.cuda.current_stream(cur).cuda_stream
+    rc = fn(layer.ref, *args, stream)
+    if rc:
+        raise PPError(rc, name)
 
 
 def kv8_reset(layer: KV8Layer):
     """Clear the layer's status word."""
-    with _on(layer.device):
-        _check(_kv8_reset(layer.ref, _stream(layer.device)), "pp_kv8_reset")
+    _call8(_kv8_reset, "pp_kv8_reset", layer)
 
 
 def kv8_append(layer: KV8Layer, k: torch.Tensor, v: torch.Tensor, sid: torch.Tensor,
@@ -546,33 +572,33 @@ def kv8_append(layer: KV8Layer, k: torch.Tensor, v: torch.Tensor, sid: torch.Ten
     sid [n] int16 and positions pos [n] int32: keys rotated by `rope`, both
     quantised into the streams' pages.  q [n, Hq, d]: queries to rotate as
     well; returns q_out (new, given, or q itself)."""
-    dev = layer.device
-    _want(sid, torch.int16, "sid", dev)
-    _want(pos, torch.int32, "pos", dev)
+    _want8(sid, _I16, "sid", layer)
+    _want8(pos, _I32, "pos", layer)
     if sid.dim() != 1 or pos.shape != sid.shape:
         raise ValueError("kv8_append: sid and pos must be [n]")
-    n = sid.shape[0]
-    k_ld = _rows(k, "k", n, layer.H, layer.d, dev)
-    v_ld = _rows(v, "v", n, layer.H, layer.d, dev)
-    if rope is not None and rope.cos_sin.device != dev:
-        raise ValueError(f"rope must be on {dev}, got {rope.cos_sin.device}")
+    n, H, d = sid.shape[0], layer.H, layer.d
+    k_ld = _rows(k, "k", n, H, d, layer)
+    v_ld = _rows(v, "v", n, H, d, layer)
+    rope_ref = None
+    if rope is not None:
+        if rope.index != layer.index:
+            raise ValueError(f"rope must be on {layer.device}, got {rope.cos_sin.device}")
+        rope_ref = rope.ref
     Hq = q_ld = qo_ld = 0
+    q_ptr = qo_ptr = None
     if q is not None:
         if q.dim() != 3:
             raise ValueError("q must be [n, Hq, d]")
         Hq = q.shape[1]
-        q_ld = _rows(q, "q", n, Hq, layer.d, dev)
+        q_ld = _rows(q, "q", n, Hq, d, layer)
         if q_out is None:
-            q_out = torch.empty((n, Hq, layer.d), dtype=torch.bfloat16, device=dev)
-        qo_ld = _rows(q_out, "q_out", n, Hq, layer.d, dev)
+            q_out = torch.empty((n, Hq, d), dtype=_BF16, device=layer.device)
+        qo_ld = _rows(q_out, "q_out", n, Hq, d, layer)
+        q_ptr, qo_ptr = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("kv8_append: q_out without q")
-    with _on(dev):
-        _check(_kv8_append(layer.ref, k.data_ptr(), k_ld, v.data_ptr(), v_ld,
-                           None if q is None else q.data_ptr(), q_ld, Hq, sid.data_ptr(),
-                           pos.data_ptr(), n, None if rope is None else rope.ref,
-                           None if q_out is None else q_out.data_ptr(), qo_ld, _stream(dev)),
-               "pp_kv8_append")
+    _call8(_kv8_append, "pp_kv8_append", layer, k.data_ptr(), k_ld, v.data_ptr(), v_ld, q_ptr, q_ld,
+           Hq, sid.data_ptr(), pos.data_ptr(), n, rope_ref, qo_ptr, qo_ld)
     return q_out
 
 
@@ -587,30 +613,30 @@ def kv8_prefill_workspace_bytes(R: int, Hq: int, H: int, d: int, doc_len: int,
 
 
 def _kv8_attn(fn, name, layer, doc_len, q, q_sid, q_pos, scale, o, lse, ws, opt, ws_fn):
-    dev = layer.device
-    _want(q_sid, torch.int16, "q_sid", dev)
-    _want(q_pos, torch.int32, "q_pos", dev)
-    rows = q_sid.shape[0]
-    if q.dim() != 3 or q_sid.dim() != 1 or q_pos.shape != (rows,):
+    _want8(q_sid, _I16, "q_sid", layer)
+    _want8(q_pos, _I32, "q_pos", layer)
+    rows = q_sid.shape[0] if q_sid.dim() == 1 else -1
+    if q.dim() != 3 or rows < 0 or q_pos.shape != q_sid.shape:
         raise ValueError(f"{name}: q must be [rows, Hq, d], q_sid and q_pos [rows]")
     Hq = q.shape[1]
-    q_ld = _rows(q, "q", rows, Hq, layer.d, dev)
+    q_ld = _rows(q, "q", rows, Hq, layer.d, layer)
     if o is None:
-        o = torch.empty((rows, Hq, layer.d), dtype=torch.bfloat16, device=dev)
-    _want(o, torch.bfloat16, "o", dev)
+        o = torch.empty((rows, Hq, layer.d), dtype=_BF16, device=layer.device)
+    _want8(o, _BF16, "o", layer)
     if o.shape != q.shape:
         raise ValueError(f"{name}: o must be [rows, Hq, d]")
+    lse_ptr = None
     if lse is not None:
-        _want(lse, torch.float32, "lse", dev)
+        _want8(lse, _F32, "lse", layer)
         if lse.shape != (rows, Hq):
             raise ValueError(f"{name}: lse must be [rows, Hq]")
-    with _on(dev):
-        if ws is None:
-            ws = workspace(ws_fn(rows, Hq, layer.H, layer.d, doc_len, opt), dev)
-        _want(ws, torch.uint8, "ws", dev)
-        _check(fn(layer.ref, doc_len, q.data_ptr(), q_ld, Hq, q_sid.data_ptr(), q_pos.data_ptr(),
-                  rows, scale, o.data_ptr(), None if lse is None else lse.data_ptr(),
-                  ws.data_ptr(), ws.numel(), _opts(opt), _stream(dev)), name)
+        lse_ptr = lse.data_ptr()
+    if ws is None:
+        with torch.cuda.device(layer.index):
+            ws = workspace(ws_fn(rows, Hq, layer.H, layer.d, doc_len, opt), layer.device)
+    _want8(ws, _U8, "ws", layer)
+    _call8(fn, name, layer, doc_len, q.data_ptr(), q_ld, Hq, q_sid.data_ptr(), q_pos.data_ptr(),
+           rows, scale, o.data_ptr(), lse_ptr, ws.data_ptr(), ws.numel(), _opts(opt))
     return o
 
 
@@ -637,10 +663,11 @@ def kv8_prefill_attn(layer: KV8Layer, doc_len: int, q: torch.Tensor, q_sid: torc
 def kv8_device_status(layer: KV8Layer) -> int:
     """The 8-bit layer's device status word (PP_DEV_* bits)."""
     out = _i32(0)
-    with _on(layer.device):
-        rc = int(_kv8_status(layer.ref, ctypes.byref(out), _stream(layer.device)))
-    if rc not in (PP_OK, PP_ERR_DEVICE_TIMEOUT):
-        _check(rc, "pp_kv8_get_device_status")
+    try:
+        _call8(_kv8_status, "pp_kv8_get_device_status", layer, ctypes.byref(out))
+    except PPError as e:
+        if e.status != PP_ERR_DEVICE_TIMEOUT:
+            raise
     return int(out.value)
 
 

@@ -128,7 +128,7 @@ def test_binding_checks_shapes_and_strides(pp):
         pp.KV8Layer(2, 64, 16, 4, 2, 2, 2, 20, "cpu", k_scale=torch.zeros((4, 3)))
     with pytest.raises(ValueError):
         pp.Rope(torch.zeros(8))
-    assert pp._rows(torch.zeros((3, 6, 64), dtype=bf)[:, 2:4], "k", 3, 2, 64, L.device) == 384
+    assert pp._rows(torch.zeros((3, 6, 64), dtype=bf)[:, 2:4], "k", 3, 2, 64, L) == 384
     assert L.nbytes() == 2 * 4 * 2 * 16 * 64 + 2 * 4 * 2 * 4 + 4 * 2 + 4 * 4 + 4
 
 
