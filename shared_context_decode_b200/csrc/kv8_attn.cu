@@ -50,6 +50,7 @@ struct Attn8Params {
   int ways;                // warps per item
   int lper;                // log2 of the 16-key chunks per page
   int has_doc;             // document partials to merge
+  int plan32;              // the plan's divisions fit 32 bits
   SplitPlan plan;
   const float* doc_o;
   const float* doc_ml;
@@ -304,14 +305,20 @@ struct DocRow {
   }
 };
 
+// CTA of the document pass that owns step t of its plan (plan_cta_of, in 32 bits
+// where they hold: a 64-bit division is some 150 instructions).
+__device__ __forceinline__ int doc_cta(const Attn8Params& p, int64_t t) {
+  return p.plan32 ? (int)(((uint32_t)(t + 1) * (uint32_t)p.plan.C - 1u) / (uint32_t)p.plan.W)
+                  : plan_cta_of(p.plan, t);
+}
 // Where the document partials of (query row `row`, query head kvh * g + hq) are.
 __device__ __forceinline__ DocRow doc_row(const Attn8Params& p, int row, int kvh, int hq) {
-  const int64_t pair = (int64_t)row * p.g + hq;
-  const int u = kvh * p.plan.G + (int)(pair / kGroupRows);
-  const int64_t ub = plan_unit_begin(p.plan, u);
+  const int pair = row * p.g + hq;                    // (the host keeps rows * Hq in 31 bits)
+  const int u = kvh * p.plan.G + pair / kGroupRows;
+  const int64_t ub = (int64_t)u * p.plan.T;
   DocRow d;
-  d.two = (int64_t)p.rows * p.g - pair / kGroupRows * kGroupRows <= 128;
-  d.n = (plan_cta_of(p.plan, ub + p.plan.T - 1) - plan_cta_of(p.plan, ub + kKv8Lead) + 1) << d.two;
+  d.two = p.rows * p.g - pair / kGroupRows * kGroupRows <= 128;
+  d.n = (doc_cta(p, ub + p.plan.T - 1) - doc_cta(p, ub + kKv8Lead) + 1) << d.two;
   d.slot = (int64_t)u * p.plan.max_chunks * kGroupRows + pair % kGroupRows;
   return d;
 }
@@ -335,17 +342,17 @@ __global__ void __launch_bounds__(WARPS * 32, (NT == 1 ? 16 : 12) / WARPS)
   extern __shared__ __align__(128) uint8_t sm[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r = lane >> 2, c = lane & 3;
-  const int per_cta = (blockDim.x >> 5) / p.ways;
-  const int64_t item = (int64_t)blockIdx.x * per_cta + warp / p.ways;
-  const int way = warp % p.ways;
+  const int lways = 31 - __clz(p.ways);              // a power of two
+  const int item = (int)blockIdx.x * (WARPS >> lways) + (warp >> lways);
+  const int way = warp & (p.ways - 1);
   const bool live = item < p.n_items;
   uint8_t* ring = sm + warp * M::WARP;
   float* my_ml = reinterpret_cast<float*>(ring);
   float* my_o = my_ml + 2 * M::ROWS;
   int r0 = 0, kvh = 0, hb = 0, nh = 1, nrow = 0;
   if (live) {
-    const int x = (int)(item % (p.L.H * p.gt));
-    r0 = (int)(item / (p.L.H * p.gt)) * p.rt;
+    const int x = item % (p.L.H * p.gt);
+    r0 = item / (p.L.H * p.gt) * p.rt;
     kvh = x / p.gt;
     hb = (x % p.gt) * p.hg;               // first query head inside the group
     nh = min(p.hg, p.g - hb);
@@ -359,37 +366,34 @@ __global__ void __launch_bounds__(WARPS * 32, (NT == 1 ? 16 : 12) / WARPS)
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const int n = t * 8 + r;
-      float x2[D / 4];
-      float am = 0.f;
+      uint32_t w2[D / 8];                  // bf16 pairs
+      uint32_t am2 = 0;                    // largest magnitudes, as bits
 #pragma unroll
-      for (int e = 0; e < D / 4; ++e) x2[e] = 0.f;
+      for (int e = 0; e < D / 8; ++e) w2[e] = 0u;
       if (n < n_pairs) {
         const uint16_t* src = p.q + (int64_t)(r0 + n / nh) * p.q_ld +
                               (int64_t)(kvh * p.g + hb + n % nh) * D + c * (D / 4);
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          const uint4 w = *reinterpret_cast<const uint4*>(src + 8 * i);
-          const uint32_t a[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 f = bf2_to_f2(a[j]);
-            // f - f is 0, or NaN where f is not finite
-            x2[8 * i + 2 * j] = f.x + (f.x - f.x);
-            x2[8 * i + 2 * j + 1] = f.y + (f.y - f.y);
-            am = fmaxf(am, fabsf(f.x) < INFINITY ? fabsf(f.x) : 0.f);
-            am = fmaxf(am, fabsf(f.y) < INFINITY ? fabsf(f.y) : 0.f);
-          }
-        }
+        for (int i = 0; i < D / 32; ++i)
+          *reinterpret_cast<uint4*>(&w2[4 * i]) = *reinterpret_cast<const uint4*>(src + 8 * i);
       }
-      am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1));
-      am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 2));
-      // 2^e with am / 2^e in [2^13, 2^14): bf16's 8 bits are exact in f16 down
-      // to 2^-30 of the row's largest value
-      int e = (int)(__float_as_uint(am) >> 23) - 127 - 13;
-      e = e < -100 ? -100 : e;
-      const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) qf[t][i] = f2_to_h2(x2[2 * i] * inv, x2[2 * i + 1] * inv);
+      for (int i = 0; i < D / 8; ++i)
+        asm("max.u16x2 %0, %0, %1;" : "+r"(am2) : "r"(w2[i] & 0x7fff7fffu));
+      uint32_t am = max(am2 & 0xffffu, am2 >> 16);
+      am = max(am, __shfl_xor_sync(0xffffffffu, am, 1));
+      am = max(am, __shfl_xor_sync(0xffffffffu, am, 2));
+      // 2^e with the row's largest value / 2^e in [2^13, 2^14): bf16's 8 bits are
+      // exact in f16 down to 2^-30 of it; a row with a NaN or infinity is all NaN
+      int e = (int)(am >> 7) - 127 - 13;
+      e = e < -100 ? -100 : e;
+      const float inv = am >= 0x7f80u ? __int_as_float(0x7fffffff)
+                                      : __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        const float2 f = bf2_to_f2(w2[i]);
+        qf[t][i] = f2_to_h2(f.x * inv, f.y * inv);
+      }
       const float qsc = __uint_as_float((uint32_t)(e + 127) << 23) * p.sl2;
 #pragma unroll
       for (int a = 0; a < 2; ++a) {
@@ -414,6 +418,7 @@ __global__ void __launch_bounds__(WARPS * 32, (NT == 1 ? 16 : 12) / WARPS)
     // ---- rows that a warp has to itself start from their first document partial
     DocRow dr2[NT][2];
     if (NT > 1 && p.has_doc && p.ways == 1) {
+      asm volatile("griddepcontrol.wait;" ::: "memory");
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         // lane n (of the tile's 8) finds pair n's partials
@@ -559,6 +564,8 @@ __global__ void __launch_bounds__(WARPS * 32, (NT == 1 ? 16 : 12) / WARPS)
   }
   if (p.ways > 1) __syncthreads(); else __syncwarp();
   if (!live) return;
+  // (the segments did not need the document pass; its partials do)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   // ---- merge: the item's warps take its rows in turn, a lane E dims.  Lane n
   // finds where pair n's document partials are.
   constexpr int E = D / 32;
@@ -677,8 +684,19 @@ cudaError_t launch_as(const Attn8Params& p, cudaStream_t st) {
   }
   const int per = WARPS / p.ways;
   const int64_t grid = ((int64_t)p.n_items + per - 1) / per;
-  kv8_attn<D, NT, WARPS><<<(unsigned)grid, WARPS * 32, SMEM, st>>>(p);
-  return cudaGetLastError();
+  // Behind a document pass the blocks may start as its CTAs end: they read
+  // the segments meanwhile and wait for it only where its partials are joined.
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(WARPS * 32);
+  cfg.dynamicSmemBytes = SMEM;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = p.has_doc ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kv8_attn<D, NT, WARPS>, p);
 }
 
 template <int D, int NT>
@@ -713,6 +731,7 @@ cudaError_t launch_kv8_attn(const pp_kv8_layer& L, int doc_len, const uint16_t* 
   p.sl2 = scale * kLog2e;
   p.has_doc = doc_pass ? 1 : 0;
   p.plan = plan;
+  p.plan32 = (plan.W + 1) * plan.C <= 0xffffffffLL;
   p.doc_o = part.doc_o; p.doc_ml = part.doc_ml;
   p.o = o; p.lse = lse;
   // Warps per item: enough to fill the GPU when items are few (they share the
