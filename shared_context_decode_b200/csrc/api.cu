@@ -8,7 +8,6 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include <algorithm>
-#include <cstdlib>
 #include <atomic>
 
 #include "common.cuh"
@@ -315,17 +314,31 @@ bool row_operand(const void* ptr, int64_t ld, int64_t heads, int32_t d) {
 }
 
 // Split of the document over the tensor-core pass's CTAs; C = 0: the document
-// is read by the segment kernel's warps instead (no pass, no workspace).
-SplitPlan kv8_plan(int32_t rows, int32_t Hq, int32_t H, int32_t doc_len, const pp_options* opt) {
-  const int ctas = (opt && opt->splits > 0) ? opt->splits : sm_count();
-  const char* e = getenv("PPKV8_DOC");
-  const int mode = e ? atoi(e) : 1;
-  if (mode == 0 || doc_len == 0) return SplitPlan{};
+// is read by the segment kernel's warps instead (no pass, no workspace), which
+// is faster while both its work and a warp's share of one document are small.
+// Measured on either side (us, pass / warps): 16 rows, 8 heads, 2048 keys 21.3 /
+// 18.8, 64 rows, 8 heads, 1024 keys 18.0 / 26.0; one row of one head, 16384
+// keys 57 / 92, 4 rows of 4 heads, 4096 keys 25.0 / 28.7, 1024 keys 14.1 / 12.6.
+SplitPlan kv8_plan(int32_t rows, int32_t Hq, int32_t H, int32_t doc_len, const pp_options* opt,
+                   bool decode) {
+  const int64_t items = pp::kv8_items(rows, Hq / H, H, decode).items;
+  const bool asked = opt && (opt->splits > 0 || opt->debug_inject_timeout);
+  if (rows == 0 || doc_len == 0 || (!asked && doc_len <= 3000 && items * doc_len <= 400000))
+    return SplitPlan{};
+  int ctas = asked && opt->splits > 0 ? opt->splits : sm_count();
   SplitPlan p{};
   p.T = (doc_len + pp::kBN - 1) / pp::kBN + pp::kKv8Lead;
   p.G = (rows * (Hq / H) + pp::kGroupRows - 1) / pp::kGroupRows;
   p.units = p.G * H;
   p.W = (int64_t)p.units * p.T;
+  // few units: not so many parts that joining them takes longer than a part
+  // (16384 keys, one row: 56 us in 148 parts, 31 in 16, 37 in 8; 4096 keys, 4
+  // rows: 25, 24 and 21)
+  if (!asked) {
+    int parts = 1;
+    while (parts * parts < 2 * p.T) ++parts;
+    ctas = (int)std::min<int64_t>(ctas, (int64_t)parts * p.units);
+  }
   p.C = (int32_t)std::min<int64_t>(std::max(ctas, 0), p.W);
   if (p.C < 1) return SplitPlan{};
   // a unit's steps lie in at most this many CTAs' ranges of floor(W / C) or one more
@@ -389,7 +402,7 @@ pp_status kv8_attend(const pp_kv8_layer* L, int32_t doc_len, const uint16_t* q, 
   if ((int64_t)rows * Hq > INT32_MAX - 256) return PP_ERR_UNSUPPORTED;
   const int sms = sm_count();
   if (sms < 1) return PP_ERR_CUDA;
-  const SplitPlan plan = kv8_plan(rows, Hq, L->H, doc_len, opt);
+  const SplitPlan plan = kv8_plan(rows, Hq, L->H, doc_len, opt, decode);
   const bool doc_pass = plan.C > 0;
   const WsLayout w = kv8_ws_layout(plan, L->d);
   if (w.total > 0 && (!ws || !aligned(ws, kAlign))) return PP_ERR_INVALID_ARG;
@@ -414,10 +427,10 @@ pp_status kv8_attend(const pp_kv8_layer* L, int32_t doc_len, const uint16_t* q, 
 }
 
 size_t kv8_workspace(int32_t rows, int32_t Hq, int32_t H, int32_t d, int32_t doc_len,
-                     const pp_options* opt) {
+                     const pp_options* opt, bool decode) {
   if (rows < 0 || H < 1 || Hq < 1 || Hq % H != 0 || (d != 64 && d != 128) || doc_len < 0) return 0;
   if ((int64_t)rows * Hq > INT32_MAX - 256) return 0;
-  return kv8_ws_layout(kv8_plan(rows, Hq, H, doc_len, opt), d).total;
+  return kv8_ws_layout(kv8_plan(rows, Hq, H, doc_len, opt, decode), d).total;
 }
 
 // Host copy of a plan for the split-plan test aids.
@@ -561,12 +574,12 @@ PP_API pp_status pp_kv8_append(const pp_kv8_layer* layer, const uint16_t* k, int
 
 PP_API size_t pp_kv8_decode_workspace_bytes(int32_t P, int32_t Hq, int32_t H, int32_t d,
                                             int32_t doc_len, const pp_options* opt) {
-  return kv8_workspace(P, Hq, H, d, doc_len, opt);
+  return kv8_workspace(P, Hq, H, d, doc_len, opt, true);
 }
 
 PP_API size_t pp_kv8_prefill_workspace_bytes(int32_t R, int32_t Hq, int32_t H, int32_t d,
                                              int32_t doc_len, const pp_options* opt) {
-  return kv8_workspace(R, Hq, H, d, doc_len, opt);
+  return kv8_workspace(R, Hq, H, d, doc_len, opt, false);
 }
 
 PP_API pp_status pp_kv8_decode_attn(const pp_kv8_layer* layer, int32_t doc_len, const uint16_t* q,

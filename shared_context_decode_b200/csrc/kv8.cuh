@@ -74,4 +74,21 @@ __device__ __forceinline__ int page_of(int32_t entry, int n_pages) {
 // CTA of step kKv8Lead.
 constexpr int kKv8Lead = 4;
 
+// How the segment pass groups (query row, query head) pairs that share a key head
+// into a warp's item.  A decode step's rows belong to different streams, an item
+// each; question rows share their segment, so 16 pairs go together.
+struct Kv8Items {
+  int most, hg, gt, rt;   // pairs at most, heads, items per key head's group, rows
+  int64_t items;
+};
+inline Kv8Items kv8_items(int rows, int g, int H, bool one_row_per_stream) {
+  Kv8Items x;
+  x.most = one_row_per_stream && g <= 8 ? 8 : 16;
+  x.hg = g < x.most ? g : x.most;
+  x.gt = (g + x.hg - 1) / x.hg;
+  x.rt = one_row_per_stream ? 1 : x.most / x.hg;
+  x.items = (int64_t)((rows + x.rt - 1) / x.rt) * H * x.gt;
+  return x;
+}
+
 }  // namespace pp

@@ -716,14 +716,12 @@ cudaError_t launch_kv8_attn(const pp_kv8_layer& L, int doc_len, const uint16_t* 
   p.q = q; p.q_ld = q_ld;
   p.Hq = Hq;
   p.g = Hq / L.H;
-  // A decode step's rows belong to different streams, an item each; question
-  // rows share their segment, so 16 (row, head) pairs go together.
-  const int most = one_row_per_stream && p.g <= 8 ? 8 : 16;
-  p.hg = p.g < most ? p.g : most;
-  p.gt = (p.g + p.hg - 1) / p.hg;
-  p.rt = one_row_per_stream ? 1 : most / p.hg;
+  const Kv8Items it = kv8_items(rows, p.g, L.H, one_row_per_stream);
+  p.hg = it.hg;
+  p.gt = it.gt;
+  p.rt = it.rt;
   p.rows = rows;
-  const int64_t items = (int64_t)((rows + p.rt - 1) / p.rt) * L.H * p.gt;
+  const int64_t items = it.items;
   if (items > 0x7fffffff / 16) return cudaErrorInvalidValue;
   p.n_items = (int)items;
   p.q_sid = q_sid; p.q_pos = q_pos;
@@ -743,8 +741,8 @@ cudaError_t launch_kv8_attn(const pp_kv8_layer& L, int doc_len, const uint16_t* 
     ways *= 2;
   p.ways = ways;
   p.lper = L.page == 16 ? 0 : L.page == 32 ? 1 : L.page == 64 ? 2 : 3;
-  if (L.d == 128) return most == 8 ? launch<128, 1>(p, st) : launch<128, 2>(p, st);
-  return most == 8 ? launch<64, 1>(p, st) : launch<64, 2>(p, st);
+  if (L.d == 128) return it.most == 8 ? launch<128, 1>(p, st) : launch<128, 2>(p, st);
+  return it.most == 8 ? launch<64, 1>(p, st) : launch<64, 2>(p, st);
 }
 
 }  // namespace pp

@@ -48,40 +48,45 @@ SHAPES = [
 ]
 
 
+# splits: the document pass is taken, however small the work
+@pytest.mark.parametrize("splits", [0, 37])
 @pytest.mark.parametrize("H,g,d,page,N,P", SHAPES)
-def test_decode(H, g, d, page, N, P):
+def test_decode(H, g, d, page, N, P, splits):
+    opt = pp().Options(splits=splits)
     rng = np.random.default_rng(N + P)
     lens = [int(x) for x in rng.integers(1, 90, P)]
     layer, doc, segs = make_cache(H, d, page, N, lens, seed=N)
     sid = [s + 1 for s in rng.permutation(P)]
     pos = [N + lens[s - 1] - 1 for s in sid]
-    run(layer, doc, segs, N, sid, pos, g, "decode", pad=1)
+    run(layer, doc, segs, N, sid, pos, g, "decode", opt=opt, pad=1)
     assert pp().kv8_device_status(layer) == 0
     sid[0] = -1                          # inactive rows, rows that see nothing of their segment
     if P > 2:
         sid[2] = -1
         pos[1] = N - 1
-    run(layer, doc, segs, N, sid, pos, g, "decode", seed=2)
-    run(layer, doc, segs, N, sid, pos, g, "decode", seed=3, doc_len=0)
+    run(layer, doc, segs, N, sid, pos, g, "decode", opt=opt, seed=2)
+    run(layer, doc, segs, N, sid, pos, g, "decode", opt=opt, seed=3, doc_len=0)
     if N > 3:                            # a document read in part
-        run(layer, doc, segs, N, sid, pos, g, "decode", seed=3, doc_len=N - 3)
+        run(layer, doc, segs, N, sid, pos, g, "decode", opt=opt, seed=3, doc_len=N - 3)
     assert pp().kv8_device_status(layer) == 0
 
 
+@pytest.mark.parametrize("splits", [0, 37])
 @pytest.mark.parametrize("H,g,d,page,N,P", SHAPES)
-def test_prefill(H, g, d, page, N, P):
+def test_prefill(H, g, d, page, N, P, splits):
+    opt = pp().Options(splits=splits)
     rng = np.random.default_rng(N + P)
     lens = [int(x) for x in rng.integers(1, 40, P)]
     layer, doc, segs = make_cache(H, d, page, N, lens, seed=N + 1)
     order = rng.permutation(P)
     sid = sum(([int(s) + 1] * lens[s] for s in order), [])
     pos = sum((list(range(N, N + lens[s])) for s in order), [])
-    run(layer, doc, segs, N, sid, pos, g, "prefill", pad=2)
+    run(layer, doc, segs, N, sid, pos, g, "prefill", opt=opt, pad=2)
     # any order, idle rows among them, a part of the rows only
     mix = rng.permutation(len(sid))[:max(1, len(sid) * 2 // 3)]
     sid, pos = [sid[i] if i % 7 else -1 for i in mix], [pos[i] for i in mix]
-    run(layer, doc, segs, N, sid, pos, g, "prefill", seed=4)
-    run(layer, doc, segs, N, sid, pos, g, "prefill", seed=5, doc_len=0)
+    run(layer, doc, segs, N, sid, pos, g, "prefill", opt=opt, seed=4)
+    run(layer, doc, segs, N, sid, pos, g, "prefill", opt=opt, seed=5, doc_len=0)
     assert pp().kv8_device_status(layer) == 0
 
 
@@ -91,8 +96,10 @@ def test_more_rows_than_one_group():
     layer, doc, segs = make_cache(2, 128, 32, 700, lens, seed=3)
     sid = sum(([s + 1] * 20 for s in range(30)), [])[:-7]
     pos = (list(range(700, 720)) * 30)[:-7]
-    run(layer, doc, segs, 700, sid, pos, 1, "prefill")
-    run(layer, doc, segs, 700, sid, pos, 3, "prefill")
+    for splits in (0, 5):
+        opt = pp().Options(splits=splits)
+        run(layer, doc, segs, 700, sid, pos, 1, "prefill", opt=opt)
+        run(layer, doc, segs, 700, sid, pos, 3, "prefill", opt=opt)
 
 
 def test_long_segments():
@@ -145,9 +152,9 @@ def test_pages_that_are_not_there_are_skipped(N):
     q = queries(2, 4, 128, 1)
     s, p = ids([1, 2], [N + 39, N + 19])
     n2 = int(keep.sum())
-    for fn in (m.kv8_decode_attn, m.kv8_prefill_attn):
+    for fn, splits in ((f, n) for f in (m.kv8_decode_attn, m.kv8_prefill_attn) for n in (0, 3)):
         lse = torch.zeros((2, 4), device=DEV)
-        o = fn(layer, N, q, s, p, 0.09, lse=lse)
+        o = fn(layer, N, q, s, p, 0.09, lse=lse, opt=m.Options(splits=splits))
         torch.cuda.synchronize()
         assert m.kv8_device_status(layer) == m.PP_DEV_BAD_PAGE
         m.kv8_reset(layer)
@@ -155,9 +162,10 @@ def test_pages_that_are_not_there_are_skipped(N):
         check(o, lse, ref)
 
 
+@pytest.mark.parametrize("splits", [0, 2])
 @pytest.mark.parametrize("N", [40, 900])
 @pytest.mark.parametrize("kind", ["decode", "prefill"])
-def test_nan_reaches_the_rows_that_see_it_and_no_others(N, kind):
+def test_nan_reaches_the_rows_that_see_it_and_no_others(N, kind, splits):
     m = pp()
     layer, doc, segs = make_cache(2, 64, 32, N, [30, 30, 30], seed=9)
     fn = m.kv8_decode_attn if kind == "decode" else m.kv8_prefill_attn
@@ -167,7 +175,7 @@ def test_nan_reaches_the_rows_that_see_it_and_no_others(N, kind):
 
     def go():
         lse = torch.zeros((3, 4), device=DEV)
-        o = fn(layer, N, q, s, p, scale, lse=lse)
+        o = fn(layer, N, q, s, p, scale, lse=lse, opt=m.Options(splits=splits))
         torch.cuda.synchronize()
         return o, lse
 
@@ -189,9 +197,10 @@ def test_nan_reaches_the_rows_that_see_it_and_no_others(N, kind):
     assert not o[0, 2:].isnan().any() and not o[2, 2:].isnan().any()
 
 
+@pytest.mark.parametrize("splits", [0, 2])
 @pytest.mark.parametrize("N", [0, 40, 900])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
-def test_non_finite_queries_give_nan_in_their_row(N, bad):
+def test_non_finite_queries_give_nan_in_their_row(N, bad, splits):
     m = pp()
     layer, doc, segs = make_cache(2, 64, 32, N, [30, 30, 30], seed=9)
     q = queries(3, 4, 64, 1)
@@ -199,15 +208,16 @@ def test_non_finite_queries_give_nan_in_their_row(N, bad):
     s, p = ids([1, 2, 3], [N + 19, N + 20, N + 29])
     for fn in (m.kv8_decode_attn, m.kv8_prefill_attn):
         lse = torch.zeros((3, 4), device=DEV)
-        o = fn(layer, N, q, s, p, 0.125, lse=lse)
+        o = fn(layer, N, q, s, p, 0.125, lse=lse, opt=m.Options(splits=splits))
         torch.cuda.synchronize()
         assert o[1, 2].isnan().all() and lse[1, 2].isnan()
         o[1, 2], lse[1, 2] = 0, 0
         assert not o.isnan().any() and not lse.isnan().any()
 
 
+@pytest.mark.parametrize("splits", [0, 3])
 @pytest.mark.parametrize("d,N", [(64, 100), (128, 1500)])
-def test_scales_far_apart_and_large_scores(d, N):
+def test_scales_far_apart_and_large_scores(d, N, splits):
     """Pages 2^-30 to 2^30 apart in value scale; keys large enough that one key
     takes all the weight."""
     m = pp()
@@ -228,7 +238,7 @@ def test_scales_far_apart_and_large_scores(d, N):
     q = queries(2, 3, d, 1)
     s, p = ids([1, 2], [N + 49, N + 19])
     lse = torch.zeros((2, 3), device=DEV)
-    o = m.kv8_decode_attn(layer, N, q, s, p, d ** -0.5, lse=lse)
+    o = m.kv8_decode_attn(layer, N, q, s, p, d ** -0.5, lse=lse, opt=m.Options(splits=splits))
     torch.cuda.synchronize()
     ro, rl, ra = oracle_attn(doc, segs, N, q.cpu(), np.array([1, 2]), np.array([N + 49, N + 19]), d ** -0.5)
     # scores reach |q||k| scale ~ 600: their fp32 sums err by up to 2^-24 * 128
@@ -346,7 +356,7 @@ def test_injected_timeout_reports_status_and_recovers(d):
     torch.cuda.synchronize()
     assert m.kv8_device_status(layer) & m.PP_DEV_TIMEOUT
     m.kv8_reset(layer)
-    run(layer, doc, segs, N, sid, pos, 1, "decode")
+    run(layer, doc, segs, N, sid, pos, 1, "decode", opt=m.Options(splits=60))
     assert m.kv8_device_status(layer) == 0
 
 
