@@ -386,7 +386,8 @@ typedef struct pp_rope {
 pp_status pp_kv8_reset(const pp_kv8_layer *layer, void *stream);
 
 /*
- * Append n rows: rotate the keys, quantise keys and values, one launch.
+ * What pp_kv8_append takes (a block of arguments: these calls run in a few
+ * microseconds, and a dozen separate ones cost a binding two of them).
  *   k, v   bf16, row i at k + i * k_ld, heads packed [H][d]; lds are multiples
  *          of 8 and at least H * d (slices of a fused projection do)
  *   q      NULL, or bf16 rows of Hq query heads to rotate with them into
@@ -394,6 +395,18 @@ pp_status pp_kv8_reset(const pp_kv8_layer *layer, void *stream);
  *   sid    int16 [n]: 0 document, 1..P_max a stream, < 0 a row to skip
  *   pos    int32 [n]
  *   rope   NULL: no rotation (q is copied)
+ */
+typedef struct pp_kv8_append_args {
+    uint16_t *k, *v, *q, *q_out;
+    int64_t k_ld, v_ld, q_ld, q_out_ld;
+    int16_t *sid;
+    int32_t *pos;
+    pp_rope *rope;
+    int32_t Hq, n;
+} pp_kv8_append_args;
+
+/*
+ * Append n rows: rotate the keys, quantise keys and values, one launch.
  * In one call the rows of a stream stand next to each other at consecutive
  * positions; the first run of a stream counts, and a row that breaks this is
  * dropped and sets PP_DEV_ROW_ORDER.  Per page and head, with A the largest
@@ -409,10 +422,7 @@ pp_status pp_kv8_reset(const pp_kv8_layer *layer, void *stream);
  * q_out with sid < 0, sid > P_max or a position outside the angles stay as
  * they were.  The same call repeated writes the same bytes.
  */
-pp_status pp_kv8_append(const pp_kv8_layer *layer, const uint16_t *k, int64_t k_ld,
-                        const uint16_t *v, int64_t v_ld, const uint16_t *q, int64_t q_ld,
-                        int32_t Hq, const int16_t *sid, const int32_t *pos, int32_t n,
-                        const pp_rope *rope, uint16_t *q_out, int64_t q_out_ld, void *stream);
+pp_status pp_kv8_append(const pp_kv8_layer *layer, const pp_kv8_append_args *args, void *stream);
 
 /*
  * Workspace bytes of the calls below (0: none needed).  They depend on the SM
@@ -424,32 +434,48 @@ size_t pp_kv8_prefill_workspace_bytes(int32_t R, int32_t Hq, int32_t H, int32_t 
                                       const pp_options *opt);
 
 /*
- * Attention over the 8-bit cache: pp_kv8_decode_attn for a decode step (one
- * row per stream, P <= P_max), pp_kv8_prefill_attn for question rows in any
- * order.  Both give the same results; they differ in how rows are grouped.
+ * What the attention calls take.
  *   q      bf16 rows of Hq query heads, q_ld elements apart, already rotated;
  *          Hq a multiple of H, query heads j * (Hq/H) .. belong to key head j
- *   q_sid  int16: stream of row i (1..P_max), or -1 for an inactive row
- *   q_pos  int32: position of row i; it sees the document (tokens
+ *   q_sid  int16 [rows]: stream of row i (1..P_max), or -1 for an inactive row
+ *   q_pos  int32 [rows]: position of row i; it sees the document (tokens
  *          0..doc_len-1) and slots 0 .. q_pos - pos0 of its own segment (none
  *          when q_pos < pos0)
- *   scale  softmax scale, finite and > 0
  *   o      bf16 [rows][Hq][d];  lse  fp32 [rows][Hq] or NULL
- *   opt    splits, debug_inject_timeout, wait_limit_log2 and events apply; the
- *          comparison modes and suffix_slices are refused
+ *   ws     workspace of ws_bytes, 256-byte aligned
+ *   opt    NULL, or: splits (the document pass's CTAs; given, the pass is taken
+ *          however small the work), debug_inject_timeout, wait_limit_log2 and
+ *          events apply; the comparison modes and suffix_slices are refused
+ *   scale  softmax scale, finite and > 0
+ */
+typedef struct pp_kv8_attn_args {
+    uint16_t *q;
+    int64_t q_ld;
+    int16_t *q_sid;
+    int32_t *q_pos;
+    uint16_t *o;
+    float *lse;
+    void *ws;
+    size_t ws_bytes;
+    pp_options *opt;
+    int32_t Hq, rows, doc_len;
+    float scale;
+} pp_kv8_attn_args;
+
+/*
+ * Attention over the 8-bit cache: pp_kv8_decode_attn for a decode step (one
+ * row per stream, rows <= P_max), pp_kv8_prefill_attn for question rows in any
+ * order.  Both give the same results; they differ in how rows are grouped.
  * Rows that see nothing, inactive rows and rows of stream 0 or > P_max (which
  * set PP_DEV_BAD_STREAM) get o = 0 and lse = -inf.  Keys on a page that is
  * not there are skipped (PP_DEV_BAD_PAGE).  A query with a NaN or infinity
- * gives NaN.
+ * gives NaN.  A workspace serves one call in flight; calls ordered on one
+ * stream may share it.
  */
-pp_status pp_kv8_decode_attn(const pp_kv8_layer *layer, int32_t doc_len, const uint16_t *q,
-                             int64_t q_ld, int32_t Hq, const int16_t *q_sid, const int32_t *q_pos,
-                             int32_t P, float scale, uint16_t *o, float *lse, void *ws,
-                             size_t ws_bytes, const pp_options *opt, void *stream);
-pp_status pp_kv8_prefill_attn(const pp_kv8_layer *layer, int32_t doc_len, const uint16_t *q,
-                              int64_t q_ld, int32_t Hq, const int16_t *q_sid, const int32_t *q_pos,
-                              int32_t R, float scale, uint16_t *o, float *lse, void *ws,
-                              size_t ws_bytes, const pp_options *opt, void *stream);
+pp_status pp_kv8_decode_attn(const pp_kv8_layer *layer, const pp_kv8_attn_args *args,
+                             void *stream);
+pp_status pp_kv8_prefill_attn(const pp_kv8_layer *layer, const pp_kv8_attn_args *args,
+                              void *stream);
 
 /* As pp_get_device_status, for an 8-bit layer (synchronises). */
 pp_status pp_kv8_get_device_status(const pp_kv8_layer *layer, int32_t *h_status, void *stream);

@@ -355,40 +355,38 @@ WsLayout kv8_ws_layout(const SplitPlan& p, int d) {
   return w;
 }
 
-pp_status kv8_append(const pp_kv8_layer* L, const uint16_t* k, int64_t k_ld, const uint16_t* v,
-                     int64_t v_ld, const uint16_t* q, int64_t q_ld, int32_t Hq, const int16_t* sid,
-                     const int32_t* pos, int32_t n, const pp_rope* rope, uint16_t* q_out,
-                     int64_t qo_ld, void* stream) {
+pp_status kv8_append(const pp_kv8_layer* L, const pp_kv8_append_args* a, void* stream) {
   pp_status s = check_kv8_layer(L);
   if (s != PP_OK) return s;
-  if (n < 0) return PP_ERR_INVALID_ARG;
+  if (!a || a->n < 0) return PP_ERR_INVALID_ARG;
+  const pp_rope* rope = a->rope;
   if (rope) {
     if (rope->dim < 0 || rope->max_pos < 1 || !rope->cos_sin || !aligned(rope->cos_sin, 16))
       return PP_ERR_INVALID_ARG;
     if (rope->dim == 0 || rope->dim % 16 != 0 || rope->dim > L->d) return PP_ERR_UNSUPPORTED;
     if (rope->interleaved != 0 && rope->interleaved != 1) return PP_ERR_INVALID_ARG;
   }
-  if (n == 0) return PP_OK;
-  if (!row_operand(k, k_ld, L->H, L->d) || !row_operand(v, v_ld, L->H, L->d) || !sid || !pos ||
-      !aligned(sid, 2) || !aligned(pos, 4))
+  if (a->n == 0) return PP_OK;
+  if (!row_operand(a->k, a->k_ld, L->H, L->d) || !row_operand(a->v, a->v_ld, L->H, L->d) ||
+      !a->sid || !a->pos || !aligned(a->sid, 2) || !aligned(a->pos, 4))
     return PP_ERR_INVALID_ARG;
-  if (!q != !q_out) return PP_ERR_INVALID_ARG;
-  if (q && (Hq < 1 || Hq > (1 << 20) || !row_operand(q, q_ld, Hq, L->d) ||
-            !row_operand(q_out, qo_ld, Hq, L->d)))
+  if (!a->q != !a->q_out) return PP_ERR_INVALID_ARG;
+  if (a->q && (a->Hq < 1 || a->Hq > (1 << 20) || !row_operand(a->q, a->q_ld, a->Hq, L->d) ||
+               !row_operand(a->q_out, a->q_out_ld, a->Hq, L->d)))
     return PP_ERR_INVALID_ARG;
   if (L->H > (1 << 17)) return PP_ERR_UNSUPPORTED;
   const int sms = sm_count();
   if (sms < 1) return PP_ERR_CUDA;
-  return from_cuda(pp::launch_kv8_append(*L, k, k_ld, v, v_ld, q, q_ld, Hq, sid, pos, n, rope,
-                                         q_out, qo_ld, sms, static_cast<cudaStream_t>(stream)));
+  return from_cuda(pp::launch_kv8_append(*L, *a, sms, static_cast<cudaStream_t>(stream)));
 }
 
-pp_status kv8_attend(const pp_kv8_layer* L, int32_t doc_len, const uint16_t* q, int64_t q_ld,
-                     int32_t Hq, const int16_t* q_sid, const int32_t* q_pos, int32_t rows,
-                     float scale, uint16_t* o, float* lse, void* ws, size_t ws_bytes,
-                     const pp_options* opt, void* stream, bool decode) {
+pp_status kv8_attend(const pp_kv8_layer* L, const pp_kv8_attn_args* a, void* stream, bool decode) {
   pp_status s = check_kv8_layer(L);
   if (s != PP_OK) return s;
+  if (!a) return PP_ERR_INVALID_ARG;
+  const int32_t rows = a->rows, doc_len = a->doc_len, Hq = a->Hq;
+  const float scale = a->scale;
+  const pp_options* opt = a->opt;
   if (rows < 0 || doc_len < 0 || Hq < 1 || Hq % L->H != 0) return PP_ERR_INVALID_ARG;
   if (decode && rows > L->P_max) return PP_ERR_UNSUPPORTED;
   if ((int64_t)doc_len > (int64_t)L->doc_pages * L->page) return PP_ERR_CAPACITY;
@@ -396,32 +394,35 @@ pp_status kv8_attend(const pp_kv8_layer* L, int32_t doc_len, const uint16_t* q, 
     return PP_ERR_UNSUPPORTED;
   if (!(scale > 0.f) || scale > 3.4e38f) return PP_ERR_INVALID_ARG;
   if (rows == 0) return PP_OK;
-  if (!row_operand(q, q_ld, Hq, L->d) || !o || !aligned(o, 16) || (lse && !aligned(lse, 4)) ||
-      !q_sid || !q_pos || !aligned(q_sid, 2) || !aligned(q_pos, 4))
+  if (!row_operand(a->q, a->q_ld, Hq, L->d) || !a->o || !aligned(a->o, 16) ||
+      (a->lse && !aligned(a->lse, 4)) || !a->q_sid || !a->q_pos || !aligned(a->q_sid, 2) ||
+      !aligned(a->q_pos, 4))
     return PP_ERR_INVALID_ARG;
   if ((int64_t)rows * Hq > INT32_MAX - 256) return PP_ERR_UNSUPPORTED;
   const int sms = sm_count();
   if (sms < 1) return PP_ERR_CUDA;
   const SplitPlan plan = kv8_plan(rows, Hq, L->H, doc_len, opt, decode);
   const bool doc_pass = plan.C > 0;
+  // both kernels count in 32 bits
+  if (plan.W > INT32_MAX ||
+      pp::kv8_items(rows, Hq / L->H, L->H, decode).items > INT32_MAX / 16)
+    return PP_ERR_UNSUPPORTED;
   const WsLayout w = kv8_ws_layout(plan, L->d);
-  if (w.total > 0 && (!ws || !aligned(ws, kAlign))) return PP_ERR_INVALID_ARG;
-  if (ws_bytes < w.total) return PP_ERR_CAPACITY;
-  const Partials part = carve(ws, w);
+  if (w.total > 0 && (!a->ws || !aligned(a->ws, kAlign))) return PP_ERR_INVALID_ARG;
+  if (a->ws_bytes < w.total) return PP_ERR_CAPACITY;
+  const Partials part = carve(a->ws, w);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaEvent_t* ev = (opt && opt->events) ? reinterpret_cast<cudaEvent_t*>(opt->events) : nullptr;
   cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
   if (ev && cudaStreamIsCapturing(st, &cap) != cudaSuccess) return PP_ERR_CUDA;
   auto mark = [&](int i) { return ev ? record_mark(ev[i], cap, st) : cudaSuccess; };
   if (mark(0) != cudaSuccess) return PP_ERR_CUDA;
-  if (doc_pass && (s = from_cuda(pp::launch_kv8_doc(*L, doc_len, q, q_ld, Hq, rows, scale, plan,
-                                                    part, wait_limit(opt),
+  if (doc_pass && (s = from_cuda(pp::launch_kv8_doc(*L, *a, plan, part, wait_limit(opt),
                                                     opt ? opt->debug_inject_timeout : 0, st))) !=
                       PP_OK)
     return s;
   if (mark(1) != cudaSuccess) return PP_ERR_CUDA;
-  if ((s = from_cuda(pp::launch_kv8_attn(*L, doc_len, q, q_ld, Hq, q_sid, q_pos, rows, decode,
-                                         scale, plan, doc_pass, part, o, lse, sms, st))) != PP_OK)
+  if ((s = from_cuda(pp::launch_kv8_attn(*L, *a, decode, plan, doc_pass, part, sms, st))) != PP_OK)
     return s;
   return from_cuda(mark(2));
 }
@@ -562,14 +563,10 @@ PP_API pp_status pp_kv8_reset(const pp_kv8_layer* layer, void* stream) {
   return from_cuda(pp::launch_kv8_reset(*layer, static_cast<cudaStream_t>(stream)));
 }
 
-PP_API pp_status pp_kv8_append(const pp_kv8_layer* layer, const uint16_t* k, int64_t k_ld,
-                               const uint16_t* v, int64_t v_ld, const uint16_t* q, int64_t q_ld,
-                               int32_t Hq, const int16_t* sid, const int32_t* pos, int32_t n,
-                               const pp_rope* rope, uint16_t* q_out, int64_t q_out_ld,
+PP_API pp_status pp_kv8_append(const pp_kv8_layer* layer, const pp_kv8_append_args* args,
                                void* stream) {
   NvtxRange nvtx_range("pp_kv8_append");
-  return kv8_append(layer, k, k_ld, v, v_ld, q, q_ld, Hq, sid, pos, n, rope, q_out, q_out_ld,
-                    stream);
+  return kv8_append(layer, args, stream);
 }
 
 PP_API size_t pp_kv8_decode_workspace_bytes(int32_t P, int32_t Hq, int32_t H, int32_t d,
@@ -582,24 +579,16 @@ PP_API size_t pp_kv8_prefill_workspace_bytes(int32_t R, int32_t Hq, int32_t H, i
   return kv8_workspace(R, Hq, H, d, doc_len, opt, false);
 }
 
-PP_API pp_status pp_kv8_decode_attn(const pp_kv8_layer* layer, int32_t doc_len, const uint16_t* q,
-                                    int64_t q_ld, int32_t Hq, const int16_t* q_sid,
-                                    const int32_t* q_pos, int32_t P, float scale, uint16_t* o,
-                                    float* lse, void* ws, size_t ws_bytes, const pp_options* opt,
+PP_API pp_status pp_kv8_decode_attn(const pp_kv8_layer* layer, const pp_kv8_attn_args* args,
                                     void* stream) {
   NvtxRange nvtx_range("pp_kv8_decode_attn");
-  return kv8_attend(layer, doc_len, q, q_ld, Hq, q_sid, q_pos, P, scale, o, lse, ws, ws_bytes, opt,
-                    stream, true);
+  return kv8_attend(layer, args, stream, true);
 }
 
-PP_API pp_status pp_kv8_prefill_attn(const pp_kv8_layer* layer, int32_t doc_len, const uint16_t* q,
-                                     int64_t q_ld, int32_t Hq, const int16_t* q_sid,
-                                     const int32_t* q_pos, int32_t R, float scale, uint16_t* o,
-                                     float* lse, void* ws, size_t ws_bytes, const pp_options* opt,
+PP_API pp_status pp_kv8_prefill_attn(const pp_kv8_layer* layer, const pp_kv8_attn_args* args,
                                      void* stream) {
   NvtxRange nvtx_range("pp_kv8_prefill_attn");
-  return kv8_attend(layer, doc_len, q, q_ld, Hq, q_sid, q_pos, R, scale, o, lse, ws, ws_bytes, opt,
-                    stream, false);
+  return kv8_attend(layer, args, stream, false);
 }
 
 PP_API pp_status pp_kv8_get_device_status(const pp_kv8_layer* layer, int32_t* h_status,

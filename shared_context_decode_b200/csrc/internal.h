@@ -84,20 +84,14 @@ cudaError_t launch_visibility(const pp_kv_layer& L, int doc_len, const int16_t* 
 // query rows over the streams' segments -- and, without a document pass, over
 // the document -- with the merge; status reset.  ld: elements between rows.
 cudaError_t launch_kv8_reset(const pp_kv8_layer& L, cudaStream_t st);
-cudaError_t launch_kv8_append(const pp_kv8_layer& L, const uint16_t* k, int64_t k_ld,
-                              const uint16_t* v, int64_t v_ld, const uint16_t* q, int64_t q_ld,
-                              int Hq, const int16_t* sid, const int32_t* pos, int n,
-                              const pp_rope* rope, uint16_t* q_out, int64_t qo_ld, int num_sms,
+cudaError_t launch_kv8_append(const pp_kv8_layer& L, const pp_kv8_append_args& a, int num_sms,
                               cudaStream_t st);
-cudaError_t launch_kv8_doc(const pp_kv8_layer& L, int doc_len, const uint16_t* q, int64_t q_ld,
-                           int Hq, int rows, float scale, const SplitPlan& plan,
+cudaError_t launch_kv8_doc(const pp_kv8_layer& L, const pp_kv8_attn_args& a, const SplitPlan& plan,
                            const Partials& part, long long wait_limit, int inject_timeout,
                            cudaStream_t st);
-cudaError_t launch_kv8_attn(const pp_kv8_layer& L, int doc_len, const uint16_t* q, int64_t q_ld,
-                            int Hq, const int16_t* q_sid, const int32_t* q_pos, int rows,
-                            bool one_row_per_stream, float scale, const SplitPlan& plan,
-                            bool doc_pass, const Partials& part, uint16_t* o, float* lse,
-                            int num_sms, cudaStream_t st);
+cudaError_t launch_kv8_attn(const pp_kv8_layer& L, const pp_kv8_attn_args& a,
+                            bool one_row_per_stream, const SplitPlan& plan, bool doc_pass,
+                            const Partials& part, int num_sms, cudaStream_t st);
 
 cudaError_t launch_exp2(const float* x, float* y_poly, float* y_hw, int n, cudaStream_t st);
 

@@ -581,23 +581,21 @@ cudaError_t launch_kv8_reset(const pp_kv8_layer& L, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-cudaError_t launch_kv8_append(const pp_kv8_layer& L, const uint16_t* k, int64_t k_ld,
-                              const uint16_t* v, int64_t v_ld, const uint16_t* q, int64_t q_ld,
-                              int Hq, const int16_t* sid, const int32_t* pos, int n,
-                              const pp_rope* rope, uint16_t* q_out, int64_t qo_ld, int num_sms,
+cudaError_t launch_kv8_append(const pp_kv8_layer& L, const pp_kv8_append_args& a, int num_sms,
                               cudaStream_t st) {
   AppendParams p{};
+  const int n = a.n, Hq = a.q ? a.Hq : 0;
   p.L = L;
-  p.k = k; p.v = v; p.q = q; p.q_out = q_out;
-  p.k_ld = k_ld; p.v_ld = v_ld; p.q_ld = q_ld; p.qo_ld = qo_ld;
-  p.Hq = q ? Hq : 0;
+  p.k = a.k; p.v = a.v; p.q = a.q; p.q_out = a.q_out;
+  p.k_ld = a.k_ld; p.v_ld = a.v_ld; p.q_ld = a.q_ld; p.qo_ld = a.q_out_ld;
+  p.Hq = Hq;
   p.n = n;
-  p.sid = sid; p.pos = pos;
-  if (rope) {
-    p.cos_sin = rope->cos_sin;
-    p.rot = rope->dim;
-    p.interleaved = rope->interleaved;
-    p.max_pos = rope->max_pos;
+  p.sid = a.sid; p.pos = a.pos;
+  if (a.rope) {
+    p.cos_sin = a.rope->cos_sin;
+    p.rot = a.rope->dim;
+    p.interleaved = a.rope->interleaved;
+    p.max_pos = a.rope->max_pos;
   }
   // A CTA looks after a window of rows for a share of the heads.  Windows are
   // long (most rows of a long run are no leaders, and a CTA that only finds
@@ -617,8 +615,7 @@ cudaError_t launch_kv8_append(const pp_kv8_layer& L, const uint16_t* k, int64_t 
   // for long calls
   p.ys = passes;
   while (p.ys > 1 && wins * (p.ys / 2) >= 16LL * num_sms) p.ys = (p.ys + 1) / 2;
-  int qs = q ? (Hq + 15) / 16 : 0;
-  if (q && p.win > 4) qs = (Hq + 31) / 32;
+  const int qs = p.win > 4 ? (Hq + 31) / 32 : (Hq + 15) / 16;
   const dim3 grid((unsigned)wins, p.ys + qs);
   if (L.d == 128)
     return brief        ? start<128, 4, true>(p, grid, st)

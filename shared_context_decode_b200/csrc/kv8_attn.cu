@@ -706,32 +706,30 @@ cudaError_t launch(const Attn8Params& p, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_kv8_attn(const pp_kv8_layer& L, int doc_len, const uint16_t* q, int64_t q_ld,
-                            int Hq, const int16_t* q_sid, const int32_t* q_pos, int rows,
-                            bool one_row_per_stream, float scale, const SplitPlan& plan,
-                            bool doc_pass, const Partials& part, uint16_t* o, float* lse,
-                            int num_sms, cudaStream_t st) {
+cudaError_t launch_kv8_attn(const pp_kv8_layer& L, const pp_kv8_attn_args& a,
+                            bool one_row_per_stream, const SplitPlan& plan, bool doc_pass,
+                            const Partials& part, int num_sms, cudaStream_t st) {
   Attn8Params p{};
+  const int rows = a.rows;
   p.L = L;
-  p.q = q; p.q_ld = q_ld;
-  p.Hq = Hq;
-  p.g = Hq / L.H;
+  p.q = a.q; p.q_ld = a.q_ld;
+  p.Hq = a.Hq;
+  p.g = a.Hq / L.H;
   const Kv8Items it = kv8_items(rows, p.g, L.H, one_row_per_stream);
   p.hg = it.hg;
   p.gt = it.gt;
   p.rt = it.rt;
   p.rows = rows;
   const int64_t items = it.items;
-  if (items > 0x7fffffff / 16) return cudaErrorInvalidValue;
   p.n_items = (int)items;
-  p.q_sid = q_sid; p.q_pos = q_pos;
-  p.doc_len = doc_pass ? 0 : doc_len;
-  p.sl2 = scale * kLog2e;
+  p.q_sid = a.q_sid; p.q_pos = a.q_pos;
+  p.doc_len = doc_pass ? 0 : a.doc_len;
+  p.sl2 = a.scale * kLog2e;
   p.has_doc = doc_pass ? 1 : 0;
   p.plan = plan;
   p.plan32 = (plan.W + 1) * plan.C <= 0xffffffffLL;
   p.doc_o = part.doc_o; p.doc_ml = part.doc_ml;
-  p.o = o; p.lse = lse;
+  p.o = a.o; p.lse = a.lse;
   // Warps per item: enough to fill the GPU when items are few (they share the
   // item's merge too, however short its keys), and a long segment cut so that
   // one item is not a CTA's whole tail.

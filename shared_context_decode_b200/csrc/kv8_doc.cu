@@ -707,20 +707,18 @@ cudaError_t launch(const Doc8Params& p, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_kv8_doc(const pp_kv8_layer& L, int doc_len, const uint16_t* q, int64_t q_ld,
-                           int Hq, int rows, float scale, const SplitPlan& plan,
+cudaError_t launch_kv8_doc(const pp_kv8_layer& L, const pp_kv8_attn_args& a, const SplitPlan& plan,
                            const Partials& part, long long wait_limit, int inject_timeout,
                            cudaStream_t st) {
   Doc8Params p{};
   p.L = L;
-  p.q = q; p.q_ld = q_ld;
-  p.g = Hq / L.H;
-  p.rows = rows * p.g;
-  p.doc_len = doc_len;
+  p.q = a.q; p.q_ld = a.q_ld;
+  p.g = a.Hq / L.H;
+  p.rows = a.rows * p.g;
+  p.doc_len = a.doc_len;
   p.plan = plan;
-  if (plan.W > INT32_MAX) return cudaErrorInvalidValue;
   p.steps = (int)plan.W;
-  p.sl2 = scale * kLog2e;
+  p.sl2 = a.scale * kLog2e;
   p.doc_o = part.doc_o; p.doc_ml = part.doc_ml;
   p.wait_limit = wait_limit;
   p.inject_timeout = inject_timeout;

@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -80,6 +81,16 @@ class RopeStruct(ctypes.Structure):
                 ("cos_sin", _vp)]
 
 
+# The argument blocks of the 8-bit calls, packed as the C structs lie in memory
+# (8-byte fields, then pairs of 4-byte ones: no padding); 0 is NULL.
+KV8_APPEND_FIELDS = ("k", "v", "q", "q_out", "k_ld", "v_ld", "q_ld", "q_out_ld", "sid", "pos",
+                     "rope", "Hq", "n")
+KV8_ATTN_FIELDS = ("q", "q_ld", "q_sid", "q_pos", "o", "lse", "ws", "ws_bytes", "opt", "Hq", "rows",
+                   "doc_len", "scale")
+_pack_append = struct.Struct("=4Q4q3Q2i").pack
+_pack_attn = struct.Struct("=Qq5Q2Q3if").pack
+
+
 _LP = ctypes.POINTER(LayerStruct)
 _LP8 = ctypes.POINTER(KV8LayerStruct)
 _OP = ctypes.POINTER(Options)
@@ -117,16 +128,12 @@ _reset_streams = _sig("pp_kv_reset_streams", _i32, _LP, _vp, _i32, _vp)
 _doc_ws = _sig("pp_doc_prefill_workspace_bytes", _sz, _i32, _i32, _i32, _OP)
 _doc_prefill = _sig("pp_doc_prefill_attn", _i32, _LP, _i32, _vp, ctypes.c_float, _vp, _vp, _vp,
                     _sz, _OP, _vp)
-_i64 = ctypes.c_int64
 _kv8_reset = _sig("pp_kv8_reset", _i32, _LP8, _vp)
-_kv8_append = _sig("pp_kv8_append", _i32, _LP8, _vp, _i64, _vp, _i64, _vp, _i64, _i32, _vp, _vp,
-                   _i32, ctypes.POINTER(RopeStruct), _vp, _i64, _vp)
+_kv8_append = _sig("pp_kv8_append", _i32, _LP8, ctypes.c_char_p, _vp)
 _kv8_dec_ws = _sig("pp_kv8_decode_workspace_bytes", _sz, _i32, _i32, _i32, _i32, _i32, _OP)
 _kv8_pre_ws = _sig("pp_kv8_prefill_workspace_bytes", _sz, _i32, _i32, _i32, _i32, _i32, _OP)
-_kv8_decode = _sig("pp_kv8_decode_attn", _i32, _LP8, _i32, _vp, _i64, _i32, _vp, _vp, _i32,
-                   ctypes.c_float, _vp, _vp, _vp, _sz, _OP, _vp)
-_kv8_prefill = _sig("pp_kv8_prefill_attn", _i32, _LP8, _i32, _vp, _i64, _i32, _vp, _vp, _i32,
-                    ctypes.c_float, _vp, _vp, _vp, _sz, _OP, _vp)
+_kv8_decode = _sig("pp_kv8_decode_attn", _i32, _LP8, ctypes.c_char_p, _vp)
+_kv8_prefill = _sig("pp_kv8_prefill_attn", _i32, _LP8, ctypes.c_char_p, _vp)
 _kv8_status = _sig("pp_kv8_get_device_status", _i32, _LP8, ctypes.POINTER(_i32), _vp)
 
 EXPORTED = ("pp_status_str", "pp_abi_version", "pp_kv_reset", "pp_kv_append",
@@ -496,7 +503,7 @@ class Rope:
         self.max_pos, self.dim = cos_sin.shape
         self.struct = RopeStruct(self.dim, int(self.interleaved), self.max_pos, 0,
                                  cos_sin.data_ptr())
-        self.ref = ctypes.byref(self.struct)
+        self.address = ctypes.addressof(self.struct)
 
     @classmethod
     def make(cls, max_pos: int, dim: int, theta: float = 10000.0, interleaved: bool = False,
@@ -546,16 +553,17 @@ def _want8(t: torch.Tensor, dtype, name: str, layer):
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _call8(fn, name: str, layer, *args):
     """fn(layer, *args, stream) on the layer's device and its current stream."""
-    cur = torch.cuda.current_device()
+    cur = _current_device()
     if cur != layer.index:
         with torch.cuda.device(layer.index):
             return _call8(fn, name, layer, *args)
-    stream = _raw_stream(cur) if _raw_stream else torch.cuda.current_stream(cur).cuda_stream
-    rc = fn(layer.ref, *args, stream)
+    rc = fn(layer.ref, *args,
+            _raw_stream(cur) if _raw_stream else torch.cuda.current_stream(cur).cuda_stream)
     if rc:
         raise PPError(rc, name)
 
@@ -574,18 +582,18 @@ def kv8_append(layer: KV8Layer, k: torch.Tensor, v: torch.Tensor, sid: torch.Ten
     well; returns q_out (new, given, or q itself)."""
     _want8(sid, _I16, "sid", layer)
     _want8(pos, _I32, "pos", layer)
-    if sid.dim() != 1 or pos.shape != sid.shape:
+    shape = sid.shape
+    if len(shape) != 1 or pos.shape != shape:
         raise ValueError("kv8_append: sid and pos must be [n]")
-    n, H, d = sid.shape[0], layer.H, layer.d
+    n, H, d = shape[0], layer.H, layer.d
     k_ld = _rows(k, "k", n, H, d, layer)
     v_ld = _rows(v, "v", n, H, d, layer)
-    rope_ref = None
+    rope_at = 0
     if rope is not None:
         if rope.index != layer.index:
             raise ValueError(f"rope must be on {layer.device}, got {rope.cos_sin.device}")
-        rope_ref = rope.ref
-    Hq = q_ld = qo_ld = 0
-    q_ptr = qo_ptr = None
+        rope_at = rope.address
+    Hq = q_ld = qo_ld = q_ptr = qo_ptr = 0
     if q is not None:
         if q.dim() != 3:
             raise ValueError("q must be [n, Hq, d]")
@@ -597,8 +605,9 @@ def kv8_append(layer: KV8Layer, k: torch.Tensor, v: torch.Tensor, sid: torch.Ten
         q_ptr, qo_ptr = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("kv8_append: q_out without q")
-    _call8(_kv8_append, "pp_kv8_append", layer, k.data_ptr(), k_ld, v.data_ptr(), v_ld, q_ptr, q_ld,
-           Hq, sid.data_ptr(), pos.data_ptr(), n, rope_ref, qo_ptr, qo_ld)
+    _call8(_kv8_append, "pp_kv8_append", layer,
+           _pack_append(k.data_ptr(), v.data_ptr(), q_ptr, qo_ptr, k_ld, v_ld, q_ld, qo_ld,
+                        sid.data_ptr(), pos.data_ptr(), rope_at, Hq, n))
     return q_out
 
 
@@ -615,28 +624,30 @@ def kv8_prefill_workspace_bytes(R: int, Hq: int, H: int, d: int, doc_len: int,
 def _kv8_attn(fn, name, layer, doc_len, q, q_sid, q_pos, scale, o, lse, ws, opt, ws_fn):
     _want8(q_sid, _I16, "q_sid", layer)
     _want8(q_pos, _I32, "q_pos", layer)
-    rows = q_sid.shape[0] if q_sid.dim() == 1 else -1
-    if q.dim() != 3 or rows < 0 or q_pos.shape != q_sid.shape:
+    shape, qshape = q_sid.shape, q.shape
+    if len(shape) != 1 or len(qshape) != 3 or q_pos.shape != shape:
         raise ValueError(f"{name}: q must be [rows, Hq, d], q_sid and q_pos [rows]")
-    Hq = q.shape[1]
+    rows, Hq = shape[0], qshape[1]
     q_ld = _rows(q, "q", rows, Hq, layer.d, layer)
     if o is None:
         o = torch.empty((rows, Hq, layer.d), dtype=_BF16, device=layer.device)
     _want8(o, _BF16, "o", layer)
-    if o.shape != q.shape:
+    if o.shape != qshape:
         raise ValueError(f"{name}: o must be [rows, Hq, d]")
-    lse_ptr = None
+    lse_at = 0
     if lse is not None:
         _want8(lse, _F32, "lse", layer)
         if lse.shape != (rows, Hq):
             raise ValueError(f"{name}: lse must be [rows, Hq]")
-        lse_ptr = lse.data_ptr()
+        lse_at = lse.data_ptr()
     if ws is None:
         with torch.cuda.device(layer.index):
             ws = workspace(ws_fn(rows, Hq, layer.H, layer.d, doc_len, opt), layer.device)
     _want8(ws, _U8, "ws", layer)
-    _call8(fn, name, layer, doc_len, q.data_ptr(), q_ld, Hq, q_sid.data_ptr(), q_pos.data_ptr(),
-           rows, scale, o.data_ptr(), lse_ptr, ws.data_ptr(), ws.numel(), _opts(opt))
+    _call8(fn, name, layer,
+           _pack_attn(q.data_ptr(), q_ld, q_sid.data_ptr(), q_pos.data_ptr(), o.data_ptr(), lse_at,
+                      ws.data_ptr(), ws.numel(), 0 if opt is None else ctypes.addressof(opt), Hq,
+                      rows, doc_len, scale))
     return o
 
 

@@ -57,15 +57,26 @@ def test_layer_checks(pp, kw, code):
 def append(pp, L=None, k=0x1000, k_ld=512, v=0x2000, v_ld=512, q=0x3000, q_ld=1024, Hq=8, sid=0x4000,
            pos=0x5000, n=3, rope=None, q_out=0x6000, qo_ld=1024):
     L = L if L is not None else fake(pp)
-    return pp._kv8_append(ctypes.byref(L), k, k_ld, v, v_ld, q, q_ld, Hq, sid, pos, n,
-                          None if rope is None else ctypes.byref(rope), q_out, qo_ld, None)
+    a = pp._pack_append(k, v, q, q_out, k_ld, v_ld, q_ld, qo_ld, sid, pos,
+                        0 if rope is None else ctypes.addressof(rope), Hq, n)
+    return pp._kv8_append(ctypes.byref(L), a, None)
 
 
 def attend(pp, fn, L=None, doc_len=500, q=0x1000, q_ld=1024, Hq=8, sid=0x2000, pos=0x3000, rows=4,
-           scale=0.1, o=0x4000, lse=None, ws=0x10000, ws_bytes=1 << 40, opt=None):
+           scale=0.1, o=0x4000, lse=0, ws=0x10000, ws_bytes=1 << 40, opt=None):
     L = L if L is not None else fake(pp)
-    return fn(ctypes.byref(L), doc_len, q, q_ld, Hq, sid, pos, rows, scale, o, lse, ws, ws_bytes,
-              None if opt is None else ctypes.byref(opt), None)
+    a = pp._pack_attn(q, q_ld, sid, pos, o, lse, ws, ws_bytes,
+                      0 if opt is None else ctypes.addressof(opt), Hq, rows, doc_len, scale)
+    return fn(ctypes.byref(L), a, None)
+
+
+def test_argument_blocks_match_the_header(pp):
+    assert list(pp.KV8_APPEND_FIELDS) == header_struct_fields("pp_kv8_append_args")
+    assert list(pp.KV8_ATTN_FIELDS) == header_struct_fields("pp_kv8_attn_args")
+    assert len(pp._pack_append(*range(13))) == 96 and len(pp._pack_attn(*range(13))) == 88
+    L = fake(pp)
+    assert pp._kv8_append(ctypes.byref(L), None, None) == pp.PP_ERR_INVALID_ARG
+    assert pp._kv8_decode(ctypes.byref(L), None, None) == pp.PP_ERR_INVALID_ARG
 
 
 def test_append_checks(pp):
@@ -74,9 +85,9 @@ def test_append_checks(pp):
     assert append(pp, n=-1) == bad
     assert append(pp, k=0x1008) == bad and append(pp, v=0) == bad
     assert append(pp, k_ld=511) == bad and append(pp, k_ld=504) == bad and append(pp, v_ld=516) == bad
-    assert append(pp, q=None) == bad and append(pp, q_out=None) == bad      # one without the other
+    assert append(pp, q=0) == bad and append(pp, q_out=0) == bad      # one without the other
     assert append(pp, q_ld=1016) == bad and append(pp, qo_ld=1000) == bad and append(pp, Hq=0) == bad
-    assert append(pp, sid=0x4001) == bad and append(pp, pos=None) == bad
+    assert append(pp, sid=0x4001) == bad and append(pp, pos=0) == bad
     R = pp.RopeStruct
     assert append(pp, rope=R(64, 0, 0, 0, 0x9000)) == bad                    # no positions
     assert append(pp, rope=R(64, 2, 10, 0, 0x9000)) == bad
@@ -95,8 +106,8 @@ def test_attention_checks(pp, which):
     assert attend(pp, fn, doc_len=513) == pp.PP_ERR_CAPACITY                 # 16 pages of 32
     assert attend(pp, fn, Hq=6) == bad and attend(pp, fn, Hq=0) == bad       # not a multiple of H
     assert attend(pp, fn, q=0x1004) == bad and attend(pp, fn, q_ld=1020) == bad
-    assert attend(pp, fn, q_ld=1016) == bad and attend(pp, fn, o=None) == bad
-    assert attend(pp, fn, sid=None) == bad and attend(pp, fn, lse=0x5002) == bad
+    assert attend(pp, fn, q_ld=1016) == bad and attend(pp, fn, o=0) == bad
+    assert attend(pp, fn, sid=0) == bad and attend(pp, fn, lse=0x5002) == bad
     for s in (0.0, -1.0, float("nan"), float("inf")):
         assert attend(pp, fn, scale=s) == bad
     for o in (pp.Options(ablation_doc_per_stream=1), pp.Options(sibling_scan=1),
