@@ -41,80 +41,51 @@ struct AppendParams {
   int ys;                            // CTAs along y for keys and values; the rest turn queries
 };
 
-// Eight consecutive dims of a row: 16 bytes of bf16 -> floats.
-__device__ __forceinline__ void unpack8(const uint4 w, float (&x)[8]) {
-  const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+// A lane's eight dims of a row, as two groups of four: dims that turn together
+// are a lane's own (j and j + rot/2, or neighbours when interleaved), so no
+// value crosses lanes and a lane needs four angles.
+struct LaneDims {
+  int a, b;        // first dims of the groups
+  bool turns;
+};
+__device__ __forceinline__ LaneDims lane_dims(const AppendParams& p, int u) {
+  const int hr = p.rot >> 3;              // lanes whose dims turn
+  const bool split = u < hr && !p.interleaved;
+  return {split ? u * 4 : u * 8, split ? (u + hr) * 4 : u * 8 + 4, u < hr};
+}
+
+// Two groups of four bf16 -> floats.
+__device__ __forceinline__ void unpack8(uint2 a, uint2 b, float (&x)[8]) {
+  const uint32_t w[4] = {a.x, a.y, b.x, b.y};
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
-    const float2 f = bf2_to_f2(a[c]);
+    const float2 f = bf2_to_f2(w[c]);
     x[2 * c] = f.x;
     x[2 * c + 1] = f.y;
   }
 }
 
-// The angles' cosines and sines a lane needs for its 8 dims (unit u of the
-// row): 8 pairs' when dim j turns with dim j + rot/2, 4 pairs' when 2j turns
-// with 2j + 1.
-__device__ __forceinline__ void load_angles(const AppendParams& p, int pos, int u, float (&cs)[8],
-                                            float (&sn)[8]) {
-  if (u * 8 >= p.rot) return;
-  const int half = p.rot >> 1;
-  const float* t = p.cos_sin + (int64_t)pos * p.rot;
-  if (p.interleaved) {
-    const float4 c = *reinterpret_cast<const float4*>(t + u * 4);
-    const float4 s = *reinterpret_cast<const float4*>(t + half + u * 4);
-    cs[0] = c.x; cs[1] = c.y; cs[2] = c.z; cs[3] = c.w;
-    sn[0] = s.x; sn[1] = s.y; sn[2] = s.z; sn[3] = s.w;
-  } else {
-    const int j = u * 8 < half ? u * 8 : u * 8 - half;
-#pragma unroll
-    for (int e = 0; e < 8; e += 4) {
-      const float4 c = *reinterpret_cast<const float4*>(t + j + e);
-      const float4 s = *reinterpret_cast<const float4*>(t + half + j + e);
-      cs[e] = c.x; cs[e + 1] = c.y; cs[e + 2] = c.z; cs[e + 3] = c.w;
-      sn[e] = s.x; sn[e + 1] = s.y; sn[e + 2] = s.z; sn[e + 3] = s.w;
-    }
-  }
-}
-
-// Rotations of 8 dims.  Every product and difference is rounded by itself (no
-// fused multiply-add), the result a plain fp32 evaluation of a cos - b sin
-// gives, so which e4m3 value a rotated key rounds to does not depend on the
-// compiler's contraction.
-__device__ __forceinline__ void turn_pairs(const float (&cs)[8], const float (&sn)[8],
-                                           float (&x)[8]) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float a = x[2 * j], b = x[2 * j + 1];
-    x[2 * j] = __fsub_rn(__fmul_rn(a, cs[j]), __fmul_rn(b, sn[j]));
-    x[2 * j + 1] = __fadd_rn(__fmul_rn(b, cs[j]), __fmul_rn(a, sn[j]));
-  }
-}
-// y: the other half's dims
-__device__ __forceinline__ void turn_halves(const float (&cs)[8], const float (&sn)[8], bool low,
-                                            float (&x)[8], const float (&y)[8]) {
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float c = __fmul_rn(x[e], cs[e]), s = __fmul_rn(y[e], sn[e]);
-    x[e] = low ? __fsub_rn(c, s) : __fadd_rn(c, s);
-  }
-}
-// The lane's 8 dims, the other half's by shuffle; all lanes of the warp call it.
-__device__ __forceinline__ void turn8(const AppendParams& p, int u, int lane, const float (&cs)[8],
-                                      const float (&sn)[8], float (&x)[8]) {
-  if (p.rot == 0) return;
-  const bool in = u * 8 < p.rot;
-  if (p.interleaved) {
-    if (in) turn_pairs(cs, sn, x);
-    return;
-  }
-  const int hu = p.rot >> 4;                       // units of a half
-  const bool low = u < hu;
-  const int other = in ? (low ? lane + hu : lane - hu) : lane;
+// Turn the lane's dims by position pos.  Every product and difference is
+// rounded by itself (no fused multiply-add), the result a plain fp32 evaluation
+// of a cos - b sin gives, so which e4m3 value a rotated key rounds to does not
+// depend on the compiler's contraction.
+__device__ __forceinline__ void turn8(const AppendParams& p, int pos, int u, float (&x)[8]) {
+  const float* t = p.cos_sin + (int64_t)pos * p.rot + u * 4;
+  const float4 c4 = __ldg(reinterpret_cast<const float4*>(t));
+  const float4 s4 = __ldg(reinterpret_cast<const float4*>(t + (p.rot >> 1)));
+  const float cs[4] = {c4.x, c4.y, c4.z, c4.w}, sn[4] = {s4.x, s4.y, s4.z, s4.w};
   float y[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) y[e] = __shfl_sync(0xffffffffu, x[e], other);
-  if (in) turn_halves(cs, sn, low, x, y);
+  for (int e = 0; e < 4; ++e) {
+    const float a = p.interleaved ? x[2 * e] : x[e], b = p.interleaved ? x[2 * e + 1] : x[4 + e];
+    y[e] = __fsub_rn(__fmul_rn(a, cs[e]), __fmul_rn(b, sn[e]));
+    y[4 + e] = __fadd_rn(__fmul_rn(b, cs[e]), __fmul_rn(a, sn[e]));
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    x[e] = p.interleaved ? y[(e & 1) * 4 + (e >> 1)] : y[e];
+    x[4 + e] = p.interleaved ? y[(e & 1) * 4 + 2 + (e >> 1)] : y[4 + e];
+  }
 }
 
 // Largest finite magnitude of 8 values, joined to a; any non-finite: bad.
@@ -128,12 +99,9 @@ __device__ __forceinline__ void amax8(const float (&x)[8], float& a, bool& bad) 
   }
 }
 
-// 8 values over a power-of-two scale -> 8 e4m3 bytes.
-__device__ __forceinline__ uint2 quant8(const float (&x)[8], float inv) {
-  uint2 r;
-  r.x = f2_to_e4m3x2(x[0] * inv, x[1] * inv) | (f2_to_e4m3x2(x[2] * inv, x[3] * inv) << 16);
-  r.y = f2_to_e4m3x2(x[4] * inv, x[5] * inv) | (f2_to_e4m3x2(x[6] * inv, x[7] * inv) << 16);
-  return r;
+// 4 values over a power-of-two scale -> 4 e4m3 bytes.
+__device__ __forceinline__ uint32_t quant4(float a, float b, float c, float d, float inv) {
+  return f2_to_e4m3x2(a * inv, b * inv) | (f2_to_e4m3x2(c * inv, d * inv) << 16);
 }
 
 // The slots [0, n) of one head's page (n * d bytes), rounded again after its
@@ -154,11 +122,12 @@ __device__ __forceinline__ void requant(uint8_t* base, int n, float ratio, int t
   }
 }
 
-// A lane's 8 dims of a row's key and value to slot `slot`.  All lanes call it.
+// A lane's 8 dims of a row's key and value to the row at k_row, v_row.  All lanes
+// call it.
 template <int D>
-__device__ __forceinline__ void put8(uint8_t* kb, uint8_t* vb, int slot, int u, bool on,
-                                     const float (&kx)[8], float (&vx)[8], float ki, float vi,
-                                     bool bad, int lane) {
+__device__ __forceinline__ void put8(uint8_t* k_row, uint8_t* v_row, const LaneDims& ld, int u,
+                                     bool on, const float (&kx)[8], float (&vx)[8], float ki,
+                                     float vi, bool bad, int lane) {
   constexpr int U = D / 8;
   uint32_t nan_lanes = 0;
   if (bad) {
@@ -174,25 +143,24 @@ __device__ __forceinline__ void put8(uint8_t* kb, uint8_t* vb, int slot, int u, 
     }
     nan_lanes = __ballot_sync(0xffffffffu, vn);
   }
-  uint2 kq = quant8(kx, ki), vq = quant8(vx, vi);
+  uint32_t k0 = quant4(kx[0], kx[1], kx[2], kx[3], ki);
   const uint32_t mine = ((1u << U) - 1u) << (lane / U * U);
-  if (u == 0 && (nan_lanes & mine)) kq.x = (kq.x & ~0xffu) | 0x7fu;
+  if (u == 0 && (nan_lanes & mine)) k0 = (k0 & ~0xffu) | 0x7fu;
   if (on) {
-    const int64_t at = (int64_t)slot * D + u * 8;
-    *reinterpret_cast<uint2*>(kb + at) = kq;
-    *reinterpret_cast<uint2*>(vb + at) = vq;
+    *reinterpret_cast<uint32_t*>(k_row + ld.a) = k0;
+    *reinterpret_cast<uint32_t*>(k_row + ld.b) = quant4(kx[4], kx[5], kx[6], kx[7], ki);
+    *reinterpret_cast<uint32_t*>(v_row + ld.a) = quant4(vx[0], vx[1], vx[2], vx[3], vi);
+    *reinterpret_cast<uint32_t*>(v_row + ld.b) = quant4(vx[4], vx[5], vx[6], vx[7], vi);
   }
 }
 
 // Sixteen rows of a head by one warp: all of them on their way to shared memory
-// at once, and kept there between the maximum and the rounding, the keys turned,
-// in 32 bits.  The loops over passes stay rolled: unrolled, the instruction
-// fetch bound the kernel.  A key row's place: D floats, the first halves of its
-// 8-dim units, then the second halves; its bf16 arrive in the upper half.
+// at once, and read there twice, for the maximum and for the rounding.  The
+// loops over passes stay rolled: unrolled, the instruction fetch bound the
+// kernel.
 template <int D>
 struct Stage16 {
-  static constexpr int KROW = D * 4, VROW = D * 2;
-  static constexpr int BYTES = 16 * (KROW + VROW);
+  static constexpr int ROW = D * 2, BYTES = 2 * 16 * ROW;   // keys, then values
 };
 
 // Rows [i, i + nr) of the call into slots [off, off + nr) of head h of page pg
@@ -206,80 +174,76 @@ __device__ __forceinline__ void write_group(const AppendParams& p, int i, int nr
   using S = Stage16<D>;
   constexpr int U = D / 8, RP = 32 / U;               // units a row, rows a pass
   const int u = lane % U, rl = lane / U;
+  const LaneDims ld = lane_dims(p, u);
   const int64_t cell = (int64_t)pg * p.L.H + h;
   uint8_t* kb = p.L.k + cell * p.L.page * D;
   uint8_t* vb = p.L.v + cell * p.L.page * D;
   const int r0 = part * 16;
   const int mine = live ? min(16, nr - r0) : 0;       // rows of this warp
-  uint8_t* ks_at = stage + u * 16;                    // lane's share of key row 0
-  uint8_t* vs_at = stage + 16 * S::KROW + u * 16;
-  float ka = 0.f, ko = 0.f, vo = 0.f;
-  uint32_t va2 = 0;                                   // bf16 magnitudes, as bits, two columns
-  float odd = 0.f;                                    // NaN when a key is not finite
+  float ko = 0.f, vo = 0.f;
   if (live && off > 0) {
     ko = p.L.k_scale[cell];
     vo = p.L.v_scale[cell];
   }
   __syncwarp();                                       // the head before is out of the stage
-  const int64_t src0 = (int64_t)(i + r0 + rl), at0 = (int64_t)h * D + u * 8;
+  {
+    const uint16_t* ks = p.k + (int64_t)(i + r0 + rl) * p.k_ld + (int64_t)h * D + u * 8;
+    const uint16_t* vs = p.v + (int64_t)(i + r0 + rl) * p.v_ld + (int64_t)h * D + u * 8;
+    uint32_t to = smem_u32(stage) + rl * S::ROW + u * 16;
 #pragma unroll 2
-  for (int r = rl; r < mine; r += RP) {
-    cp_async16(smem_u32(ks_at + r * S::KROW + D * 2), p.k + (src0 + r - rl) * p.k_ld + at0, 16);
-    cp_async16(smem_u32(vs_at + r * S::VROW), p.v + (src0 + r - rl) * p.v_ld + at0, 16);
+    for (int r = rl; r < mine; r += RP) {
+      cp_async16(to, ks, 16);
+      cp_async16(to + 16 * S::ROW, vs, 16);
+      ks += RP * p.k_ld;
+      vs += RP * p.v_ld;
+      to += RP * S::ROW;
+    }
   }
   cp_async_wait_all();
   __syncwarp();
-  const int half = p.rot >> 4, pair = u < half ? u + half : u - half;   // units of a half
-  for (int q = 0; q < mine; q += RP) {
-    const int r = q + rl;
-    const bool on = r < mine;
-    float x[8], y[8], cs[8], sn[8];
-    if (on) {
-      unpack8(*reinterpret_cast<const uint4*>(ks_at + r * S::KROW + D * 2), x);
-      if (u * 8 < p.rot) {
-        load_angles(p, pos0 + r0 + r, u, cs, sn);
-        if (p.interleaved) {
-          turn_pairs(cs, sn, x);
-        } else {
-          unpack8(*reinterpret_cast<const uint4*>(ks_at + r * S::KROW + D * 2 + (pair - u) * 16), y);
-          turn_halves(cs, sn, u < half, x, y);
-        }
-      }
+  const uint8_t* at_a = stage + ld.a * 2;             // the lane's groups of key row 0
+  const uint8_t* at_b = stage + ld.b * 2;
+  auto key = [&](int r, float (&x)[8]) {
+    unpack8(*reinterpret_cast<const uint2*>(at_a + r * S::ROW),
+            *reinterpret_cast<const uint2*>(at_b + r * S::ROW), x);
+    if (ld.turns) turn8(p, pos0 + r0 + r, u, x);
+  };
+  auto value_bits = [&](int r, uint2& a, uint2& b) {
+    a = *reinterpret_cast<const uint2*>(at_a + (16 + r) * S::ROW);
+    b = *reinterpret_cast<const uint2*>(at_b + (16 + r) * S::ROW);
+  };
+  float ka = 0.f, odd = 0.f;                          // odd: NaN when a key is not finite
+  uint32_t va2 = 0;                                   // bf16 magnitudes, as bits, two columns
+#pragma unroll 2
+  for (int r = rl; r < mine; r += RP) {
+    float x[8];
+    key(r, x);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        ka = fmaxf(ka, fabsf(x[e]));
-        odd = fmaf(x[e], 0.f, odd);
-      }
-      const uint4 v = *reinterpret_cast<const uint4*>(vs_at + r * S::VROW);
-      const uint32_t a[4] = {v.x, v.y, v.z, v.w};
+    for (int e = 0; e < 8; ++e) {
+      ka = fmaxf(ka, fabsf(x[e]));
+      odd = fmaf(x[e], 0.f, odd);
+    }
+    uint2 a, b;
+    value_bits(r, a, b);
+    const uint32_t w[4] = {a.x, a.y, b.x, b.y};
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        asm("max.u16x2 %0, %0, %1;" : "+r"(va2) : "r"(a[c] & 0x7fff7fffu));
-    }
-    __syncwarp();                                     // every bf16 of these rows has been read
-    if (on) {
-      *reinterpret_cast<float4*>(ks_at + r * S::KROW) = make_float4(x[0], x[1], x[2], x[3]);
-      *reinterpret_cast<float4*>(ks_at + r * S::KROW + D * 2) = make_float4(x[4], x[5], x[6], x[7]);
-    }
+    for (int c = 0; c < 4; ++c)
+      asm("max.u16x2 %0, %0, %1;" : "+r"(va2) : "r"(w[c] & 0x7fff7fffu));
   }
   const uint32_t vm = max(va2 & 0xffffu, va2 >> 16);
   float va = __uint_as_float(vm << 16);
   const bool bad = __any_sync(0xffffffffu, odd != 0.f || vm >= 0x7f80u);
-  auto turned = [&](int r, float (&x)[8]) {
-    const float4 a = *reinterpret_cast<const float4*>(ks_at + r * S::KROW);
-    const float4 b = *reinterpret_cast<const float4*>(ks_at + r * S::KROW + D * 2);
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-  };
   if (bad) {                                          // rare: the largest finite ones
     if (lane == 0) set_status(p.L.status, PP_DEV_NONFINITE);
     ka = va = 0.f;
     bool any = false;
     for (int r = rl; r < mine; r += RP) {
       float x[8];
-      turned(r, x);
+      key(r, x);
       amax8(x, ka, any);
-      unpack8(*reinterpret_cast<const uint4*>(vs_at + r * S::VROW), x);
+      uint2 a, b;
+      value_bits(r, a, b);
+      unpack8(a, b, x);
       amax8(x, va, any);
     }
   }
@@ -310,14 +274,19 @@ __device__ __forceinline__ void write_group(const AppendParams& p, int i, int nr
     p.L.v_scale[cell] = vs;
   }
   const float ki = 1.f / ks, vi = 1.f / vs;
+  uint8_t* k_row = kb + (off + r0 + rl) * D;
+  uint8_t* v_row = vb + (off + r0 + rl) * D;
 #pragma unroll 2
   for (int q = 0; q < mine; q += RP) {
-    const int r = q + rl;
-    const int rr = r < mine ? r : 0;
+    const int r = q + rl < mine ? q + rl : 0;
     float kx[8], vx[8];
-    turned(rr, kx);
-    unpack8(*reinterpret_cast<const uint4*>(vs_at + rr * S::VROW), vx);
-    put8<D>(kb, vb, off + r0 + r, u, r < mine, kx, vx, ki, vi, bad, lane);
+    key(r, kx);
+    uint2 a, b;
+    value_bits(r, a, b);
+    unpack8(a, b, vx);
+    put8<D>(k_row, v_row, ld, u, q + rl < mine, kx, vx, ki, vi, bad, lane);
+    k_row += RP * D;
+    v_row += RP * D;
   }
 }
 
@@ -328,6 +297,7 @@ __device__ __forceinline__ void write_short(const AppendParams& p, int i, int nr
                                             int off, int h, bool live, int lane) {
   constexpr int U = D / 8;
   const int u = lane % U;
+  const LaneDims ld = lane_dims(p, u);
   const int64_t cell = (int64_t)pg * p.L.H + h;
   uint8_t* kb = p.L.k + cell * p.L.page * D;
   uint8_t* vb = p.L.v + cell * p.L.page * D;
@@ -339,18 +309,13 @@ __device__ __forceinline__ void write_short(const AppendParams& p, int i, int nr
   float kx[8], vx[8], ka = 0.f, va = 0.f;
   bool bad = false;
   auto load = [&](int r) {
-    uint4 k = make_uint4(0, 0, 0, 0), v = k;
-    float cs[8], sn[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) cs[e] = sn[e] = 0.f;
-    if (live) {
-      k = __ldg(reinterpret_cast<const uint4*>(p.k + (int64_t)(i + r) * p.k_ld + (int64_t)h * D + u * 8));
-      v = __ldg(reinterpret_cast<const uint4*>(p.v + (int64_t)(i + r) * p.v_ld + (int64_t)h * D + u * 8));
-    }
-    if (p.rot) load_angles(p, pos0 + r, u, cs, sn);
-    unpack8(k, kx);
-    unpack8(v, vx);
-    turn8(p, u, lane, cs, sn, kx);
+    const uint16_t* k = p.k + (int64_t)(i + r) * p.k_ld + (int64_t)h * D;
+    const uint16_t* v = p.v + (int64_t)(i + r) * p.v_ld + (int64_t)h * D;
+    unpack8(__ldg(reinterpret_cast<const uint2*>(k + ld.a)),
+            __ldg(reinterpret_cast<const uint2*>(k + ld.b)), kx);
+    unpack8(__ldg(reinterpret_cast<const uint2*>(v + ld.a)),
+            __ldg(reinterpret_cast<const uint2*>(v + ld.b)), vx);
+    if (ld.turns) turn8(p, pos0 + r, u, kx);
   };
   for (int r = 0; r < nr; ++r) {
     load(r);
@@ -362,7 +327,7 @@ __device__ __forceinline__ void write_short(const AppendParams& p, int i, int nr
     ka = fmaxf(ka, __shfl_xor_sync(0xffffffffu, ka, o));
     va = fmaxf(va, __shfl_xor_sync(0xffffffffu, va, o));
   }
-  bad = __any_sync(0xffffffffu, bad);
+  bad = __any_sync(0xffffffffu, bad && live);
   if (bad && lane == 0) set_status(p.L.status, PP_DEV_NONFINITE);
   float ks = scale_for(ka), vs = scale_for(va);
   if (live && off > 0) {
@@ -379,7 +344,7 @@ __device__ __forceinline__ void write_short(const AppendParams& p, int i, int nr
   const float ki = 1.f / ks, vi = 1.f / vs;
   for (int r = 0; r < nr; ++r) {
     if (nr > 1) load(r);
-    put8<D>(kb, vb, off + r, u, live, kx, vx, ki, vi, bad, lane);
+    put8<D>(kb + (off + r) * D, vb + (off + r) * D, ld, u, live, kx, vx, ki, vi, bad, lane);
   }
 }
 
@@ -413,35 +378,37 @@ __device__ __forceinline__ void turn_queries(const AppendParams& p, int w0, int 
                                              int warp, int lane) {
   constexpr int U = D / 8, RP = 32 / U;
   const int u = lane % U, hl = lane / U;
+  const LaneDims ld = lane_dims(p, u);
   const int row = w0 + lane;
   const int s_l = row < w1 ? p.sid[row] : -1, ps_l = row < w1 ? p.pos[row] : -1;
   for (int i = w0 + warp; i < w1; i += WARPS) {
     const int s = __shfl_sync(0xffffffffu, s_l, i - w0), ps = __shfl_sync(0xffffffffu, ps_l, i - w0);
     if (s < 0 || s > p.L.P_max || ps < 0 || (p.rot && ps >= p.max_pos)) continue;
-    float cs[8], sn[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) cs[e] = sn[e] = 0.f;
-    if (p.rot) load_angles(p, ps, u, cs, sn);
-    const uint16_t* src = p.q + (int64_t)i * p.q_ld + u * 8;
-    uint16_t* dst = p.q_out + (int64_t)i * p.qo_ld + u * 8;
+    const uint16_t* src = p.q + (int64_t)i * p.q_ld;
+    uint16_t* dst = p.q_out + (int64_t)i * p.qo_ld;
     for (int h0 = hb; h0 < he; h0 += 4 * RP) {
-      uint4 w[4];
+      uint2 a[4], b[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int h = h0 + j * RP + hl;
-        w[j] = make_uint4(0, 0, 0, 0);
-        if (h < he) w[j] = *reinterpret_cast<const uint4*>(src + (int64_t)h * D);
+        a[j] = b[j] = make_uint2(0, 0);
+        if (h < he) {
+          a[j] = *reinterpret_cast<const uint2*>(src + (int64_t)h * D + ld.a);
+          b[j] = *reinterpret_cast<const uint2*>(src + (int64_t)h * D + ld.b);
+        }
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int h = h0 + j * RP + hl;
         float x[8];
-        unpack8(w[j], x);
-        turn8(p, u, lane, cs, sn, x);
-        if (h < he)
-          *reinterpret_cast<uint4*>(dst + (int64_t)h * D) =
-              make_uint4(f2_to_bf2(x[0], x[1]), f2_to_bf2(x[2], x[3]), f2_to_bf2(x[4], x[5]),
-                         f2_to_bf2(x[6], x[7]));
+        unpack8(a[j], b[j], x);
+        if (ld.turns) turn8(p, ps, u, x);
+        if (h < he) {
+          *reinterpret_cast<uint2*>(dst + (int64_t)h * D + ld.a) =
+              make_uint2(f2_to_bf2(x[0], x[1]), f2_to_bf2(x[2], x[3]));
+          *reinterpret_cast<uint2*>(dst + (int64_t)h * D + ld.b) =
+              make_uint2(f2_to_bf2(x[4], x[5]), f2_to_bf2(x[6], x[7]));
+        }
       }
     }
   }
@@ -609,13 +576,15 @@ cudaError_t launch_kv8_append(const pp_kv8_layer& L, const pp_kv8_append_args& a
   const int hpp = brief ? warps * 256 / L.d : warps / (L.page >> 4);
   const int passes = (L.H + hpp - 1) / hpp;
   p.win = 1;
-  while (p.win < 32 && (int64_t)((n + p.win - 1) / p.win) * passes > 32LL * num_sms) p.win *= 2;
+  const int64_t most = (brief ? 32LL : 8LL) * num_sms;   // (a short form's block is small)
+  while (p.win < 32 && (int64_t)((n + p.win - 1) / p.win) * passes > most) p.win *= 2;
   const int64_t wins = (n + p.win - 1) / p.win;
   // scanning the ids before a leader is the share's fixed cost: fewer shares
   // for long calls
   p.ys = passes;
-  while (p.ys > 1 && wins * (p.ys / 2) >= 16LL * num_sms) p.ys = (p.ys + 1) / 2;
-  const int qs = p.win > 4 ? (Hq + 31) / 32 : (Hq + 15) / 16;
+  while (p.ys > 1 && wins * (p.ys / 2) >= 8LL * num_sms) p.ys = (p.ys + 1) / 2;
+  const int qh = p.win > 4 ? 1024 / L.d : 16;   // heads of a block that turns queries
+  const int qs = (Hq + qh - 1) / qh;
   const dim3 grid((unsigned)wins, p.ys + qs);
   if (L.d == 128)
     return brief        ? start<128, 4, true>(p, grid, st)
