@@ -342,7 +342,8 @@ pp_status pp_doc_prefill_attn(const pp_kv_layer *layer, int32_t doc_len, const u
  *   H          key/value heads;  d  64 or 128
  *   page       tokens of a page: 16, 32, 64 or 128
  *   n_pages    pages of the pool
- *   k, v       e4m3 [n_pages][H][page][d], 16-byte aligned
+ *   k, v       e4m3 [n_pages][H][page][d], 16-byte aligned; no NaN among the
+ *              values of slots in use (the append moves a NaN into the key)
  *   k_scale, v_scale   fp32 [n_pages][H]; a stored value x stands for
  *              x * scale; powers of two, 2^-40 .. 2^40 (written by the append)
  *   doc_table  int32 [doc_pages]: page of document tokens i * page ..

@@ -371,10 +371,10 @@ pp_status kv8_append(const pp_kv8_layer* L, const pp_kv8_append_args* a, void* s
       !a->sid || !a->pos || !aligned(a->sid, 2) || !aligned(a->pos, 4))
     return PP_ERR_INVALID_ARG;
   if (!a->q != !a->q_out) return PP_ERR_INVALID_ARG;
-  if (a->q && (a->Hq < 1 || a->Hq > (1 << 20) || !row_operand(a->q, a->q_ld, a->Hq, L->d) ||
+  if (a->q && (a->Hq < 1 || a->Hq > (1 << 17) || !row_operand(a->q, a->q_ld, a->Hq, L->d) ||
                !row_operand(a->q_out, a->q_out_ld, a->Hq, L->d)))
     return PP_ERR_INVALID_ARG;
-  if (L->H > (1 << 17)) return PP_ERR_UNSUPPORTED;
+  if (L->H > (1 << 14)) return PP_ERR_UNSUPPORTED;    // blocks along y
   const int sms = sm_count();
   if (sms < 1) return PP_ERR_CUDA;
   return from_cuda(pp::launch_kv8_append(*L, *a, sms, static_cast<cudaStream_t>(stream)));

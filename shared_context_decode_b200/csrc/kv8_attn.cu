@@ -213,16 +213,14 @@ __device__ __forceinline__ void chunk_step(State<D, NT>& st, const uint32_t (&qf
   }
 #pragma unroll
   for (int w = 0; w < D / 32; ++w) {      // 4 bytes of each value row: dims 4w .. 4w + 3 of the lane's
-    uint32_t x[4][2];
-#pragma unroll
-    for (int a = 0; a < 4; ++a) {
-      x[a][0] = e4m3x2_to_h2(vx[a][w]);
-      x[a][1] = e4m3x2_hi_to_h2(vx[a][w]);
-    }
+    // two keys' bytes interleaved, then to f16: dims 4w + (0, 1 | 2, 3)
+    const uint32_t ka0 = __byte_perm(vx[0][w], vx[1][w], 0x5140), ka1 = __byte_perm(vx[0][w], vx[1][w], 0x7362);
+    const uint32_t kb0 = __byte_perm(vx[2][w], vx[3][w], 0x5140), kb1 = __byte_perm(vx[2][w], vx[3][w], 0x7362);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const uint32_t a0 = __byte_perm(x[0][i], x[1][i], 0x5410), a1 = __byte_perm(x[0][i], x[1][i], 0x7632);
-      const uint32_t a2 = __byte_perm(x[2][i], x[3][i], 0x5410), a3 = __byte_perm(x[2][i], x[3][i], 0x7632);
+      const uint32_t ka = i ? ka1 : ka0, kb = i ? kb1 : kb0;
+      const uint32_t a0 = e4m3x2_to_h2(ka), a1 = e4m3x2_hi_to_h2(ka);
+      const uint32_t a2 = e4m3x2_to_h2(kb), a3 = e4m3x2_hi_to_h2(kb);
 #pragma unroll
       for (int t = 0; t < NT; ++t) mma_f16(st.o[t][2 * w + i], a0, a1, a2, a3, pb[t][0], pb[t][1]);
     }

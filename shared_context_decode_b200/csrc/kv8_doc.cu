@@ -253,7 +253,7 @@ __global__ void __maxnreg__(kRegs8) kv8_doc_tc(const Doc8Params p) {
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_base;
-  // every CTA is resident: the segment pass may fill SMs as they end
+  // the segment pass may fill SMs as this pass's CTAs end
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   if (warp == 0) {

@@ -220,3 +220,42 @@ def test_pages_past_two_and_four_gib():
             assert np.array_equal(getattr(layer, t)[pg].float().cpu().double().numpy(), getattr(rep, t)[i])
             assert np.array_equal(getattr(layer, t + "_scale")[pg].cpu().double().numpy(),
                                   getattr(rep, t + "_scale")[i])
+
+
+@pytest.mark.parametrize("shift", [0, 1, 3, 5])
+def test_ids_at_any_alignment(shift):
+    """Stream ids that start on any 2-byte boundary, positions on any 4-byte one,
+    with a row that breaks its stream's run far behind it."""
+    m = pp()
+    layer, rep = new_cache(2, 64, 16, 40, 2, 10, seed=8)
+    sid = sum(([s] * 20 for s in range(1, 30)), []) + [7, 31] + [-1] * 5 + [32] * 9
+    pos = sum((list(range(10, 30)) for s in range(1, 30)), []) + [30, 10] + [0] * 5 + list(range(10, 19))
+    n = len(sid)
+    q, k, v = rows(n, 2, 2, 64, 4)
+    s = torch.tensor([0] * shift + sid, dtype=torch.int16, device=DEV)[shift:]
+    p = torch.tensor([0] * shift + pos, dtype=torch.int32, device=DEV)[shift:]
+    m.kv8_append(layer, k, v, s, p)
+    torch.cuda.synchronize()
+    assert rep.append(k.float().cpu().numpy(), v.float().cpu().numpy(), sid, pos) == [580]
+    same_cache(layer, rep)
+    assert m.kv8_device_status(layer) == m.PP_DEV_ROW_ORDER
+
+
+def test_one_layer_for_two_calls_at_once():
+    """Appends of different streams on two CUDA streams."""
+    m = pp()
+    layer, rep = new_cache(8, 128, 32, 64, 3, 20, seed=9)
+    calls = []
+    for half in (0, 1):
+        sid = sum(([s] * 33 for s in range(1 + 32 * half, 33 + 32 * half)), [])
+        pos = list(range(20, 53)) * 32
+        q, k, v = rows(len(sid), 8, 8, 128, 5 + half)
+        calls.append((k, v, torch.tensor(sid, dtype=torch.int16, device=DEV),
+                      torch.tensor(pos, dtype=torch.int32, device=DEV), torch.cuda.Stream()))
+        rep.append(k.float().cpu().numpy(), v.float().cpu().numpy(), sid, pos)
+    torch.cuda.synchronize()
+    for k, v, s, p, st in calls:
+        with torch.cuda.stream(st):
+            m.kv8_append(layer, k, v, s, p)
+    torch.cuda.synchronize()
+    same_cache(layer, rep)
