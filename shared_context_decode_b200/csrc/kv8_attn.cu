@@ -356,28 +356,87 @@ __global__ void __launch_bounds__(WARPS * 32, (NT == 1 ? 16 : 12) / WARPS)
     nh = min(p.hg, p.g - hb);
     nrow = min(p.rt, p.rows - r0);
     const int n_pairs = nrow * nh;
-    // ---- queries: B operand of S^T (row n = r of tile t), scaled into f16
-    State<D, NT> st;
-    uint32_t qf[NT][D / 8];
-    float qs[NT][2];
-    int lim[NT][2], sidr[NT][2];
+    // ---- what the item starts from, all on its way at once: lane i's row, the
+    // queries' bits, the document partials of rows that a warp has to itself
+    int sid_l = -1, ps_l = -1;
+    if (lane < nrow) {
+      sid_l = p.q_sid[r0 + lane];
+      ps_l = p.q_pos[r0 + lane];
+    }
+    uint32_t w2[NT][D / 8];                // bf16 pairs of row n = r of tile t
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const int n = t * 8 + r;
-      uint32_t w2[D / 8];                  // bf16 pairs
-      uint32_t am2 = 0;                    // largest magnitudes, as bits
 #pragma unroll
-      for (int e = 0; e < D / 8; ++e) w2[e] = 0u;
+      for (int e = 0; e < D / 8; ++e) w2[t][e] = 0u;
       if (n < n_pairs) {
         const uint16_t* src = p.q + (int64_t)(r0 + n / nh) * p.q_ld +
                               (int64_t)(kvh * p.g + hb + n % nh) * D + c * (D / 4);
 #pragma unroll
         for (int i = 0; i < D / 32; ++i)
-          *reinterpret_cast<uint4*>(&w2[4 * i]) = *reinterpret_cast<const uint4*>(src + 8 * i);
+          *reinterpret_cast<uint4*>(&w2[t][4 * i]) = *reinterpret_cast<const uint4*>(src + 8 * i);
       }
+    }
+    State<D, NT> st;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int a = 0; a < 2; ++a) {
+        st.m[t][a] = -INFINITY;
+        st.l[t][a] = 0.f;
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) st.o[t][j][a] = st.o[t][j][2 + a] = 0.f;
+      }
+    DocRow dr2[NT][2];
+    if (NT > 1 && p.has_doc && p.ways == 1) {
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+      DocRow d{0, 0, 0};                   // of pair `lane`
+      const int sid_p = __shfl_sync(0xffffffffu, sid_l, lane < n_pairs ? lane / nh : 0);
+      if (lane < n_pairs && stream_query(sid_p, p.L.P_max))
+        d = doc_row(p, r0 + lane / nh, kvh, hb + lane % nh);
+      float2 ml[NT][2];
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+          const int n2 = t * 8 + 2 * c + a;
+          dr2[t][a].slot = __shfl_sync(0xffffffffu, d.slot, n2);
+          dr2[t][a].n = __shfl_sync(0xffffffffu, d.n, n2);
+          dr2[t][a].two = __shfl_sync(0xffffffffu, d.two, n2);
+          ml[t][a] = make_float2(-INFINITY, 0.f);
+          if (dr2[t][a].n == 0) continue;
+          ml[t][a] = __ldg(reinterpret_cast<const float2*>(p.doc_ml) + dr2[t][a].slot);
+          float x[D / 8];
+          load_part<D>(x, p.doc_o + dr2[t][a].slot * D, r);
+#pragma unroll
+          for (int j = 0; j < D / 16; ++j) {
+            st.o[t][j][a] = x[2 * j];
+            st.o[t][j][2 + a] = x[2 * j + 1];
+          }
+        }
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+          st.m[t][a] = ml[t][a].x;
+          st.l[t][a] = r == 0 ? ml[t][a].y : 0.f;
+          if (ml[t][a].x == -INFINITY) {   // saw no key: its O may hold anything
+            st.l[t][a] = 0.f;
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) st.o[t][j][a] = st.o[t][j][2 + a] = 0.f;
+          }
+        }
+    }
+    // ---- queries: B operand of S^T, scaled into f16
+    uint32_t qf[NT][D / 8];
+    float qs[NT][2];
+    int lim[NT][2], sidr[NT][2];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      uint32_t am2 = 0;                    // largest magnitudes, as bits
 #pragma unroll
       for (int i = 0; i < D / 8; ++i)
-        asm("max.u16x2 %0, %0, %1;" : "+r"(am2) : "r"(w2[i] & 0x7fff7fffu));
+        asm("max.u16x2 %0, %0, %1;" : "+r"(am2) : "r"(w2[t][i] & 0x7fff7fffu));
       uint32_t am = max(am2 & 0xffffu, am2 >> 16);
       am = max(am, __shfl_xor_sync(0xffffffffu, am, 1));
       am = max(am, __shfl_xor_sync(0xffffffffu, am, 2));
@@ -389,7 +448,7 @@ __global__ void __launch_bounds__(WARPS * 32, (NT == 1 ? 16 : 12) / WARPS)
                                       : __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
       for (int i = 0; i < D / 8; ++i) {
-        const float2 f = bf2_to_f2(w2[i]);
+        const float2 f = bf2_to_f2(w2[t][i]);
         qf[t][i] = f2_to_h2(f.x * inv, f.y * inv);
       }
       const float qsc = __uint_as_float((uint32_t)(e + 127) << 23) * p.sl2;
@@ -397,51 +456,12 @@ __global__ void __launch_bounds__(WARPS * 32, (NT == 1 ? 16 : 12) / WARPS)
       for (int a = 0; a < 2; ++a) {
         qs[t][a] = __shfl_sync(0xffffffffu, qsc, (2 * c + a) * 4);
         const int n2 = t * 8 + 2 * c + a;
-        int sd = 0, lm = -1;
-        if (n2 < n_pairs) {
-          sd = p.q_sid[r0 + n2 / nh];
-          const int ps = p.q_pos[r0 + n2 / nh];
-          sd = stream_query(sd, p.L.P_max) ? sd : 0;
-          const int cap = p.L.seg_pages * p.L.page;
-          lm = sd && ps >= p.L.pos0 ? min(ps - p.L.pos0, cap - 1) : -1;
-        }
-        sidr[t][a] = sd;
-        lim[t][a] = lm;
-        st.m[t][a] = -INFINITY;
-        st.l[t][a] = 0.f;
-#pragma unroll
-        for (int j = 0; j < D / 16; ++j) st.o[t][j][a] = st.o[t][j][2 + a] = 0.f;
-      }
-    }
-    // ---- rows that a warp has to itself start from their first document partial
-    DocRow dr2[NT][2];
-    if (NT > 1 && p.has_doc && p.ways == 1) {
-      asm volatile("griddepcontrol.wait;" ::: "memory");
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        // lane n (of the tile's 8) finds pair n's partials
-        DocRow d{0, 0, 0};
-        const int n = t * 8 + (lane & 7);
-        if (n < n_pairs && stream_query(p.q_sid[r0 + n / nh], p.L.P_max))
-          d = doc_row(p, r0 + n / nh, kvh, hb + n % nh);
-#pragma unroll
-        for (int a = 0; a < 2; ++a) {
-          dr2[t][a].slot = __shfl_sync(0xffffffffu, d.slot, 2 * c + a);
-          dr2[t][a].n = __shfl_sync(0xffffffffu, d.n, 2 * c + a);
-          dr2[t][a].two = __shfl_sync(0xffffffffu, d.two, 2 * c + a);
-          if (dr2[t][a].n == 0) continue;
-          const float2 ml = __ldg(reinterpret_cast<const float2*>(p.doc_ml) + dr2[t][a].slot);
-          if (ml.x == -INFINITY) continue;     // saw no key: its O may hold anything
-          float x[D / 8];
-          load_part<D>(x, p.doc_o + dr2[t][a].slot * D, r);
-          st.m[t][a] = ml.x;
-          st.l[t][a] = r == 0 ? ml.y : 0.f;
-#pragma unroll
-          for (int j = 0; j < D / 16; ++j) {
-            st.o[t][j][a] = x[2 * j];
-            st.o[t][j][2 + a] = x[2 * j + 1];
-          }
-        }
+        const int at = n2 < n_pairs ? n2 / nh : 0;
+        const int sd = __shfl_sync(0xffffffffu, sid_l, at), ps = __shfl_sync(0xffffffffu, ps_l, at);
+        const bool on = n2 < n_pairs && stream_query(sd, p.L.P_max);
+        const int cap = p.L.seg_pages * p.L.page;
+        sidr[t][a] = on ? sd : 0;
+        lim[t][a] = on && ps >= p.L.pos0 ? min(ps - p.L.pos0, cap - 1) : -1;
       }
     }
     // ---- document
@@ -465,10 +485,12 @@ __global__ void __launch_bounds__(WARPS * 32, (NT == 1 ? 16 : 12) / WARPS)
                   lane);
     }
     // ---- segments: one pass per stretch of rows of one stream
+    const int before = __shfl_up_sync(0xffffffffu, sid_l, 1);
+    const uint32_t starts = __ballot_sync(0xffffffffu, lane < nrow && (lane == 0 || sid_l != before));
     for (int ra = 0; ra < nrow;) {
-      const int s = p.q_sid[r0 + ra];
-      int rb = ra + 1;
-      while (rb < nrow && p.q_sid[r0 + rb] == s) ++rb;
+      const int s = __shfl_sync(0xffffffffu, sid_l, ra);
+      const uint32_t rest = starts >> ra >> 1;
+      const int rb = rest ? ra + __ffs(rest) : nrow;
       if (s == 0 || s > p.L.P_max) {
         if (kvh == 0 && hb == 0 && way == 0 && lane == 0) set_status(p.L.status, PP_DEV_BAD_STREAM);
       } else if (s > 0) {
