@@ -281,7 +281,7 @@ __device__ __forceinline__ void part_of(int n, int w, int ways, int& c0, int& c1
   c1 = (int)((int64_t)n * (w + 1) / ways);
 }
 
-constexpr int kMaxWays = 8;   // warps of a CTA, and of an item, at most
+constexpr int kMaxWays = 16;   // warps of a CTA, and of an item, at most
 
 // A warp's shared memory: its ring, and over it, when the keys are done, its
 // partial result: (m, l) of its rows, then O, rows of D + 4 floats.
@@ -331,7 +331,7 @@ __device__ __forceinline__ void load_part(float (&x)[D / 8], const float* row, i
   }
 }
 
-// Four warps a block, and eight where that many share an item.
+// Four warps a block, and as many as share an item where that is more.
 template <int D, int NT, int WARPS>
 __global__ void __launch_bounds__(WARPS * 32, (NT == 1 ? 16 : 12) / WARPS)
     kv8_attn(const Attn8Params p) {
@@ -721,6 +721,8 @@ cudaError_t launch_as(const Attn8Params& p, cudaStream_t st) {
 
 template <int D, int NT>
 cudaError_t launch(const Attn8Params& p, cudaStream_t st) {
+  if constexpr (NT == 1)
+    if (p.ways > 8) return launch_as<D, NT, 16>(p, st);
   return p.ways > 4 ? launch_as<D, NT, 8>(p, st) : launch_as<D, NT, 4>(p, st);
 }
 
@@ -755,8 +757,10 @@ cudaError_t launch_kv8_attn(const pp_kv8_layer& L, const pp_kv8_attn_args& a,
   // one item is not a CTA's whole tail.
   const int64_t chunks = (int64_t)L.seg_pages * L.page / 16 + (p.doc_len + 15) / 16;
   int ways = 1;
-  while (ways < kMaxWays && (items * ways < 12LL * num_sms || (ways < 4 && chunks / ways > 16)))
+  while (ways < 8 && (items * ways < 12LL * num_sms || (ways < 4 && chunks / ways > 16)))
     ways *= 2;
+  // (a block an SM, and a document long enough to share)
+  if (ways == 8 && it.most == 8 && items <= 3 * num_sms / 2 && chunks > 40) ways = kMaxWays;
   p.ways = ways;
   p.lper = L.page == 16 ? 0 : L.page == 32 ? 1 : L.page == 64 ? 2 : 3;
   if (L.d == 128) return it.most == 8 ? launch<128, 1>(p, st) : launch<128, 2>(p, st);
