@@ -443,7 +443,7 @@ __global__ void __launch_bounds__(WARPS * 32, (NT == 1 ? 16 : 12) / WARPS)
       // 2^e with the row's largest value / 2^e in [2^13, 2^14): bf16's 8 bits are
       // exact in f16 down to 2^-30 of it; a row with a NaN or infinity is all NaN
       int e = (int)(am >> 7) - 127 - 13;
-      e = e < -100 ? -100 : e;
+      e = e < -60 ? -60 : e;
       const float inv = am >= 0x7f80u ? __int_as_float(0x7fffffff)
                                       : __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll

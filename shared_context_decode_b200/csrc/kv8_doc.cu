@@ -51,6 +51,8 @@ static_assert(128 * kRegsCtl + 128 * kRegsConv + 256 * kRegsSoft <= kThreads8 * 
 // for every 16 keys the key scale and the value scale's logarithm, -inf where
 // there are no keys; [8]: whether any of the tile's keys are not there.
 constexpr int kInfo = 8, kInfoLd = 9;
+// Least factor of a score: a hidden one is -inf, and -inf * 0 would be NaN.
+constexpr float kLeast = 1e-37f;
 
 struct Doc8Params {
   pp_kv8_layer L;
@@ -181,7 +183,7 @@ __device__ __forceinline__ float load_queries(const Doc8Params& p, uint8_t* tile
   // 2^e with the largest value / 2^e in [2^13, 2^14): bf16's 8 bits are exact in
   // f16 down to 2^-30 of it
   int e = (int)(am >> 7) - 127 - 13;
-  e = e < -100 ? -100 : e;
+  e = e < -60 ? -60 : e;
   const float inv = am >= 0x7f80u ? __int_as_float(0x7fffffff)
                                   : __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll 4
@@ -543,7 +545,7 @@ __global__ void __maxnreg__(kRegs8) kv8_doc_tc(const Doc8Params p) {
               float y = __uint_as_float(x[q * 16]);
 #pragma unroll
               for (int e = 1; e < 16; ++e) y = fmaxf(y, __uint_as_float(x[q * 16 + e]));
-              mx = fmaxf(mx, fmaf(y, in.x * qs, in.y));
+              mx = fmaxf(mx, fmaf(y, fmaxf(in.x * qs, kLeast), in.y));
             }
           }
           return mx;
@@ -569,7 +571,7 @@ __global__ void __maxnreg__(kRegs8) kv8_doc_tc(const Doc8Params p) {
             uint32_t (&x)[32] = r[c & 1];
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-              const float a = in[c & 1][q].x * qs, g = in[c & 1][q].y, b = g - m;
+              const float a = fmaxf(in[c & 1][q].x * qs, kLeast), g = in[c & 1][q].y, b = g - m;
               const float rv = g == -INFINITY ? 0.f : ex2_mufu(-g);   // 1 / value scale
               const float2 av = make_float2(a, a), bv = make_float2(b, b);
               float2 rs[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
@@ -624,7 +626,7 @@ __global__ void __maxnreg__(kRegs8) kv8_doc_tc(const Doc8Params p) {
           raise = true;
         }
         // A NaN score: the sum is NaN, or, from the polynomial, still huge.
-        if (sum > 4096.f || sum != sum) lt = __int_as_float(0x7fffffff);
+        if (sum > 1e18f || sum != sum) lt = __int_as_float(0x7fffffff);
         none = none && lt == lt;
         l += lt;
         tmem_st32(t_S, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));

@@ -435,3 +435,51 @@ def test_maximum_that_keeps_rising():
         tol = 2.0 ** -8 * np.abs(ro) + (2.0 ** -7 + 2.0 ** -10 + 2.0 ** -12) * ra + 1e-30
         assert (err <= tol).all(), (err / tol).max()
         assert np.abs(lse.cpu().numpy() - rl).max() <= 2.0 ** -8
+
+
+@pytest.mark.parametrize("splits", [0, 2])
+def test_queries_and_pages_of_zeros_and_tiny_factors(splits):
+    """Queries of zeros and of bf16's smallest normals, an all-zero page at the
+    least scale, softmax scales down to 1e-30: uniform or nearly uniform weights,
+    also in the document's last, hidden-tailed tile."""
+    m = pp()
+    N, d = 203, 64
+    layer, doc, segs = make_cache(2, d, 16, N, [20, 7, 3], seed=23)
+    pg = int(layer.doc_table[5])
+    layer.k.view(torch.uint8)[pg] = 0
+    layer.k_scale[pg] = 2.0 ** -40
+    doc[0][80:96] = 0
+    q = queries(3, 4, d, 1)
+    q[0] = 0
+    q[1] = 1.2e-38
+    s, p = ids([1, 2, 3], [N + 19, N + 6, N + 2])
+    for scale in (0.125, 1e-6, 1e-30):
+        for fn in (m.kv8_decode_attn, m.kv8_prefill_attn):
+            lse = torch.zeros((3, 4), device=DEV)
+            o = fn(layer, N, q, s, p, scale, lse=lse, opt=m.Options(splits=splits))
+            torch.cuda.synchronize()
+            check(o, lse, oracle_attn(doc, segs, N, q.cpu(), np.array([1, 2, 3]),
+                                      np.array([N + 19, N + 6, N + 2]), scale), scale)
+    assert m.kv8_device_status(layer) == 0
+
+
+@pytest.mark.parametrize("splits", [0, 2])
+@pytest.mark.parametrize("mag", [2.0 ** 8, 2.0 ** 15])
+def test_scores_of_a_million(splits, mag):
+    """Scores so large that one key takes all: the output is that key's value."""
+    m = pp()
+    N, d = 500, 128
+    layer, doc, segs = make_cache(1, d, 32, N, [5], seed=24)
+    q = (doc[0][[7, 130, 480]].transpose(0, 1) * mag).to(torch.bfloat16).to(DEV)      # [1, 3, d]
+    s, p = ids([1], [N + 4])
+    lse = torch.zeros((1, 3), device=DEV)
+    o = m.kv8_decode_attn(layer, N, q, s, p, 1.0, lse=lse, opt=m.Options(splits=splits))
+    torch.cuda.synchronize()
+    sc = torch.einsum("hd,nd->hn", q[0].cpu().double(), torch.cat([doc[0][:, 0], segs[0][0][:, 0]]).double())
+    two = sc.topk(2).values
+    # the runner-up is further off than the scores' fp32 error, 128 * 2^-24 of the sum of magnitudes
+    gap = (two[:, 0] - two[:, 1]) / (128 * 2.0 ** -24 * two[:, 0])
+    assert (gap > 100).all()
+    v = torch.cat([doc[1][:, 0], segs[0][1][:, 0]])[sc.argmax(1)]
+    assert torch.equal(o[0].float().cpu(), v.to(torch.bfloat16).float())
+    assert ((lse[0].cpu().double() - two[:, 0]).abs() <= 2.0 ** -16 * two[:, 0]).all()
