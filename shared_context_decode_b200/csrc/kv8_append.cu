@@ -440,6 +440,19 @@ __global__ void __launch_bounds__(WARPS * 32, (SHORT ? 32 : 24) / WARPS)
   if (row < w1) {
     s_l = p.sid[row];
     ps_l = p.pos[row];
+  }
+  // the row before: a lane's neighbour, the window's first row's from memory
+  int s_b = -1, ps_b = -1;
+  if (lane == 0 && w0 > 0) {
+    s_b = p.sid[w0 - 1];
+    ps_b = p.pos[w0 - 1];
+  }
+  const int s_n = __shfl_up_sync(0xffffffffu, s_l, 1), ps_n = __shfl_up_sync(0xffffffffu, ps_l, 1);
+  if (lane > 0) {
+    s_b = s_n;
+    ps_b = ps_n;
+  }
+  if (row < w1) {
     if (s_l > p.L.P_max) {
       err = PP_DEV_BAD_STREAM;
     } else if (s_l >= 0) {
@@ -447,7 +460,7 @@ __global__ void __launch_bounds__(WARPS * 32, (SHORT ? 32 : 24) / WARPS)
       if (ps_l < 0 || slot < 0)
         err = s_l == 0 ? PP_DEV_DOC_OUT_OF_RANGE : PP_DEV_BAD_POSITION;
       else    // a row that follows its neighbour within a page is not a leader
-        lead = row == 0 || slot % page == 0 || p.sid[row - 1] != s_l || p.pos[row - 1] != ps_l - 1;
+        lead = row == 0 || slot % page == 0 || s_b != s_l || ps_b != ps_l - 1;
     }
   }
   const bool first_cta = blockIdx.y == 0 && warp == 0;

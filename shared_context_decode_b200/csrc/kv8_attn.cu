@@ -331,7 +331,8 @@ __device__ __forceinline__ void load_part(float (&x)[D / 8], const float* row, i
   }
 }
 
-// Four warps a block, and as many as share an item where that is more.
+// The warps that share an item make a block: with four items of different
+// lengths to a block the shorter ones' places stayed empty.
 template <int D, int NT, int WARPS>
 __global__ void __launch_bounds__(WARPS * 32, (NT == 1 ? 16 : 12) / WARPS)
     kv8_attn(const Attn8Params p) {
@@ -723,7 +724,10 @@ template <int D, int NT>
 cudaError_t launch(const Attn8Params& p, cudaStream_t st) {
   if constexpr (NT == 1)
     if (p.ways > 8) return launch_as<D, NT, 16>(p, st);
-  return p.ways > 4 ? launch_as<D, NT, 8>(p, st) : launch_as<D, NT, 4>(p, st);
+  return p.ways > 4   ? launch_as<D, NT, 8>(p, st)
+         : p.ways > 2 ? launch_as<D, NT, 4>(p, st)
+         : p.ways > 1 ? launch_as<D, NT, 2>(p, st)
+                      : launch_as<D, NT, 1>(p, st);
 }
 
 }  // namespace

@@ -29,6 +29,11 @@
 //   warps 8-15   softmax, one thread a row; queries to f16; partial results
 // TMEM: O_0 | O_1 | S_0 | S_1, P over the first 64 columns of its S.
 //
+// Bound: the softmax warps' instruction latency.  At 256 rows, 32 heads and 16384
+// keys (73 us; 134 MB, 69 GFLOP) a tile of 256 rows takes a CTA about 3450
+// cycles: 1700 of exponentials on each stream, 1250 of products and hand-over
+// behind them, the other stream's under both; the tensor pipe is busy for half.
+//
 // Every wait is bounded: on expiry the kernel sets PP_DEV_TIMEOUT, raises a
 // CTA-wide abort flag, drains its own copies and MMAs (bounded), frees TMEM
 // and returns.
@@ -138,8 +143,6 @@ __device__ __forceinline__ bool next_seg8(const Doc8Params& p, Runs8& r, Seg8& s
 }
 
 // One arrival for a warp whose lanes have all done what the barrier stands for.
-// (An arrival by every lane is an atomic on one address 32 times over: with
-// those, barriers alone took 1.7 us of a tile's 3.6.)
 __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
   __syncwarp();
   if (lane == 0) mbar_arrive(bar);
@@ -579,10 +582,12 @@ __global__ void __maxnreg__(kRegs8) kv8_doc_tc(const Doc8Params p) {
               for (int e = 0; e < 16; e += 2) {
                 const float2 w = ffma2(make_float2(__uint_as_float(x[q * 16 + e]),
                                                    __uint_as_float(x[q * 16 + e + 1])), av, bv);
-                // a quarter on the FMA pipe: MUFU alone took 104 us where this takes
-                // 88 (256 rows, 32 heads, 16384 keys), 2 in 5 the same 88
-                const float2 pv = (e >> 1) % 4 == 2 ? ex2_poly2_nan(w)
-                                                    : make_float2(ex2_mufu(w.x), ex2_mufu(w.y));
+                // three in eight on the FMA pipe (none / 1/8 / 1/4 / 3/8 / 1/2: 79 / 77 /
+                // 74 / 73 / 77 us at 256 rows, 32 heads, 16384 keys, 1416 / 1362 / 1312 /
+                // 1279 / 1382 at 8192 rows, 12000 keys)
+                const float2 pv = (e >> 1) % 8 % 3 == 1
+                                      ? ex2_poly2_nan(w)
+                                      : make_float2(ex2_mufu(w.x), ex2_mufu(w.y));
                 rs[(e >> 1) & 1] = fadd2(rs[(e >> 1) & 1], pv);
                 pk[c * 16 + q * 8 + (e >> 1)] = f2_to_h2(pv.x, pv.y);
               }
