@@ -524,11 +524,13 @@ _BF16, _I16, _I32, _F32, _U8 = (torch.bfloat16, torch.int16, torch.int32, torch.
 def _rows(t: torch.Tensor, name: str, n: int, heads: int, d: int, layer) -> int:
     """Checks rows [n, heads, d] bf16 whose heads are packed and whose rows may
     be strided; returns the elements between rows."""
-    if isinstance(t, torch.Tensor) and t.dtype is _BF16 and t.get_device() == layer.index and \
-            t.shape == (n, heads, d):
-        s0, s1, s2 = t.stride()
-        if s2 == 1 and s1 == d and s0 >= heads * d and s0 % 8 == 0:
-            return s0
+    try:
+        if t.dtype is _BF16 and t.get_device() == layer.index and t.shape == (n, heads, d):
+            s0, s1, s2 = t.stride()
+            if s2 == 1 and s1 == d and s0 >= heads * d and not s0 & 7:
+                return s0
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != _BF16:
@@ -547,22 +549,25 @@ def _rows(t: torch.Tensor, name: str, n: int, heads: int, d: int, layer) -> int:
 
 
 def _want8(t: torch.Tensor, dtype, name: str, layer):
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == layer.index and
-            t.is_contiguous()):
-        _want(t, dtype, name, layer.device)
+    try:
+        if t.dtype is dtype and t.get_device() == layer.index and t.is_contiguous():
+            return
+    except AttributeError:
+        pass
+    _want(t, dtype, name, layer.device)
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _call8(fn, name: str, layer, *args):
-    """fn(layer, *args, stream) on the layer's device and its current stream."""
+def _call8(fn, name: str, layer, arg):
+    """fn(layer, arg, stream) on the layer's device and its current stream."""
     cur = _current_device()
     if cur != layer.index:
         with torch.cuda.device(layer.index):
-            return _call8(fn, name, layer, *args)
-    rc = fn(layer.ref, *args,
+            return _call8(fn, name, layer, arg)
+    rc = fn(layer.ref, arg,
             _raw_stream(cur) if _raw_stream else torch.cuda.current_stream(cur).cuda_stream)
     if rc:
         raise PPError(rc, name)
@@ -570,7 +575,8 @@ def _call8(fn, name: str, layer, *args):
 
 def kv8_reset(layer: KV8Layer):
     """Clear the layer's status word."""
-    _call8(_kv8_reset, "pp_kv8_reset", layer)
+    with torch.cuda.device(layer.index):
+        _check(_kv8_reset(layer.ref, _stream(layer.device)), "pp_kv8_reset")
 
 
 def kv8_append(layer: KV8Layer, k: torch.Tensor, v: torch.Tensor, sid: torch.Tensor,
