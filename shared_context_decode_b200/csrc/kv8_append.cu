@@ -48,9 +48,10 @@ struct LaneDims {
   int a, b;        // first dims of the groups
   bool turns;
 };
+template <bool INTER>
 __device__ __forceinline__ LaneDims lane_dims(const AppendParams& p, int u) {
   const int hr = p.rot >> 3;              // lanes whose dims turn
-  const bool split = u < hr && !p.interleaved;
+  const bool split = u < hr && !INTER;
   return {split ? u * 4 : u * 8, split ? (u + hr) * 4 : u * 8 + 4, u < hr};
 }
 
@@ -65,10 +66,12 @@ __device__ __forceinline__ void unpack8(uint2 a, uint2 b, float (&x)[8]) {
   }
 }
 
-// Turn the lane's dims by position pos.  Every product and difference is
+// Turn the lane's dims by position pos; INTER: neighbours turn together (known
+// when compiled: selecting at run time doubled the rotation's instructions).  Every product and difference is
 // rounded by itself (no fused multiply-add), the result a plain fp32 evaluation
 // of a cos - b sin gives, so which e4m3 value a rotated key rounds to does not
 // depend on the compiler's contraction.
+template <bool INTER>
 __device__ __forceinline__ void turn8(const AppendParams& p, int pos, int u, float (&x)[8]) {
   const float* t = p.cos_sin + (int64_t)pos * p.rot + u * 4;
   const float4 c4 = __ldg(reinterpret_cast<const float4*>(t));
@@ -77,14 +80,14 @@ __device__ __forceinline__ void turn8(const AppendParams& p, int pos, int u, flo
   float y[8];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    const float a = p.interleaved ? x[2 * e] : x[e], b = p.interleaved ? x[2 * e + 1] : x[4 + e];
+    const float a = INTER ? x[2 * e] : x[e], b = INTER ? x[2 * e + 1] : x[4 + e];
     y[e] = __fsub_rn(__fmul_rn(a, cs[e]), __fmul_rn(b, sn[e]));
     y[4 + e] = __fadd_rn(__fmul_rn(b, cs[e]), __fmul_rn(a, sn[e]));
   }
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    x[e] = p.interleaved ? y[(e & 1) * 4 + (e >> 1)] : y[e];
-    x[4 + e] = p.interleaved ? y[(e & 1) * 4 + 2 + (e >> 1)] : y[4 + e];
+    x[e] = INTER ? y[(e & 1) * 4 + (e >> 1)] : y[e];
+    x[4 + e] = INTER ? y[(e & 1) * 4 + 2 + (e >> 1)] : y[4 + e];
   }
 }
 
@@ -166,7 +169,7 @@ struct Stage16 {
 // Rows [i, i + nr) of the call into slots [off, off + nr) of head h of page pg
 // by the `wph` warps of a head, 16 rows each; all of the block's warps call it
 // (live: this one has a head), for its one barrier.
-template <int D, int WARPS>
+template <int D, int WARPS, bool INTER>
 __device__ __forceinline__ void write_group(const AppendParams& p, int i, int nr, int pos0, int pg,
                                             int off, int h, bool live, int part, int wph,
                                             float2 (&red)[WARPS], uint8_t* stage, int warp,
@@ -174,7 +177,7 @@ __device__ __forceinline__ void write_group(const AppendParams& p, int i, int nr
   using S = Stage16<D>;
   constexpr int U = D / 8, RP = 32 / U;               // units a row, rows a pass
   const int u = lane % U, rl = lane / U;
-  const LaneDims ld = lane_dims(p, u);
+  const LaneDims ld = lane_dims<INTER>(p, u);
   const int64_t cell = (int64_t)pg * p.L.H + h;
   uint8_t* kb = p.L.k + cell * p.L.page * D;
   uint8_t* vb = p.L.v + cell * p.L.page * D;
@@ -206,23 +209,21 @@ __device__ __forceinline__ void write_group(const AppendParams& p, int i, int nr
   auto key = [&](int r, float (&x)[8]) {
     unpack8(*reinterpret_cast<const uint2*>(at_a + r * S::ROW),
             *reinterpret_cast<const uint2*>(at_b + r * S::ROW), x);
-    if (ld.turns) turn8(p, pos0 + r0 + r, u, x);
+    if (ld.turns) turn8<INTER>(p, pos0 + r0 + r, u, x);
   };
   auto value_bits = [&](int r, uint2& a, uint2& b) {
     a = *reinterpret_cast<const uint2*>(at_a + (16 + r) * S::ROW);
     b = *reinterpret_cast<const uint2*>(at_b + (16 + r) * S::ROW);
   };
-  float ka = 0.f, odd = 0.f;                          // odd: NaN when a key is not finite
+  float ka = 0.f;                                     // NaN once a key is
   uint32_t va2 = 0;                                   // bf16 magnitudes, as bits, two columns
 #pragma unroll 2
   for (int r = rl; r < mine; r += RP) {
     float x[8];
     key(r, x);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      ka = fmaxf(ka, fabsf(x[e]));
-      odd = fmaf(x[e], 0.f, odd);
-    }
+    for (int e = 0; e < 8; ++e)
+      asm("max.NaN.f32 %0, %0, %1;" : "+f"(ka) : "f"(fabsf(x[e])));
     uint2 a, b;
     value_bits(r, a, b);
     const uint32_t w[4] = {a.x, a.y, b.x, b.y};
@@ -232,7 +233,7 @@ __device__ __forceinline__ void write_group(const AppendParams& p, int i, int nr
   }
   const uint32_t vm = max(va2 & 0xffffu, va2 >> 16);
   float va = __uint_as_float(vm << 16);
-  const bool bad = __any_sync(0xffffffffu, odd != 0.f || vm >= 0x7f80u);
+  const bool bad = __any_sync(0xffffffffu, !(ka < INFINITY) || vm >= 0x7f80u);
   if (bad) {                                          // rare: the largest finite ones
     if (lane == 0) set_status(p.L.status, PP_DEV_NONFINITE);
     ka = va = 0.f;
@@ -292,12 +293,12 @@ __device__ __forceinline__ void write_group(const AppendParams& p, int i, int nr
 
 // The same for short runs (one row of a decode step): a warp takes 32 / U heads
 // side by side, U lanes each, all rows of one after another.  h: the lane's head.
-template <int D>
+template <int D, bool INTER>
 __device__ __forceinline__ void write_short(const AppendParams& p, int i, int nr, int pos0, int pg,
                                             int off, int h, bool live, int lane) {
   constexpr int U = D / 8;
   const int u = lane % U;
-  const LaneDims ld = lane_dims(p, u);
+  const LaneDims ld = lane_dims<INTER>(p, u);
   const int64_t cell = (int64_t)pg * p.L.H + h;
   uint8_t* kb = p.L.k + cell * p.L.page * D;
   uint8_t* vb = p.L.v + cell * p.L.page * D;
@@ -315,7 +316,7 @@ __device__ __forceinline__ void write_short(const AppendParams& p, int i, int nr
             __ldg(reinterpret_cast<const uint2*>(k + ld.b)), kx);
     unpack8(__ldg(reinterpret_cast<const uint2*>(v + ld.a)),
             __ldg(reinterpret_cast<const uint2*>(v + ld.b)), vx);
-    if (ld.turns) turn8(p, pos0 + r, u, kx);
+    if (ld.turns) turn8<INTER>(p, pos0 + r, u, kx);
   };
   for (int r = 0; r < nr; ++r) {
     load(r);
@@ -373,12 +374,12 @@ __device__ __forceinline__ void scan_ids(const int16_t* sid, int i, int s, int& 
 }
 
 // Turn the window's queries: a warp a row, four passes of heads in flight.
-template <int D, int WARPS>
+template <int D, int WARPS, bool INTER>
 __device__ __forceinline__ void turn_queries(const AppendParams& p, int w0, int w1, int hb, int he,
                                              int warp, int lane) {
   constexpr int U = D / 8, RP = 32 / U;
   const int u = lane % U, hl = lane / U;
-  const LaneDims ld = lane_dims(p, u);
+  const LaneDims ld = lane_dims<INTER>(p, u);
   const int row = w0 + lane;
   const int s_l = row < w1 ? p.sid[row] : -1, ps_l = row < w1 ? p.pos[row] : -1;
   for (int i = w0 + warp; i < w1; i += WARPS) {
@@ -402,7 +403,7 @@ __device__ __forceinline__ void turn_queries(const AppendParams& p, int w0, int 
         const int h = h0 + j * RP + hl;
         float x[8];
         unpack8(a[j], b[j], x);
-        if (ld.turns) turn8(p, ps, u, x);
+        if (ld.turns) turn8<INTER>(p, ps, u, x);
         if (h < he) {
           *reinterpret_cast<uint2*>(dst + (int64_t)h * D + ld.a) =
               make_uint2(f2_to_bf2(x[0], x[1]), f2_to_bf2(x[2], x[3]));
@@ -415,7 +416,7 @@ __device__ __forceinline__ void turn_queries(const AppendParams& p, int w0, int 
 }
 
 // WARPS: 4, or 8 for pages of 128 tokens.  SHORT: for runs of about a row.
-template <int D, int WARPS, bool SHORT>
+template <int D, int WARPS, bool SHORT, bool INTER>
 __global__ void __launch_bounds__(WARPS * 32, (SHORT ? 32 : 24) / WARPS)
     kv8_append(const AppendParams p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -423,7 +424,7 @@ __global__ void __launch_bounds__(WARPS * 32, (SHORT ? 32 : 24) / WARPS)
   const int w1 = min(p.n, w0 + p.win);
   if ((int)blockIdx.y >= p.ys) {
     const int part = blockIdx.y - p.ys, parts = gridDim.y - p.ys;
-    turn_queries<D, WARPS>(p, w0, w1, p.Hq * part / parts, p.Hq * (part + 1) / parts, warp, lane);
+    turn_queries<D, WARPS, INTER>(p, w0, w1, p.Hq * part / parts, p.Hq * (part + 1) / parts, warp, lane);
     return;
   }
   __shared__ int red_cnt[WARPS], red_last[WARPS];
@@ -523,10 +524,10 @@ __global__ void __launch_bounds__(WARPS * 32, (SHORT ? 32 : 24) / WARPS)
     for (int h0 = hb; h0 < he; h0 += hpp) {
       if constexpr (SHORT) {
         const int h = h0 + warp * (256 / D) + lane / (D / 8);
-        write_short<D>(p, i, nr, ps, pg, off, h < he ? h : hb, h < he, lane);
+        write_short<D, INTER>(p, i, nr, ps, pg, off, h < he ? h : hb, h < he, lane);
       } else {
         const int h = h0 + warp / wph;
-        write_group<D, WARPS>(p, i, nr, ps, pg, off, h, h < he, warp % wph, wph, red[buf],
+        write_group<D, WARPS, INTER>(p, i, nr, ps, pg, off, h, h < he, warp % wph, wph, red[buf],
                               stage + warp * Stage16<D>::BYTES, warp, lane);
         buf ^= 1;
       }
@@ -536,8 +537,8 @@ __global__ void __launch_bounds__(WARPS * 32, (SHORT ? 32 : 24) / WARPS)
 
 __global__ void kv8_clear_status(int32_t* status) { *status = 0; }
 
-template <int D, int WARPS, bool SHORT>
-cudaError_t start(const AppendParams& p, dim3 grid, cudaStream_t st) {
+template <int D, int WARPS, bool SHORT, bool INTER>
+cudaError_t start_as(const AppendParams& p, dim3 grid, cudaStream_t st) {
   constexpr int SMEM = SHORT ? 0 : WARPS * Stage16<D>::BYTES;
   static std::atomic<uint64_t> ready{0};
   int dev = 0;
@@ -545,13 +546,18 @@ cudaError_t start(const AppendParams& p, dim3 grid, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const uint64_t bit = 1ull << (dev & 63);
   if (SMEM > 0 && !(ready.load() & bit)) {
-    e = cudaFuncSetAttribute(kv8_append<D, WARPS, SHORT>,
+    e = cudaFuncSetAttribute(kv8_append<D, WARPS, SHORT, INTER>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit);
   }
-  kv8_append<D, WARPS, SHORT><<<grid, WARPS * 32, SMEM, st>>>(p);
+  kv8_append<D, WARPS, SHORT, INTER><<<grid, WARPS * 32, SMEM, st>>>(p);
   return cudaGetLastError();
+}
+template <int D, int WARPS, bool SHORT>
+cudaError_t start(const AppendParams& p, dim3 grid, cudaStream_t st) {
+  return p.interleaved ? start_as<D, WARPS, SHORT, true>(p, grid, st)
+                       : start_as<D, WARPS, SHORT, false>(p, grid, st);
 }
 
 }  // namespace
