@@ -66,16 +66,13 @@ __device__ __forceinline__ void unpack8(uint2 a, uint2 b, float (&x)[8]) {
   }
 }
 
-// Turn the lane's dims by position pos; INTER: neighbours turn together (known
+// Turn the lane's dims by the angles' cosines and sines; INTER: neighbours turn together (known
 // when compiled: selecting at run time doubled the rotation's instructions).  Every product and difference is
 // rounded by itself (no fused multiply-add), the result a plain fp32 evaluation
 // of a cos - b sin gives, so which e4m3 value a rotated key rounds to does not
 // depend on the compiler's contraction.
 template <bool INTER>
-__device__ __forceinline__ void turn8(const AppendParams& p, int pos, int u, float (&x)[8]) {
-  const float* t = p.cos_sin + (int64_t)pos * p.rot + u * 4;
-  const float4 c4 = __ldg(reinterpret_cast<const float4*>(t));
-  const float4 s4 = __ldg(reinterpret_cast<const float4*>(t + (p.rot >> 1)));
+__device__ __forceinline__ void turn8(const float4 c4, const float4 s4, float (&x)[8]) {
   const float cs[4] = {c4.x, c4.y, c4.z, c4.w}, sn[4] = {s4.x, s4.y, s4.z, s4.w};
   float y[8];
 #pragma unroll
@@ -89,6 +86,14 @@ __device__ __forceinline__ void turn8(const AppendParams& p, int pos, int u, flo
     x[e] = INTER ? y[(e & 1) * 4 + (e >> 1)] : y[e];
     x[4 + e] = INTER ? y[(e & 1) * 4 + 2 + (e >> 1)] : y[4 + e];
   }
+}
+
+// The same by position pos, from the table.
+template <bool INTER>
+__device__ __forceinline__ void turn8_at(const AppendParams& p, int pos, int u, float (&x)[8]) {
+  const float* t = p.cos_sin + (int64_t)pos * p.rot + u * 4;
+  turn8<INTER>(__ldg(reinterpret_cast<const float4*>(t)),
+               __ldg(reinterpret_cast<const float4*>(t + (p.rot >> 1))), x);
 }
 
 // Largest finite magnitude of 8 values, joined to a; any non-finite: bad.
@@ -166,13 +171,23 @@ struct Stage16 {
   static constexpr int ROW = D * 2, BYTES = 2 * 16 * ROW;   // keys, then values
 };
 
+// Whether a page's angles are kept in shared memory for the heads that use them:
+// up to 8 KB, which costs no block its place (61 ragged questions, pages of 16,
+// half of d turned: 13.2 us from the table, 12.0 so; pages of 64, all of d turned,
+// 32 KB: 165 and 181 for a document of 16384 tokens).
+__host__ __device__ inline bool keep_angles(int page, int rot) {
+  return rot > 0 && page * rot * 4 <= 8192;
+}
+
 // Rows [i, i + nr) of the call into slots [off, off + nr) of head h of page pg
 // by the `wph` warps of a head, 16 rows each; all of the block's warps call it
-// (live: this one has a head), for its one barrier.
+// (live: this one has a head), for its one barrier.  angles: of the page's rows,
+// in the table or, where they are few, in shared memory.
 template <int D, int WARPS, bool INTER>
-__device__ __forceinline__ void write_group(const AppendParams& p, int i, int nr, int pos0, int pg,
+__device__ __forceinline__ void write_group(const AppendParams& p, int i, int nr, int pg,
                                             int off, int h, bool live, int part, int wph,
-                                            float2 (&red)[WARPS], uint8_t* stage, int warp,
+                                            float2 (&red)[WARPS], uint8_t* stage,
+                                            const float* angles, int warp,
                                             int lane) {
   using S = Stage16<D>;
   constexpr int U = D / 8, RP = 32 / U;               // units a row, rows a pass
@@ -209,7 +224,11 @@ __device__ __forceinline__ void write_group(const AppendParams& p, int i, int nr
   auto key = [&](int r, float (&x)[8]) {
     unpack8(*reinterpret_cast<const uint2*>(at_a + r * S::ROW),
             *reinterpret_cast<const uint2*>(at_b + r * S::ROW), x);
-    if (ld.turns) turn8<INTER>(p, pos0 + r0 + r, u, x);
+    if (ld.turns) {
+      const float* t = angles + (r0 + r) * p.rot + u * 4;
+      turn8<INTER>(*reinterpret_cast<const float4*>(t),
+                   *reinterpret_cast<const float4*>(t + (p.rot >> 1)), x);
+    }
   };
   auto value_bits = [&](int r, uint2& a, uint2& b) {
     a = *reinterpret_cast<const uint2*>(at_a + (16 + r) * S::ROW);
@@ -316,7 +335,7 @@ __device__ __forceinline__ void write_short(const AppendParams& p, int i, int nr
             __ldg(reinterpret_cast<const uint2*>(k + ld.b)), kx);
     unpack8(__ldg(reinterpret_cast<const uint2*>(v + ld.a)),
             __ldg(reinterpret_cast<const uint2*>(v + ld.b)), vx);
-    if (ld.turns) turn8<INTER>(p, pos0 + r, u, kx);
+    if (ld.turns) turn8_at<INTER>(p, pos0 + r, u, kx);
   };
   for (int r = 0; r < nr; ++r) {
     load(r);
@@ -403,7 +422,7 @@ __device__ __forceinline__ void turn_queries(const AppendParams& p, int w0, int 
         const int h = h0 + j * RP + hl;
         float x[8];
         unpack8(a[j], b[j], x);
-        if (ld.turns) turn8<INTER>(p, ps, u, x);
+        if (ld.turns) turn8_at<INTER>(p, ps, u, x);
         if (h < he) {
           *reinterpret_cast<uint2*>(dst + (int64_t)h * D + ld.a) =
               make_uint2(f2_to_bf2(x[0], x[1]), f2_to_bf2(x[2], x[3]));
@@ -467,8 +486,11 @@ __global__ void __launch_bounds__(WARPS * 32, (SHORT ? 32 : 24) / WARPS)
   const bool first_cta = blockIdx.y == 0 && warp == 0;
   if (first_cta && err) set_status(p.L.status, err);
   uint32_t leaders = __ballot_sync(0xffffffffu, lead);
+  float* staged = reinterpret_cast<float*>(stage + WARPS * Stage16<D>::BYTES);
+  const bool keep = !SHORT && keep_angles(page, p.rot);
   int buf = 0;
   while (leaders) {                     // the same in every warp
+    if (keep) __syncthreads();          // the leader before is done with its angles
     const int l = __ffs(leaders) - 1;
     leaders &= leaders - 1;
     const int i = w0 + l;
@@ -489,6 +511,13 @@ __global__ void __launch_bounds__(WARPS * 32, (SHORT ? 32 : 24) / WARPS)
       const uint32_t m = __ballot_sync(0xffffffffu, in);
       nr = r0 + (m == 0xffffffffu ? 32 : __ffs(~m) - 1);
       if (m != 0xffffffffu) break;
+    }
+    const float* angles = p.cos_sin + (int64_t)ps * p.rot;    // the rows' lie in a row
+    if (keep) {
+      const int n16 = min(nr, max(0, p.max_pos - ps)) * (p.rot / 4);
+      for (int c = threadIdx.x; c < n16; c += blockDim.x)
+        cp_async16(smem_u32(staged + c * 4), angles + c * 4, 16);
+      angles = staged;
     }
     // The stream's run must be its only one and its positions consecutive:
     // count the earlier rows of the stream and find the last row of another.
@@ -518,6 +547,10 @@ __global__ void __launch_bounds__(WARPS * 32, (SHORT ? 32 : 24) / WARPS)
     else if (pg < 0) err = PP_DEV_BAD_PAGE;
     else err = p.rot && ps + nr > p.max_pos ? PP_DEV_BAD_POSITION : 0;   // past the angle table
     if (err && first_cta && lane == 0) set_status(p.L.status, err);
+    if (keep) {
+      cp_async_wait_all();
+      __syncthreads();
+    }
     if (err == PP_DEV_BAD_POSITION) nr = p.max_pos - ps;
     else if (err) continue;
     if (nr <= 0) continue;
@@ -527,8 +560,8 @@ __global__ void __launch_bounds__(WARPS * 32, (SHORT ? 32 : 24) / WARPS)
         write_short<D, INTER>(p, i, nr, ps, pg, off, h < he ? h : hb, h < he, lane);
       } else {
         const int h = h0 + warp / wph;
-        write_group<D, WARPS, INTER>(p, i, nr, ps, pg, off, h, h < he, warp % wph, wph, red[buf],
-                              stage + warp * Stage16<D>::BYTES, warp, lane);
+        write_group<D, WARPS, INTER>(p, i, nr, pg, off, h, h < he, warp % wph, wph, red[buf],
+                                     stage + warp * Stage16<D>::BYTES, angles, warp, lane);
         buf ^= 1;
       }
     }
@@ -539,19 +572,23 @@ __global__ void kv8_clear_status(int32_t* status) { *status = 0; }
 
 template <int D, int WARPS, bool SHORT, bool INTER>
 cudaError_t start_as(const AppendParams& p, dim3 grid, cudaStream_t st) {
-  constexpr int SMEM = SHORT ? 0 : WARPS * Stage16<D>::BYTES;
+  // the stages, and the angles of a page's rows
+  constexpr int MOST = SHORT ? 0 : WARPS * Stage16<D>::BYTES + 8192;
+  const int smem = SHORT ? 0
+                         : WARPS * Stage16<D>::BYTES +
+                               (keep_angles(p.L.page, p.rot) ? p.L.page * p.rot * 4 : 0);
   static std::atomic<uint64_t> ready{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const uint64_t bit = 1ull << (dev & 63);
-  if (SMEM > 0 && !(ready.load() & bit)) {
+  if (!SHORT && !(ready.load() & bit)) {
     e = cudaFuncSetAttribute(kv8_append<D, WARPS, SHORT, INTER>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, MOST);
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit);
   }
-  kv8_append<D, WARPS, SHORT, INTER><<<grid, WARPS * 32, SMEM, st>>>(p);
+  kv8_append<D, WARPS, SHORT, INTER><<<grid, WARPS * 32, smem, st>>>(p);
   return cudaGetLastError();
 }
 template <int D, int WARPS, bool SHORT>
