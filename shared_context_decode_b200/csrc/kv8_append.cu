@@ -310,13 +310,18 @@ __device__ __forceinline__ void write_group(const AppendParams& p, int i, int nr
   }
 }
 
-// The same for short runs (one row of a decode step): a warp takes 32 / U heads
-// side by side, U lanes each, all rows of one after another.  h: the lane's head.
-template <int D, bool INTER>
+constexpr int kShortWarps = 4;
+
+// The same without stages, for calls of many short runs (a decode step): a warp
+// takes 32 / U heads side by side, U lanes each (h: the lane's), and of the run's
+// rows W = 1: all, W = kShortWarps: its share, the block's warps together.
+template <int D, bool INTER, int W>
 __device__ __forceinline__ void write_short(const AppendParams& p, int i, int nr, int pos0, int pg,
-                                            int off, int h, bool live, int lane) {
+                                            int off, int h, bool live,
+                                            float2 (*red)[kShortWarps][256 / D], int warp,
+                                            int lane) {
   constexpr int U = D / 8;
-  const int u = lane % U;
+  const int u = lane % U, r0 = W == 1 ? 0 : warp;
   const LaneDims ld = lane_dims<INTER>(p, u);
   const int64_t cell = (int64_t)pg * p.L.H + h;
   uint8_t* kb = p.L.k + cell * p.L.page * D;
@@ -337,7 +342,7 @@ __device__ __forceinline__ void write_short(const AppendParams& p, int i, int nr
             __ldg(reinterpret_cast<const uint2*>(v + ld.b)), vx);
     if (ld.turns) turn8_at<INTER>(p, pos0 + r, u, kx);
   };
-  for (int r = 0; r < nr; ++r) {
+  for (int r = r0; r < nr; r += W) {
     load(r);
     amax8(kx, ka, bad);
     amax8(vx, va, bad);
@@ -347,30 +352,42 @@ __device__ __forceinline__ void write_short(const AppendParams& p, int i, int nr
     ka = fmaxf(ka, __shfl_xor_sync(0xffffffffu, ka, o));
     va = fmaxf(va, __shfl_xor_sync(0xffffffffu, va, o));
   }
+  if constexpr (W > 1) {
+    if (u == 0) (*red)[warp][lane / U] = make_float2(ka, va);
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const float2 y = (*red)[w][lane / U];
+      ka = fmaxf(ka, y.x);
+      va = fmaxf(va, y.y);
+    }
+  }
   bad = __any_sync(0xffffffffu, bad && live);
   if (bad && lane == 0) set_status(p.L.status, PP_DEV_NONFINITE);
   float ks = scale_for(ka), vs = scale_for(va);
   if (live && off > 0) {
-    if (ks > ko) requant<D>(kb, off, ko / ks, u, U);
+    const int t = r0 * U + u;
+    if (ks > ko) requant<D>(kb, off, ko / ks, t, W * U);
     else ks = ko;
-    if (vs > vo) requant<D>(vb, off, vo / vs, u, U);
+    if (vs > vo) requant<D>(vb, off, vo / vs, t, W * U);
     else vs = vo;
   }
   __syncwarp();
-  if (live && u == 0) {
+  if (live && u == 0 && r0 == 0) {
     p.L.k_scale[cell] = ks;
     p.L.v_scale[cell] = vs;
   }
   const float ki = 1.f / ks, vi = 1.f / vs;
-  for (int r = 0; r < nr; ++r) {
+  for (int r = r0; r < nr; r += W) {
     if (nr > 1) load(r);
     put8<D>(kb + (off + r) * D, vb + (off + r) * D, ld, u, live, kx, vx, ki, vi, bad, lane);
   }
 }
 
 // Of the rows before i: how many are of stream s (joined to cnt), and the last
-// that is not (joined to last); 16 bytes of ids a thread at a time.
-__device__ __forceinline__ void scan_ids(const int16_t* sid, int i, int s, int& cnt, int& last) {
+// that is not (joined to last); 16 bytes of ids a thread at a time, thread t of nt.
+__device__ __forceinline__ void scan_ids(const int16_t* sid, int i, int s, int t, int nt, int& cnt,
+                                         int& last) {
   auto one = [&](int j, int id) {
     const bool same = id == s;
     cnt += same ? 1 : 0;
@@ -378,9 +395,9 @@ __device__ __forceinline__ void scan_ids(const int16_t* sid, int i, int s, int& 
   };
   const int lead = min(i, (int)((16 - (reinterpret_cast<uintptr_t>(sid) & 15)) & 15) / 2);
   const int vecs = (i - lead) / 8;
-  for (int j = threadIdx.x; j < lead; j += blockDim.x) one(j, sid[j]);
+  for (int j = t; j < lead; j += nt) one(j, sid[j]);
 #pragma unroll 4
-  for (int v = threadIdx.x; v < vecs; v += blockDim.x) {
+  for (int v = t; v < vecs; v += nt) {
     const int4 w = __ldg(reinterpret_cast<const int4*>(sid + lead) + v);
     const int a[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -389,7 +406,91 @@ __device__ __forceinline__ void scan_ids(const int16_t* sid, int i, int s, int& 
       one(lead + v * 8 + 2 * c + 1, a[c] >> 16);
     }
   }
-  for (int j = lead + vecs * 8 + threadIdx.x; j < i; j += blockDim.x) one(j, sid[j]);
+  for (int j = lead + vecs * 8 + t; j < i; j += nt) one(j, sid[j]);
+}
+
+// What a warp knows of its block's window of rows, a lane each.
+struct Window {
+  int s, ps;             // the lane's row: stream and position
+  uint32_t leaders;      // rows that are the first of their run in a page
+};
+__device__ __forceinline__ Window look(const AppendParams& p, int w0, int w1, bool tell, int lane) {
+  const int row = w0 + lane;
+  Window w{-1, -1, 0};
+  int err = 0;
+  bool lead = false;
+  if (row < w1) {
+    w.s = p.sid[row];
+    w.ps = p.pos[row];
+  }
+  // the row before: a lane's neighbour, the window's first row's from memory
+  int s_b = -1, ps_b = -1;
+  if (lane == 0 && w0 > 0) {
+    s_b = p.sid[w0 - 1];
+    ps_b = p.pos[w0 - 1];
+  }
+  const int s_n = __shfl_up_sync(0xffffffffu, w.s, 1), ps_n = __shfl_up_sync(0xffffffffu, w.ps, 1);
+  if (lane > 0) {
+    s_b = s_n;
+    ps_b = ps_n;
+  }
+  if (row < w1) {
+    if (w.s > p.L.P_max) {
+      err = PP_DEV_BAD_STREAM;
+    } else if (w.s >= 0) {
+      const int slot = w.s == 0 ? w.ps : w.ps - p.L.pos0;
+      if (w.ps < 0 || slot < 0)
+        err = w.s == 0 ? PP_DEV_DOC_OUT_OF_RANGE : PP_DEV_BAD_POSITION;
+      else    // a row that follows its neighbour within a page is not a leader
+        lead = row == 0 || slot % p.L.page == 0 || s_b != w.s || ps_b != w.ps - 1;
+    }
+  }
+  if (tell && err) set_status(p.L.status, err);
+  w.leaders = __ballot_sync(0xffffffffu, lead);
+  return w;
+}
+
+// A leader's page and the rows of its run that fall into it, found by a warp.
+struct Lead {
+  int i, s, ps, off, pg, nr;
+  bool fits;             // inside the table
+};
+__device__ __forceinline__ Lead open_lead(const AppendParams& p, int i, int s, int ps, int lane) {
+  const int page = p.L.page;
+  const int slot = s == 0 ? ps : ps - p.L.pos0, seg = slot / page;
+  Lead x{i, s, ps, slot % page, -1, 1, seg < (s == 0 ? p.L.doc_pages : p.L.seg_pages)};
+  if (x.fits)
+    x.pg = page_of(s == 0 ? p.L.doc_table[seg]
+                          : p.L.seg_table[(int64_t)(s - 1) * p.L.seg_pages + seg], p.L.n_pages);
+  const int most = min(page - x.off, p.n - i);
+  for (int r0 = 1; r0 < most; r0 += 32) {
+    const int r = r0 + lane;
+    const bool in = r < most && p.sid[i + r] == s && (int64_t)p.pos[i + r] == (int64_t)ps + r;
+    const uint32_t m = __ballot_sync(0xffffffffu, in);
+    x.nr = r0 + (m == 0xffffffffu ? 32 : __ffs(~m) - 1);
+    if (m != 0xffffffffu) break;
+  }
+  return x;
+}
+
+// The rows to write (none: 0) of a leader whose stream has cnt rows before it, the
+// last row of another being `last`: the stream's run must be its only one and its
+// positions consecutive.
+__device__ __forceinline__ int rows_of(const AppendParams& p, const Lead& x, int cnt, int last,
+                                       bool tell) {
+  const int a = last + 1;               // first row of the run
+  int err = 0, nr = x.nr;
+  if (cnt != x.i - a || (int64_t)x.ps - p.pos[a] != x.i - a) err = PP_DEV_ROW_ORDER;
+  else if (!x.fits) err = x.s == 0 ? PP_DEV_DOC_OUT_OF_RANGE : PP_DEV_SEGMENT_OVERFLOW;
+  else if (x.pg < 0) err = PP_DEV_BAD_PAGE;
+  if (err) {
+    nr = 0;
+  } else if (p.rot && x.ps + nr > p.max_pos) {       // past the angle table
+    err = PP_DEV_BAD_POSITION;
+    nr = max(0, p.max_pos - x.ps);
+  }
+  if (err && tell) set_status(p.L.status, err);
+  return nr;
 }
 
 // Turn the window's queries: a warp a row, four passes of heads in flight.
@@ -434,10 +535,9 @@ __device__ __forceinline__ void turn_queries(const AppendParams& p, int w0, int 
   }
 }
 
-// WARPS: 4, or 8 for pages of 128 tokens.  SHORT: for runs of about a row.
-template <int D, int WARPS, bool SHORT, bool INTER>
-__global__ void __launch_bounds__(WARPS * 32, (SHORT ? 32 : 24) / WARPS)
-    kv8_append(const AppendParams p) {
+// WARPS: 4, or 8 for pages of 128 tokens.
+template <int D, int WARPS, bool INTER>
+__global__ void __launch_bounds__(WARPS * 32, 24 / WARPS) kv8_append(const AppendParams p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int w0 = blockIdx.x * p.win;
   const int w1 = min(p.n, w0 + p.win);
@@ -449,80 +549,29 @@ __global__ void __launch_bounds__(WARPS * 32, (SHORT ? 32 : 24) / WARPS)
   __shared__ int red_cnt[WARPS], red_last[WARPS];
   extern __shared__ __align__(16) uint8_t stage[];
   __shared__ float2 red[2][WARPS];
-  const int page = p.L.page;
-  const int wph = SHORT ? 1 : page >> 4;            // warps a head
-  const int hpp = SHORT ? WARPS * 256 / D : WARPS / wph;   // heads a pass
+  const int wph = p.L.page >> 4;                    // warps a head
+  const int hpp = WARPS / wph;                      // heads a pass
   const int hb = p.L.H * (int)blockIdx.y / p.ys, he = p.L.H * ((int)blockIdx.y + 1) / p.ys;
-  // every warp looks at the window's rows, a lane each (at most 32)
-  const int row = w0 + lane;
-  int s_l = -1, ps_l = -1, err = 0;
-  bool lead = false;
-  if (row < w1) {
-    s_l = p.sid[row];
-    ps_l = p.pos[row];
-  }
-  // the row before: a lane's neighbour, the window's first row's from memory
-  int s_b = -1, ps_b = -1;
-  if (lane == 0 && w0 > 0) {
-    s_b = p.sid[w0 - 1];
-    ps_b = p.pos[w0 - 1];
-  }
-  const int s_n = __shfl_up_sync(0xffffffffu, s_l, 1), ps_n = __shfl_up_sync(0xffffffffu, ps_l, 1);
-  if (lane > 0) {
-    s_b = s_n;
-    ps_b = ps_n;
-  }
-  if (row < w1) {
-    if (s_l > p.L.P_max) {
-      err = PP_DEV_BAD_STREAM;
-    } else if (s_l >= 0) {
-      const int slot = s_l == 0 ? ps_l : ps_l - p.L.pos0;
-      if (ps_l < 0 || slot < 0)
-        err = s_l == 0 ? PP_DEV_DOC_OUT_OF_RANGE : PP_DEV_BAD_POSITION;
-      else    // a row that follows its neighbour within a page is not a leader
-        lead = row == 0 || slot % page == 0 || s_b != s_l || ps_b != ps_l - 1;
-    }
-  }
   const bool first_cta = blockIdx.y == 0 && warp == 0;
-  if (first_cta && err) set_status(p.L.status, err);
-  uint32_t leaders = __ballot_sync(0xffffffffu, lead);
+  Window w = look(p, w0, w1, first_cta, lane);      // every warp alike
   float* staged = reinterpret_cast<float*>(stage + WARPS * Stage16<D>::BYTES);
-  const bool keep = !SHORT && keep_angles(page, p.rot);
+  const bool keep = keep_angles(p.L.page, p.rot);
   int buf = 0;
-  while (leaders) {                     // the same in every warp
+  while (w.leaders) {                   // the same in every warp
     if (keep) __syncthreads();          // the leader before is done with its angles
-    const int l = __ffs(leaders) - 1;
-    leaders &= leaders - 1;
-    const int i = w0 + l;
-    const int s = __shfl_sync(0xffffffffu, s_l, l), ps = __shfl_sync(0xffffffffu, ps_l, l);
-    const int slot = s == 0 ? ps : ps - p.L.pos0;
-    const int off = slot % page, seg = slot / page;
-    int pg = -1;
-    const bool fits = seg < (s == 0 ? p.L.doc_pages : p.L.seg_pages);
-    if (fits)
-      pg = page_of(s == 0 ? p.L.doc_table[seg]
-                          : p.L.seg_table[(int64_t)(s - 1) * p.L.seg_pages + seg], p.L.n_pages);
-    // rows of the run that fall into this page
-    const int most = min(page - off, p.n - i);
-    int nr = 1;
-    for (int r0 = 1; r0 < most; r0 += 32) {
-      const int r = r0 + lane;
-      const bool in = r < most && p.sid[i + r] == s && (int64_t)p.pos[i + r] == (int64_t)ps + r;
-      const uint32_t m = __ballot_sync(0xffffffffu, in);
-      nr = r0 + (m == 0xffffffffu ? 32 : __ffs(~m) - 1);
-      if (m != 0xffffffffu) break;
-    }
-    const float* angles = p.cos_sin + (int64_t)ps * p.rot;    // the rows' lie in a row
+    const int l = __ffs(w.leaders) - 1;
+    w.leaders &= w.leaders - 1;
+    const Lead x = open_lead(p, w0 + l, __shfl_sync(0xffffffffu, w.s, l),
+                             __shfl_sync(0xffffffffu, w.ps, l), lane);
+    const float* angles = p.cos_sin + (int64_t)x.ps * p.rot;  // the rows' lie in a row
     if (keep) {
-      const int n16 = min(nr, max(0, p.max_pos - ps)) * (p.rot / 4);
+      const int n16 = min(x.nr, max(0, p.max_pos - x.ps)) * (p.rot / 4);
       for (int c = threadIdx.x; c < n16; c += blockDim.x)
         cp_async16(smem_u32(staged + c * 4), angles + c * 4, 16);
       angles = staged;
     }
-    // The stream's run must be its only one and its positions consecutive:
-    // count the earlier rows of the stream and find the last row of another.
     int cnt = 0, last = -1;
-    scan_ids(p.sid, i, s, cnt, last);
+    scan_ids(p.sid, x.i, x.s, threadIdx.x, WARPS * 32, cnt, last);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       cnt += __shfl_xor_sync(0xffffffffu, cnt, o);
@@ -537,64 +586,116 @@ __global__ void __launch_bounds__(WARPS * 32, (SHORT ? 32 : 24) / WARPS)
     cnt = 0;
     last = -1;
 #pragma unroll
-    for (int w = 0; w < WARPS; ++w) {
-      cnt += red_cnt[w];
-      last = max(last, red_last[w]);
+    for (int v = 0; v < WARPS; ++v) {
+      cnt += red_cnt[v];
+      last = max(last, red_last[v]);
     }
-    const int a = last + 1;             // first row of the run
-    if (cnt != i - a || (int64_t)ps - p.pos[a] != i - a) err = PP_DEV_ROW_ORDER;
-    else if (!fits) err = s == 0 ? PP_DEV_DOC_OUT_OF_RANGE : PP_DEV_SEGMENT_OVERFLOW;
-    else if (pg < 0) err = PP_DEV_BAD_PAGE;
-    else err = p.rot && ps + nr > p.max_pos ? PP_DEV_BAD_POSITION : 0;   // past the angle table
-    if (err && first_cta && lane == 0) set_status(p.L.status, err);
+    const int nr = rows_of(p, x, cnt, last, first_cta && lane == 0);
     if (keep) {
       cp_async_wait_all();
       __syncthreads();
     }
-    if (err == PP_DEV_BAD_POSITION) nr = p.max_pos - ps;
-    else if (err) continue;
-    if (nr <= 0) continue;
+    if (nr == 0) continue;
     for (int h0 = hb; h0 < he; h0 += hpp) {
-      if constexpr (SHORT) {
-        const int h = h0 + warp * (256 / D) + lane / (D / 8);
-        write_short<D, INTER>(p, i, nr, ps, pg, off, h < he ? h : hb, h < he, lane);
-      } else {
-        const int h = h0 + warp / wph;
-        write_group<D, WARPS, INTER>(p, i, nr, pg, off, h, h < he, warp % wph, wph, red[buf],
-                                     stage + warp * Stage16<D>::BYTES, angles, warp, lane);
-        buf ^= 1;
-      }
+      const int h = h0 + warp / wph;
+      write_group<D, WARPS, INTER>(p, x.i, nr, x.pg, x.off, h, h < he, warp % wph, wph, red[buf],
+                                   stage + warp * Stage16<D>::BYTES, angles, warp, lane);
+      buf ^= 1;
+    }
+  }
+}
+
+// For calls of many short runs: a warp takes a leader of the window by itself, and
+// the block's warps together the runs of more than kAlone rows.  (One warp for any
+// run: a question of 250 rows took 60 us, a document's 1000 133.)
+constexpr int kAlone = 2;
+template <int D, bool INTER>
+__global__ void __launch_bounds__(kShortWarps * 32, 32 / kShortWarps)
+    kv8_append_short(const AppendParams p) {
+  constexpr int HW = 256 / D;           // heads a warp takes side by side
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int w0 = blockIdx.x * p.win;
+  const int w1 = min(p.n, w0 + p.win);
+  if ((int)blockIdx.y >= p.ys) {
+    const int part = blockIdx.y - p.ys, parts = gridDim.y - p.ys;
+    turn_queries<D, kShortWarps, INTER>(p, w0, w1, p.Hq * part / parts, p.Hq * (part + 1) / parts,
+                                        warp, lane);
+    return;
+  }
+  __shared__ int rows[32];              // of a leader, where the block shares it
+  __shared__ int page_at[32], off_at[32];
+  __shared__ float2 red[2][kShortWarps][HW];
+  const int hb = p.L.H * (int)blockIdx.y / p.ys, he = p.L.H * ((int)blockIdx.y + 1) / p.ys;
+  const Window w = look(p, w0, w1, blockIdx.y == 0 && warp == 0, lane);
+  const int hl = lane / (D / 8);
+  int k = 0;
+  for (uint32_t m = w.leaders; m; m &= m - 1, ++k) {
+    if (k % kShortWarps != warp) continue;
+    const int l = __ffs(m) - 1;
+    const Lead x = open_lead(p, w0 + l, __shfl_sync(0xffffffffu, w.s, l),
+                             __shfl_sync(0xffffffffu, w.ps, l), lane);
+    int cnt = 0, last = -1;
+    scan_ids(p.sid, x.i, x.s, lane, 32, cnt, last);
+    cnt = __reduce_add_sync(0xffffffffu, cnt);
+    last = __reduce_max_sync(0xffffffffu, last);
+    const int nr = rows_of(p, x, cnt, last, blockIdx.y == 0 && lane == 0);
+    if (lane == 0) {
+      rows[l] = nr > kAlone ? nr : 0;
+      page_at[l] = x.pg;
+      off_at[l] = x.off;
+    }
+    if (nr == 0 || nr > kAlone) continue;
+    for (int h0 = hb; h0 < he; h0 += HW) {
+      const int h = h0 + hl;
+      write_short<D, INTER, 1>(p, x.i, nr, x.ps, x.pg, x.off, h < he ? h : hb, h < he, nullptr, warp,
+                               lane);
+    }
+  }
+  if (w.leaders == 0) return;           // (the same in every warp)
+  __syncthreads();
+  int buf = 0;
+  for (uint32_t m = w.leaders; m; m &= m - 1) {
+    const int l = __ffs(m) - 1, nr = rows[l];
+    if (nr == 0) continue;
+    const int ps = __shfl_sync(0xffffffffu, w.ps, l);
+    for (int h0 = hb; h0 < he; h0 += HW) {
+      const int h = h0 + hl;
+      write_short<D, INTER, kShortWarps>(p, w0 + l, nr, ps, page_at[l], off_at[l], h < he ? h : hb,
+                                         h < he, &red[buf], warp, lane);
+      buf ^= 1;
     }
   }
 }
 
 __global__ void kv8_clear_status(int32_t* status) { *status = 0; }
 
-template <int D, int WARPS, bool SHORT, bool INTER>
-cudaError_t start_as(const AppendParams& p, dim3 grid, cudaStream_t st) {
+template <int D, int WARPS, bool INTER>
+cudaError_t start_long(const AppendParams& p, dim3 grid, cudaStream_t st) {
   // the stages, and the angles of a page's rows
-  constexpr int MOST = SHORT ? 0 : WARPS * Stage16<D>::BYTES + 8192;
-  const int smem = SHORT ? 0
-                         : WARPS * Stage16<D>::BYTES +
-                               (keep_angles(p.L.page, p.rot) ? p.L.page * p.rot * 4 : 0);
+  constexpr int MOST = WARPS * Stage16<D>::BYTES + 8192;
+  const int smem = WARPS * Stage16<D>::BYTES +
+                   (keep_angles(p.L.page, p.rot) ? p.L.page * p.rot * 4 : 0);
   static std::atomic<uint64_t> ready{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const uint64_t bit = 1ull << (dev & 63);
-  if (!SHORT && !(ready.load() & bit)) {
-    e = cudaFuncSetAttribute(kv8_append<D, WARPS, SHORT, INTER>,
+  if (!(ready.load() & bit)) {
+    e = cudaFuncSetAttribute(kv8_append<D, WARPS, INTER>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, MOST);
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit);
   }
-  kv8_append<D, WARPS, SHORT, INTER><<<grid, WARPS * 32, smem, st>>>(p);
+  kv8_append<D, WARPS, INTER><<<grid, WARPS * 32, smem, st>>>(p);
   return cudaGetLastError();
 }
-template <int D, int WARPS, bool SHORT>
-cudaError_t start(const AppendParams& p, dim3 grid, cudaStream_t st) {
-  return p.interleaved ? start_as<D, WARPS, SHORT, true>(p, grid, st)
-                       : start_as<D, WARPS, SHORT, false>(p, grid, st);
+template <int D, bool INTER>
+cudaError_t start(const AppendParams& p, bool brief, int warps, dim3 grid, cudaStream_t st) {
+  if (brief) {
+    kv8_append_short<D, INTER><<<grid, kShortWarps * 32, 0, st>>>(p);
+    return cudaGetLastError();
+  }
+  return warps == 8 ? start_long<D, 8, INTER>(p, grid, st) : start_long<D, 4, INTER>(p, grid, st);
 }
 
 }  // namespace
@@ -628,10 +729,10 @@ cudaError_t launch_kv8_append(const pp_kv8_layer& L, const pp_kv8_append_args& a
   // (One row by a warp of the long form: a decode step of 256 streams, 32 heads
   // took 54 us; questions by the short form 159 us.)
   const bool brief = n <= L.P_max;
-  const int warps = !brief && L.page == 128 ? 8 : 4;
-  const int hpp = brief ? warps * 256 / L.d : warps / (L.page >> 4);
+  const int warps = brief ? kShortWarps : L.page == 128 ? 8 : 4;
+  const int hpp = brief ? 256 / L.d : warps / (L.page >> 4);
   const int passes = (L.H + hpp - 1) / hpp;
-  p.win = 1;
+  p.win = brief ? kShortWarps : 1;
   const int64_t most = (brief ? 32LL : 8LL) * num_sms;   // (a short form's block is small)
   while (p.win < 32 && (int64_t)((n + p.win - 1) / p.win) * passes > most) p.win *= 2;
   const int64_t wins = (n + p.win - 1) / p.win;
@@ -643,12 +744,10 @@ cudaError_t launch_kv8_append(const pp_kv8_layer& L, const pp_kv8_append_args& a
   const int qs = (Hq + qh - 1) / qh;
   const dim3 grid((unsigned)wins, p.ys + qs);
   if (L.d == 128)
-    return brief        ? start<128, 4, true>(p, grid, st)
-           : warps == 8 ? start<128, 8, false>(p, grid, st)
-                        : start<128, 4, false>(p, grid, st);
-  return brief        ? start<64, 4, true>(p, grid, st)
-         : warps == 8 ? start<64, 8, false>(p, grid, st)
-                      : start<64, 4, false>(p, grid, st);
+    return p.interleaved ? start<128, true>(p, brief, warps, grid, st)
+                         : start<128, false>(p, brief, warps, grid, st);
+  return p.interleaved ? start<64, true>(p, brief, warps, grid, st)
+                       : start<64, false>(p, brief, warps, grid, st);
 }
 
 }  // namespace pp
