@@ -606,8 +606,9 @@ __global__ void __launch_bounds__(WARPS * 32, 24 / WARPS) kv8_append(const Appen
 }
 
 // For calls of many short runs: a warp takes a leader of the window by itself, and
-// the block's warps together the runs of more than kAlone rows.  (One warp for any
-// run: a question of 250 rows took 60 us, a document's 1000 133.)
+// the block's warps together the runs of more than kAlone rows.  (All rows of a run
+// by the warp that has its heads: a step of 256 rows, 32 heads 7.1 us, so 7.8; but a
+// question of 250 rows 60 and 22, a document's 1000 133 and 46.)
 constexpr int kAlone = 2;
 template <int D, bool INTER>
 __global__ void __launch_bounds__(kShortWarps * 32, 32 / kShortWarps)
@@ -628,9 +629,12 @@ __global__ void __launch_bounds__(kShortWarps * 32, 32 / kShortWarps)
   const int hb = p.L.H * (int)blockIdx.y / p.ys, he = p.L.H * ((int)blockIdx.y + 1) / p.ys;
   const Window w = look(p, w0, w1, blockIdx.y == 0 && warp == 0, lane);
   const int hl = lane / (D / 8);
-  int k = 0;
-  for (uint32_t m = w.leaders; m; m &= m - 1, ++k) {
-    if (k % kShortWarps != warp) continue;
+  auto skip = [](uint32_t m, int k) {   // all but its first k leaders
+#pragma unroll
+    for (int z = 0; z < kShortWarps; ++z) m = z < k ? m & (m - 1) : m;
+    return m;
+  };
+  for (uint32_t m = skip(w.leaders, warp); m; m = skip(m, kShortWarps)) {
     const int l = __ffs(m) - 1;
     const Lead x = open_lead(p, w0 + l, __shfl_sync(0xffffffffu, w.s, l),
                              __shfl_sync(0xffffffffu, w.ps, l), lane);
@@ -639,8 +643,8 @@ __global__ void __launch_bounds__(kShortWarps * 32, 32 / kShortWarps)
     cnt = __reduce_add_sync(0xffffffffu, cnt);
     last = __reduce_max_sync(0xffffffffu, last);
     const int nr = rows_of(p, x, cnt, last, blockIdx.y == 0 && lane == 0);
-    if (lane == 0) {
-      rows[l] = nr > kAlone ? nr : 0;
+    if (lane == 0) rows[l] = nr > kAlone ? nr : 0;
+    if (nr > kAlone && lane == 0) {
       page_at[l] = x.pg;
       off_at[l] = x.off;
     }
@@ -726,8 +730,8 @@ cudaError_t launch_kv8_append(const pp_kv8_layer& L, const pp_kv8_append_args& a
   // that out costs a launch slot) and shares small, as far as the grid stays
   // between a few CTAs an SM and about 64.
   // A stream has one run a call, so more rows than streams means long runs.
-  // (One row by a warp of the long form: a decode step of 256 streams, 32 heads
-  // took 54 us; questions by the short form 159 us.)
+  // (A decode step of 256 streams, 32 heads by the long form took 54 us, a question
+  // of 250 rows 12 by it and 22 by the short one.)
   const bool brief = n <= L.P_max;
   const int warps = brief ? kShortWarps : L.page == 128 ? 8 : 4;
   const int hpp = brief ? 256 / L.d : warps / (L.page >> 4);

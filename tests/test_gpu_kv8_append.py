@@ -196,6 +196,41 @@ def test_long_runs_over_many_windows():
     call(layer, rep, sid, pos, 2)
 
 
+@pytest.mark.parametrize("H,d,page,rot,inter", [(3, 128, 64, 128, False), (5, 64, 16, 32, True),
+                                                (2, 128, 128, 0, False), (9, 64, 32, 64, False)])
+def test_long_runs_among_fewer_rows_than_streams(H, d, page, rot, inter):
+    """Calls of fewer rows than the cache has streams, with runs of one, two, three and many
+    rows side by side, a NaN far inside a run, pages whose scale grows, runs that end the
+    angles or repeat."""
+    m = pp()
+    N, P = 150, 700
+    layer, rep = new_cache(H, d, page, P, -(-260 // page), N, seed=H)
+    rope = m.Rope.make(N + 230, rot, interleaved=inter, device=DEV) if rot else None
+    assert call(layer, rep, [0] * N, list(range(N)), 1, rope, Hq=2 * H) == []
+    lens = [1, 2, 3, 4, 1, 200, 1, 1, 5, 65, 2, 1, 1, 1, 3, 130]
+    sid = sum(([600 - 7 * s] * n for s, n in enumerate(lens)), [])
+    pos = sum((list(range(N, N + n)) for n in lens), [])
+
+    def poke(q, k, v):
+        k[60, H - 1, 7] = float("nan")
+        v[100, 0, d - 1] = float("nan")
+        v[300, 0, 0] = float("inf")
+
+    assert call(layer, rep, sid, pos, 2, rope, Hq=H, poke=poke) == []
+    assert m.kv8_device_status(layer) == m.PP_DEV_NONFINITE
+    m.kv8_reset(layer)
+    more = [3, 1, 9, 17, 2, 25, 1]
+    sid = sum(([600 - 7 * s] * n for s, n in enumerate(more)), []) + [600]
+    pos = sum((list(range(N + lens[s], N + lens[s] + n)) for s, n in enumerate(more)), []) + [N + 4]
+    got = call(layer, rep, sid, pos, 3, rope, mag=256.0)
+    assert got == [len(sid) - 1]
+    assert m.kv8_device_status(layer) == m.PP_DEV_ROW_ORDER
+    m.kv8_reset(layer)
+    if rot:          # past the angles
+        assert call(layer, rep, [565] * 20, list(range(N + 225, N + 245)), 4, rope) == list(range(5, 20))
+        assert m.kv8_device_status(layer) == m.PP_DEV_BAD_POSITION
+
+
 def test_pages_past_two_and_four_gib():
     """A pool whose last pages lie more than 4 GiB behind its first."""
     m = pp()
