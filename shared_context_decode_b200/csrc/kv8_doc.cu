@@ -23,7 +23,7 @@
 // softmax runs, the tensor core works for the other; a converted tile serves
 // both M tiles.  Warp roles (512 threads):
 //   warp 0       loader: bulk copies of page chunks to shared memory, page
-//                tables and scales
+//                tables and scales (d 64: of the keys, warp 3 of the values)
 //   warp 1       MMA issuer          warp 2   TMEM allocator
 //   warps 4-7    e4m3 -> f16 into the MMA's 128-byte-swizzled layout
 //   warps 8-15   softmax, one thread a row; queries to f16; partial results
@@ -82,14 +82,21 @@ struct Cfg8 {
   static constexpr int TILE = KH * BOX;           // f16 tile of queries, keys or values
   static constexpr int RAW = 128 * D;             // e4m3 tile
   static constexpr int NF = 4;                    // f16 key / value tiles (alternating)
-  static constexpr int NR = D == 128 ? 2 : 4;     // e4m3 key / value tiles (alternating)
+  static constexpr int NR = D == 128 ? 1 : 2;     // e4m3 tiles of keys, and as many of values
+  // Keys and values each by their own loader and two converting warps, or one
+  // loader and four warps for both in turn.  Apart, a tile waits for nothing of
+  // the other kind's, which pays where two tiles of a kind fit (d 64, 64 / 256
+  // rows, 32768 keys: 92 -> 72 / 123 -> 117 us); with one (d 128: 107 -> 113 /
+  // 130 -> 133) it costs more than it gives.
+  static constexpr bool APART = NR > 1;
+  static constexpr int CONV = APART ? 2 : 4;      // warps that convert a tile
   static constexpr int OFF_F = 2 * TILE;
   static constexpr int OFF_R = OFF_F + NF * TILE;
-  static constexpr int OFF_INFO = OFF_R + NR * RAW;
+  static constexpr int OFF_INFO = OFF_R + 2 * NR * RAW;
   static constexpr int OFF_BAR = OFF_INFO + kInfo * kInfoLd * 8;
-  // raw_full[NR], raw_empty[NR], f_full[NF], f_empty[NF], q_full[2], s_full[2],
+  // raw_full[2 NR], raw_empty[2 NR] (keys, values), f_full[NF], f_empty[NF], q_full[2], s_full[2],
   // p_full[2], o_done[2], drain
-  static constexpr int NBAR = 2 * NR + 2 * NF + 9;
+  static constexpr int NBAR = 4 * NR + 2 * NF + 9;
   static constexpr int USED = OFF_BAR + NBAR * 8 + 8;   // TMEM base and abort flag last
   // at least 120 KB so one CTA owns an SM's TMEM
   static constexpr int SMEM = USED > 120 * 1024 ? USED : 120 * 1024;
@@ -216,8 +223,8 @@ __global__ void __maxnreg__(kRegs8) kv8_doc_tc(const Doc8Params p) {
   }
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* raw_full = bar;
-  uint64_t* raw_empty = raw_full + C::NR;
-  uint64_t* f_full = raw_empty + C::NR;
+  uint64_t* raw_empty = raw_full + 2 * C::NR;
+  uint64_t* f_full = raw_empty + 2 * C::NR;
   uint64_t* f_empty = f_full + C::NF;
   uint64_t* q_full = f_empty + C::NF;
   uint64_t* s_full = q_full + 2;
@@ -232,12 +239,12 @@ __global__ void __maxnreg__(kRegs8) kv8_doc_tc(const Doc8Params p) {
   int32_t* status = p.L.status;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < C::NR; ++i) {
+    for (int i = 0; i < 2 * C::NR; ++i) {
       mbar_init(raw_full + i, 1);
-      mbar_init(raw_empty + i, 4);
+      mbar_init(raw_empty + i, C::CONV);
     }
     for (int i = 0; i < C::NF; ++i) {
-      mbar_init(f_full + i, 4);
+      mbar_init(f_full + i, C::CONV);
       mbar_init(f_empty + i, 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -261,7 +268,7 @@ __global__ void __maxnreg__(kRegs8) kv8_doc_tc(const Doc8Params p) {
   // the segment pass may fill SMs as this pass's CTAs end
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  if (warp == 0) {
+  if (warp == 0 || (C::APART && warp == 3)) {
     // ------------------------------------------------------------ loader ----
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCtl));
     const int page = p.L.page, ppt = kBN / page;   // pages per tile
@@ -269,7 +276,8 @@ __global__ void __maxnreg__(kRegs8) kv8_doc_tc(const Doc8Params p) {
     const int per = 32 / ppt;                      // tiles per batch of 32 pages, a lane each
     Runs8 t = runs;
     Seg8 s;
-    int ht = 0, kt = 0;
+    const int kind = warp == 3;                    // where apart: 0 keys, 1 values
+    int kt = 0, ht = 0;                            // tiles; copies this warp started
     bool ok = true;
     // Table entries are loaded two batches ahead, scales one, so that neither
     // dependent load stands between two tiles' copies.
@@ -314,36 +322,42 @@ __global__ void __maxnreg__(kRegs8) kv8_doc_tc(const Doc8Params p) {
         for (int o = 4; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
         total = __shfl_sync(0xffffffffu, total, 0);   // lanes 0..7 hold all pages of a tile
         const int64_t at = ((int64_t)(pg < 0 ? 0 : pg) * p.L.H + s.h) * page * D;
-        for (int kv = 0; kv < 2; ++kv, ++ht) {
-          const int sl = ht % C::NR, f = ht / C::NR;
-          if (f > 0 &&
-              !(ok = warp_wait(raw_empty + sl, (f - 1) & 1, abort_flag, p.wait_limit, status)))
+        const int sl = kt % C::NR, f = kt / C::NR;
+        for (int x = 0; x < (C::APART ? 1 : 2); ++x) {
+          const int kv = C::APART ? kind : x;
+          uint64_t* full = raw_full + kv * C::NR + sl;
+          if (f > 0 && !(ok = warp_wait(raw_empty + kv * C::NR + sl, (f - 1) & 1, abort_flag,
+                                        p.wait_limit, status)))
             break;
-          if (kv == 0 && lane < ppt) {
+          // (two loaders write the same scales: the softmax reads them behind the keys'
+          // arrival, the values' converter behind the values')
+          if ((C::APART || kv == 0) && lane < ppt) {
             for (int gq = 0; gq < groups; ++gq) {
               info[(kt % kInfo) * kInfoLd + lane * groups + gq] =
                   n > gq * 16 ? make_float2(ks, (float)((int)(__float_as_uint(vs) >> 23) - 127))
                               : make_float2(1.f, -INFINITY);
             }
           }
-          if (kv == 0 && lane == 0)
+          if ((C::APART || kv == 0) && lane == 0)
             info[(kt % kInfo) * kInfoLd + 8].x = total < (uint32_t)(kBN * D) ? 1.f : 0.f;
           __syncwarp();
-          if (lane == 0) mbar_arrive_expect_tx(raw_full + sl, total);
+          if (lane == 0) mbar_arrive_expect_tx(full, total);
           __syncwarp();
-          if (bytes && !(p.inject_timeout && ht == 0))   // test hook: this copy never lands
-            bulk_load(smem + C::OFF_R + sl * C::RAW + lane * page * D, (kv ? p.L.v : p.L.k) + at,
-                      bytes, raw_full + sl);
+          if (bytes && !(p.inject_timeout && kt + kv == 0))   // test hook: this copy never lands
+            bulk_load(smem + C::OFF_R + (kv * C::NR + sl) * C::RAW + lane * page * D,
+                      (kv ? p.L.v : p.L.k) + at, bytes, full);
+          ++ht;
         }
       }
     }
     if (!ok && lane == 0) {
       // Drain: wait (bounded, abort flag ignored) for the copies still in flight.
-      for (int back = 1; back <= C::NR && ht - back >= 0; ++back) {
-        const int k2 = ht - back;
-        if (p.inject_timeout && k2 == 0) continue;
+      for (int back = 1; back <= (C::APART ? 1 : 2) * C::NR && ht - back >= 0; ++back) {
+        const int kv = C::APART ? kind : (ht - back) & 1, k2 = C::APART ? ht - back : (ht - back) >> 1;
+        if (p.inject_timeout && k2 + kv == 0) continue;
         volatile int never = 0;
-        mbar_wait(raw_full + k2 % C::NR, (k2 / C::NR) & 1, &never, p.wait_limit, nullptr);
+        mbar_wait(raw_full + kv * C::NR + k2 % C::NR, (k2 / C::NR) & 1, &never, p.wait_limit,
+                  nullptr);
       }
     }
   } else if (warp == 1) {
@@ -438,8 +452,8 @@ __global__ void __maxnreg__(kRegs8) kv8_doc_tc(const Doc8Params p) {
     // eight threads that access shared memory together take two rows, with u
     // dealt out so that their loads and both of their stores meet 32 different
     // banks.  RS is a multiple of 8: the swizzle is the same for all rows.
-    constexpr int UR = D / 16, RS = 128 / UR, IT = 128 / RS;
-    const int tid = threadIdx.x - 128;
+    constexpr int NT = C::CONV * 32, UR = D / 16, RS = NT / UR, IT = 128 / RS;
+    const int kind = (warp - 4) >> 1, tid = threadIdx.x % NT;
     const int sub = tid & 7;
     const int u = D == 128 ? sub : sub & 3;
     const int r0 = D == 128 ? (tid >> 4) * 2 + ((sub >> 2) ^ ((tid >> 3) & 1)) : tid >> 2;
@@ -449,15 +463,16 @@ __global__ void __maxnreg__(kRegs8) kv8_doc_tc(const Doc8Params p) {
     const int dst1 = (u >> 2) * C::BOX + r0 * 128 + (((ua + 1) ^ (r0 & 7)) << 4);
     Runs8 t = runs;
     Seg8 s;
-    int ht = 0, kt = 0;
+    int kt = 0;
     bool ok = true;
     while (ok && next_seg8(p, t, s)) {
       for (int j = 0; ok && j < s.n; ++j, ++kt) {
-        for (int kv = 0; kv < 2; ++kv, ++ht) {
-          const int sr = ht % C::NR, sf = ht % C::NF;
-          if (!(ok = warp_wait(raw_full + sr, (ht / C::NR) & 1, abort_flag, p.wait_limit, status)))
+        for (int x = 0; x < (C::APART ? 1 : 2); ++x) {
+          const int kv = C::APART ? kind : x;
+          const int sr = kv * C::NR + kt % C::NR, ft = 2 * kt + kv, sf = ft % C::NF;
+          if (!(ok = warp_wait(raw_full + sr, (kt / C::NR) & 1, abort_flag, p.wait_limit, status)))
             break;
-          if (ht >= C::NF && !(ok = warp_wait(f_empty + sf, (ht / C::NF - 1) & 1, abort_flag,
+          if (ft >= C::NF && !(ok = warp_wait(f_empty + sf, (ft / C::NF - 1) & 1, abort_flag,
                                               p.wait_limit, status)))
             break;
           const uint8_t* src = smem + C::OFF_R + sr * C::RAW + src0;

@@ -370,6 +370,18 @@ def test_any_split_of_the_document_gives_the_same(splits):
     run(layer, doc, segs, N, sid, pos, 5, "decode", opt=m.Options(splits=splits))
 
 
+@pytest.mark.parametrize("P,page,splits", [(40, 16, 3), (40, 128, 0), (300, 32, 7), (300, 64, 0)])
+def test_long_documents_of_64_dims(P, page, splits):
+    """Many tiles a run, keys and values brought in by separate warps; the last
+    tile ends inside a page."""
+    m = pp()
+    N = 6001
+    layer, doc, segs = make_cache(2, 64, page, N, [5] * P, seed=P + page)
+    sid, pos = list(range(1, P + 1)), [N + 4] * P
+    run(layer, doc, segs, N, sid, pos, 1, "decode", opt=m.Options(splits=splits) if splits else None)
+    assert m.kv8_device_status(layer) == 0
+
+
 def test_pool_past_four_gib():
     """Pages that lie more than 4 GiB behind the pool's first, read by both
     kernels."""
