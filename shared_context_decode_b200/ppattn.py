@@ -561,8 +561,14 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
+def _on_gpu(layer, name: str):
+    if layer.index < 0:
+        raise ValueError(f"{name}: the layer must be on a CUDA device, is on {layer.device}")
+
+
 def _call8(fn, name: str, layer, arg):
     """fn(layer, arg, stream) on the layer's device and its current stream."""
+    _on_gpu(layer, name)
     cur = _current_device()
     if cur != layer.index:
         with torch.cuda.device(layer.index):
@@ -575,6 +581,7 @@ def _call8(fn, name: str, layer, arg):
 
 def kv8_reset(layer: KV8Layer):
     """Clear the layer's status word."""
+    _on_gpu(layer, "pp_kv8_reset")
     with torch.cuda.device(layer.index):
         _check(_kv8_reset(layer.ref, _stream(layer.device)), "pp_kv8_reset")
 
@@ -647,6 +654,7 @@ def _kv8_attn(fn, name, layer, doc_len, q, q_sid, q_pos, scale, o, lse, ws, opt,
             raise ValueError(f"{name}: lse must be [rows, Hq]")
         lse_at = lse.data_ptr()
     if ws is None:
+        _on_gpu(layer, name)
         with torch.cuda.device(layer.index):
             ws = workspace(ws_fn(rows, Hq, layer.H, layer.d, doc_len, opt), layer.device)
     _want8(ws, _U8, "ws", layer)

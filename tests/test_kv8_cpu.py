@@ -182,3 +182,16 @@ def test_oracle_page_grows_and_rounds_again():
     assert np.array_equal(r.k[1, 0, 0], e4m3(x * 2.0 ** -10))
     assert r.append(k, k, [1], [0]) == [] and r.k_scale[1, 0] == 2.0 ** -8   # afresh
     assert r.append(np.repeat(k, 3, 0), np.repeat(k, 3, 0), [1, 0, 1], [1, 0, 2]) == [1, 2]
+
+
+def test_a_layer_in_host_memory_reaches_no_kernel(pp):
+    L = pp.KV8Layer(2, 64, 16, 4, 2, 1, 1, 4, device="cpu")
+    k = torch.zeros((2, 2, 64), dtype=torch.bfloat16)
+    s, p = torch.ones(2, dtype=torch.int16), torch.tensor([4, 5], dtype=torch.int32)
+    ws = torch.empty(256, dtype=torch.uint8)
+    for call in (lambda: pp.kv8_append(L, k, k, s, p), lambda: pp.kv8_reset(L),
+                 lambda: pp.kv8_decode_attn(L, 4, k, s, p, 0.1),
+                 lambda: pp.kv8_prefill_attn(L, 4, k, s, p, 0.1, ws=ws),
+                 lambda: pp.kv8_device_status(L)):
+        with pytest.raises(ValueError, match="CUDA device"):
+            call()
