@@ -131,12 +131,11 @@ __device__ __forceinline__ float2 ex2_poly2_clamped(float2 x) {
 __device__ __forceinline__ float2 ex2_poly2(float2 x) {
   return ex2_poly2_clamped(make_float2(fmaxf(x.x, -126.f), fmaxf(x.y, -126.f)));
 }
-// The same, but a NaN gives a huge number (0x7f7fffff: the canonical NaN's bits
-// plus the exponent a NaN leaves) and not 2^-126.
+// For any x: from 127 on 2^127 (above it the sum of exponents would wrap, to a small
+// or negative number), which a NaN gives too.
 __device__ __forceinline__ float2 ex2_poly2_nan(float2 x) {
-  asm("max.NaN.f32 %0, %0, %1;" : "+f"(x.x) : "f"(-126.f));
-  asm("max.NaN.f32 %0, %0, %1;" : "+f"(x.y) : "f"(-126.f));
-  return ex2_poly2_clamped(x);
+  return ex2_poly2_clamped(make_float2(fmaxf(fminf(x.x, 127.f), -126.f),
+                                       fmaxf(fminf(x.y, 127.f), -126.f)));
 }
 
 // Softmax exponentials: pairs p with p % 5 in {1, 3} go to the FMA-pipe

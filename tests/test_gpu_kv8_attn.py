@@ -449,6 +449,34 @@ def test_maximum_that_keeps_rising():
         assert np.abs(lse.cpu().numpy() - rl).max() <= 2.0 ** -8
 
 
+@pytest.mark.parametrize("scale", [0.05, 0.22, 0.5, 0.9])
+@pytest.mark.parametrize("d", [64, 128])
+def test_one_key_far_above_all_before_it(d, scale):
+    """A single key, at another place of its 16 in every head, whose score is up to
+    1200 binades above the reference that the tiles before it gave."""
+    m = pp()
+    N, H, rows, page = 900, 16, 40, 32
+    layer, doc, segs = make_cache(H, d, page, N, [9] * rows, seed=31, spread=0)
+    q = torch.ones((rows, H, d), dtype=torch.bfloat16, device=DEV)
+    s, p = ids(list(range(1, rows + 1)), [N + 8] * rows)
+    k = layer.k.view(torch.uint8)
+    for h in range(H):
+        t = 640 + h
+        k[layer.doc_table[t // page].item(), h, t % page] = 0x7e          # 448 * 2^-6
+        doc[0][t, h] = 7.0
+    for splits in (1, 5):
+        lse = torch.zeros((rows, H), device=DEV)
+        o = m.kv8_decode_attn(layer, N, q, s, p, scale, lse=lse, opt=m.Options(splits=splits))
+        torch.cuda.synchronize()
+        # the score is 7 d scale <= 807: 1164 in base 2, whose five roundings of 2^-24
+        # are 2^-11.5, of a probability and (times ln 2) of lse
+        ref = oracle_attn(doc, segs, N, q.cpu(), s.cpu().numpy(), p.cpu().numpy(), scale)
+        err = np.abs(o.float().cpu().numpy() - ref[0])
+        tol = 2.0 ** -8 * np.abs(ref[0]) + (2.0 ** -10 + 2.0 ** -12 + 2.0 ** -10.5) * ref[2] + 1e-30
+        assert (err <= tol).all(), (err / tol).max()
+        assert np.abs(lse.cpu().numpy() - ref[1]).max() <= 2.0 ** -11.5 + 2.0 ** -12
+
+
 @pytest.mark.parametrize("splits", [0, 2])
 def test_queries_and_pages_of_zeros_and_tiny_factors(splits):
     """Queries of zeros and of bf16's smallest normals, an all-zero page at the
