@@ -114,7 +114,8 @@ __device__ __forceinline__ float ex2_mufu(float x) {
 // clamped at -126 (2^f can be just below 1, exponent field 126, so n >= -126
 // keeps the field >= 0): -inf and underflow give at most 2^-125, zero for
 // every use here.  Valid for x <= 64.
-__device__ __forceinline__ float2 ex2_poly2_clamped(float2 x) {
+__device__ __forceinline__ float2 ex2_poly2(float2 x) {
+  x = make_float2(fmaxf(x.x, -126.f), fmaxf(x.y, -126.f));
   constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23
   const float2 t = fadd2_rm(x, make_float2(kMagic, kMagic));
   const float2 n = fadd2(t, make_float2(-kMagic, -kMagic));
@@ -128,14 +129,22 @@ __device__ __forceinline__ float2 ex2_poly2_clamped(float2 x) {
   r.y = __int_as_float(__float_as_int(p.y) + (__float_as_int(t.y) << 23));
   return r;
 }
-__device__ __forceinline__ float2 ex2_poly2(float2 x) {
-  return ex2_poly2_clamped(make_float2(fmaxf(x.x, -126.f), fmaxf(x.y, -126.f)));
-}
-// For any x: from 127 on 2^127 (above it the sum of exponents would wrap, to a small
-// or negative number), which a NaN gives too.
-__device__ __forceinline__ float2 ex2_poly2_nan(float2 x) {
-  return ex2_poly2_clamped(make_float2(fmaxf(fminf(x.x, 127.f), -126.f),
-                                       fmaxf(fminf(x.y, 127.f), -126.f)));
+// The same by a degree-4 polynomial (relative minimax on [0, 1) by Remez exchange,
+// 2.7e-6 in fp32), for sums that are an answer themselves, and for any x: from 127 on
+// 2^127 (above it the sum of exponents would wrap, to a small or negative number),
+// which a NaN gives too.
+__device__ __forceinline__ float2 ex2_poly2_wide(float2 x) {
+  constexpr float kMagic = 12582912.0f;
+  x = make_float2(fmaxf(fminf(x.x, 127.f), -126.f), fmaxf(fminf(x.y, 127.f), -126.f));
+  const float2 t = fadd2_rm(x, make_float2(kMagic, kMagic));
+  const float2 n = fadd2(t, make_float2(-kMagic, -kMagic));
+  const float2 f = fadd2(x, make_float2(-n.x, -n.y));
+  float2 p = ffma2(make_float2(0.0135341679f, 0.0135341679f), f, make_float2(0.0520114606f, 0.0520114606f));
+  p = ffma2(p, f, make_float2(0.241442757f, 0.241442757f));
+  p = ffma2(p, f, make_float2(0.693003834f, 0.693003834f));
+  p = ffma2(p, f, make_float2(1.00000259f, 1.00000259f));
+  return make_float2(__int_as_float(__float_as_int(p.x) + (__float_as_int(t.x) << 23)),
+                     __int_as_float(__float_as_int(p.y) + (__float_as_int(t.y) << 23)));
 }
 
 // Softmax exponentials: pairs p with p % 5 in {1, 3} go to the FMA-pipe

@@ -30,7 +30,7 @@
 // TMEM: O_0 | O_1 | S_0 | S_1, P over the first 64 columns of its S.
 //
 // Bound: the softmax warps' instruction latency.  At 256 rows, 32 heads and 16384
-// keys (73 us; 134 MB, 69 GFLOP) a tile of 256 rows takes a CTA about 3450
+// keys (75 us; 134 MB, 69 GFLOP) a tile of 256 rows takes a CTA about 3450
 // cycles: 1700 of exponentials on each stream, 1250 of products and hand-over
 // behind them, the other stream's under both; the tensor pipe is busy for half.
 //
@@ -597,11 +597,11 @@ __global__ void __maxnreg__(kRegs8) kv8_doc_tc(const Doc8Params p) {
               for (int e = 0; e < 16; e += 2) {
                 const float2 w = ffma2(make_float2(__uint_as_float(x[q * 16 + e]),
                                                    __uint_as_float(x[q * 16 + e + 1])), av, bv);
-                // three in eight on the FMA pipe (none / 1/8 / 1/4 / 3/8 / 1/2: 79 / 77 /
-                // 74 / 73 / 77 us at 256 rows, 32 heads, 16384 keys, 1416 / 1362 / 1312 /
-                // 1279 / 1382 at 8192 rows, 12000 keys)
-                const float2 pv = (e >> 1) % 8 % 3 == 1
-                                      ? ex2_poly2_nan(w)
+                // one in four on the FMA pipe (1/8, 1/4, 5/16, 3/8 of them: 1490 / 1511 /
+                // 1536 / 1599 us of a question prefill of 8192 rows, 12000 keys; decode of
+                // 256 rows, 16384 keys 133 / 130 / 130 / 131)
+                const float2 pv = (e >> 1) % 4 == 1
+                                      ? ex2_poly2_wide(w)
                                       : make_float2(ex2_mufu(w.x), ex2_mufu(w.y));
                 rs[(e >> 1) & 1] = fadd2(rs[(e >> 1) & 1], pv);
                 pk[c * 16 + q * 8 + (e >> 1)] = f2_to_h2(pv.x, pv.y);
