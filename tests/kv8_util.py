@@ -99,7 +99,7 @@ def check(o, lse, ref, what=""):
          2^-11 sum p|v|   the probabilities' own error: scores are fp32 sums of
                           128 exact products (128 * 2^-24 of |q||k| scale ~ 20:
                           2^-13), an exponential in fp32 or by a polynomial of
-                          8.4e-5 (2^-13.5), in numerator and denominator,
+                          2.7e-6 (2^-18), in numerator and denominator,
          2^-12 sum p|v|   probabilities below 2^-14 of the row's reference lose
                           2^-25 of it at most: 2^-13 over 4096 keys, twice
        and the scores' error on lse."""
