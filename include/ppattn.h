@@ -472,6 +472,10 @@ typedef struct pp_kv8_attn_args {
  * not there are skipped (PP_DEV_BAD_PAGE).  A query with a NaN or infinity
  * gives NaN.  A workspace serves one call in flight; calls ordered on one
  * stream may share it.
+ * A probability p is rounded to f16 together with its page's value scale vs:
+ * to 2^-11 of itself, but a key's share of o also to 2^-16 max(p vs), the
+ * largest of the row's keys (pages whose value scales lie 2^14 apart or more
+ * feel it).
  */
 pp_status pp_kv8_decode_attn(const pp_kv8_layer *layer, const pp_kv8_attn_args *args,
                              void *stream);
