@@ -516,6 +516,17 @@ pp_status pp_debug_split_plan_causal(int32_t doc_len, int32_t H, int32_t ctas, i
                                      int32_t h_out_len);
 
 /*
+ * Test aid (host only): the runs of document tiles that the 8-bit cache's document
+ * pass gives its CTAs, with `splits` as in pp_options (0: the calls' own choice, on a
+ * device of num_sms SMs).  h_out[0..4] = T (steps per unit), units, W, C (0: no
+ * pass), max_chunks; h_out[5] = number of runs; then per run six entries: CTA,
+ * unit, first tile, tiles, whether the unit has two M tiles, and a bit for each of
+ * the CTA's two streams that has a tile in the run.
+ */
+pp_status pp_debug_kv8_runs(int32_t rows, int32_t Hq, int32_t H, int32_t doc_len, int32_t decode,
+                            int32_t splits, int32_t num_sms, int64_t *h_out, int32_t h_out_len);
+
+/*
  * Test aid: the document pass's two base-2 exponentials on n device floats:
  * y_poly[i] from the FMA-pipe polynomial (range reduction + degree-3
  * minimax), y_hw[i] from the hardware ex2 instruction.  No counterpart on

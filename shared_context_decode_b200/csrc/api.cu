@@ -320,12 +320,12 @@ bool row_operand(const void* ptr, int64_t ld, int64_t heads, int32_t d) {
 // 18.8, 64 rows, 8 heads, 1024 keys 18.0 / 26.0; one row of one head, 16384
 // keys 57 / 92, 4 rows of 4 heads, 4096 keys 25.0 / 28.7, 1024 keys 14.1 / 12.6.
 SplitPlan kv8_plan(int32_t rows, int32_t Hq, int32_t H, int32_t doc_len, const pp_options* opt,
-                   bool decode) {
+                   bool decode, int sms) {
   const int64_t items = pp::kv8_items(rows, Hq / H, H, decode).items;
   const bool asked = opt && (opt->splits > 0 || opt->debug_inject_timeout);
   if (rows == 0 || doc_len == 0 || (!asked && doc_len <= 3000 && items * doc_len <= 400000))
     return SplitPlan{};
-  int ctas = asked && opt->splits > 0 ? opt->splits : sm_count();
+  int ctas = asked && opt->splits > 0 ? opt->splits : sms;
   SplitPlan p{};
   p.T = (doc_len + pp::kBN - 1) / pp::kBN + pp::kKv8Lead;
   p.G = (rows * (Hq / H) + pp::kGroupRows - 1) / pp::kGroupRows;
@@ -401,7 +401,7 @@ pp_status kv8_attend(const pp_kv8_layer* L, const pp_kv8_attn_args* a, void* str
   if ((int64_t)rows * Hq > INT32_MAX - 256) return PP_ERR_UNSUPPORTED;
   const int sms = sm_count();
   if (sms < 1) return PP_ERR_CUDA;
-  const SplitPlan plan = kv8_plan(rows, Hq, L->H, doc_len, opt, decode);
+  const SplitPlan plan = kv8_plan(rows, Hq, L->H, doc_len, opt, decode, sms);
   const bool doc_pass = plan.C > 0;
   // both kernels count in 32 bits
   if (plan.W > INT32_MAX ||
@@ -431,7 +431,27 @@ size_t kv8_workspace(int32_t rows, int32_t Hq, int32_t H, int32_t d, int32_t doc
                      const pp_options* opt, bool decode) {
   if (rows < 0 || H < 1 || Hq < 1 || Hq % H != 0 || (d != 64 && d != 128) || doc_len < 0) return 0;
   if ((int64_t)rows * Hq > INT32_MAX - 256) return 0;
-  return kv8_ws_layout(kv8_plan(rows, Hq, H, doc_len, opt, decode), d).total;
+  return kv8_ws_layout(kv8_plan(rows, Hq, H, doc_len, opt, decode, sm_count()), d).total;
+}
+
+// The document pass's runs of every CTA, as the kernel's roles walk them.
+pp_status write_kv8_runs(const SplitPlan& p, int rows, int64_t* h_out, int32_t h_out_len) {
+  if (h_out_len < 6) return PP_ERR_CAPACITY;
+  const int64_t head[5] = {p.T, p.units, p.W, p.C, p.max_chunks};
+  for (int i = 0; i < 5; ++i) h_out[i] = head[i];
+  int64_t runs = 0;
+  for (int cta = 0; cta < p.C; ++cta) {
+    pp::Runs8 r = pp::first_run8(p, cta);
+    pp::Seg8 s;
+    for (; pp::next_seg8(p, rows, r, s); ++runs) {
+      if (6 + 6 * (runs + 1) > h_out_len) return PP_ERR_CAPACITY;
+      const int64_t run[6] = {cta, s.u, s.j0, s.n, s.two,
+                              (int)pp::has_tile8(s, 0) + 2 * (int)pp::has_tile8(s, 1)};
+      for (int i = 0; i < 6; ++i) h_out[6 + 6 * runs + i] = run[i];
+    }
+  }
+  h_out[5] = runs;
+  return PP_OK;
 }
 
 // Host copy of a plan for the split-plan test aids.
@@ -630,6 +650,19 @@ PP_API pp_status pp_debug_split_plan_causal(int32_t doc_len, int32_t H, int32_t 
   return write_plan(make_plan(doc_len, H, doc_len, ctas, true), h_out, h_out_len);
 }
 
+PP_API pp_status pp_debug_kv8_runs(int32_t rows, int32_t Hq, int32_t H, int32_t doc_len,
+                                   int32_t decode, int32_t splits, int32_t num_sms, int64_t* h_out,
+                                   int32_t h_out_len) {
+  if (rows < 0 || H < 1 || Hq < 1 || Hq % H != 0 || doc_len < 0 || splits < 0 || num_sms < 1 ||
+      !h_out)
+    return PP_ERR_INVALID_ARG;
+  if ((int64_t)rows * Hq > INT32_MAX - 256) return PP_ERR_UNSUPPORTED;
+  pp_options opt{};
+  opt.splits = splits;
+  const SplitPlan p = kv8_plan(rows, Hq, H, doc_len, &opt, decode != 0, num_sms);
+  if (p.W > INT32_MAX) return PP_ERR_UNSUPPORTED;
+  return write_kv8_runs(p, rows * (Hq / H), h_out, h_out_len);
+}
 
 PP_API pp_status pp_debug_exp2(const float* x, float* y_poly, float* y_hw, int32_t n,
                                void* stream) {

@@ -74,6 +74,61 @@ __device__ __forceinline__ int page_of(int32_t entry, int n_pages) {
 // CTA of step kKv8Lead.
 constexpr int kKv8Lead = 4;
 
+// A run of tiles of one unit, (key head, row group), in a CTA of the document pass.
+// Steps are counted in 32 bits (the host sees to it), and only a CTA's first run
+// divides: 64-bit divisions at every role's start took 3600 cycles.
+struct Seg8 {
+  int u, h, gi, j0, n;
+  bool two;     // two M tiles; else one, its tiles dealt out to the streams
+};
+struct Runs8 {
+  int t, t_end, u, h, gi;
+};
+__host__ __device__ __forceinline__ Runs8 first_run8(const SplitPlan& p, int cta) {
+  Runs8 r;
+  const int q = (int)p.W / p.C, m = (int)p.W - q * p.C;   // floor(cta W / C)
+  r.t = cta * q + cta * m / p.C;
+  r.t_end = (cta + 1) * q + (cta + 1) * m / p.C;
+  r.u = r.t / p.T;
+  r.h = r.u / p.G;
+  r.gi = r.u - r.h * p.G;
+  return r;
+}
+// rows: (query row, query head) pairs of a key head.
+__host__ __device__ __forceinline__ bool next_seg8(const SplitPlan& p, int rows, Runs8& r,
+                                                   Seg8& s) {
+  while (r.t < r.t_end) {
+    s.u = r.u;
+    s.h = r.h;
+    s.gi = r.gi;
+    s.two = rows - s.gi * kGroupRows > 128;
+    const int v = r.t - r.u * p.T;              // step of the unit
+    const int n = p.T - v < r.t_end - r.t ? p.T - v : r.t_end - r.t;
+    r.t += n;
+    if (v + n == p.T) {
+      ++r.u;
+      if (++r.gi == p.G) {
+        r.gi = 0;
+        ++r.h;
+      }
+    }
+    s.j0 = v > kKv8Lead ? v - kKv8Lead : 0;
+    s.n = v + n - kKv8Lead - s.j0;
+    if (s.n > 0) return true;
+  }
+  return false;
+}
+// The first tile of stream st (0, 1) in a run, and whether it has one: a run of one
+// tile of one M tile leaves stream 1 without.  Such a stream takes no part in the
+// run's barriers: nothing would hold its warps back before their next run's arrival,
+// and a barrier two phases on looks to its waiter like one that has not moved.
+__host__ __device__ __forceinline__ int first_tile8(const Seg8& s, int st) {
+  return s.two ? 0 : st;
+}
+__host__ __device__ __forceinline__ bool has_tile8(const Seg8& s, int st) {
+  return first_tile8(s, st) < s.n;
+}
+
 // How the segment pass groups (query row, query head) pairs that share a key head
 // into a warp's item.  A decode step's rows belong to different streams, an item
 // each; question rows share their segment, so 16 pairs go together, unless that

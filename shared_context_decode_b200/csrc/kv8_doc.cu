@@ -67,7 +67,6 @@ struct Doc8Params {
   int rows;     // (query row, query head) pairs of a key head
   int doc_len;
   SplitPlan plan;
-  int steps;    // plan.W
   float sl2;
   float* doc_o;
   float* doc_ml;
@@ -104,50 +103,6 @@ struct Cfg8 {
   static constexpr uint32_t T_S = 2 * D, TMEM_COLS = 512;
   static_assert(T_S + 2 * kBN <= TMEM_COLS, "TMEM budget");
 };
-
-// A run of tiles of one unit, (key head, row group).  The plan counts steps: a
-// unit's tiles, and kKv8Lead ahead of them for what starting a run costs.  Steps
-// are counted in 32 bits (the host sees to it), and only a CTA's first run
-// divides: 64-bit divisions at every role's start took 3600 cycles.
-struct Seg8 {
-  int u, h, gi, j0, n;
-  bool two;     // two M tiles; else one, its tiles dealt out to the streams
-};
-struct Runs8 {
-  int t, t_end, u, h, gi;
-};
-__device__ __forceinline__ Runs8 first_run8(const Doc8Params& p, int cta) {
-  Runs8 r;
-  const int q = p.steps / p.plan.C, m = p.steps - q * p.plan.C;   // floor(cta W / C)
-  r.t = cta * q + cta * m / p.plan.C;
-  r.t_end = (cta + 1) * q + (cta + 1) * m / p.plan.C;
-  r.u = r.t / p.plan.T;
-  r.h = r.u / p.plan.G;
-  r.gi = r.u - r.h * p.plan.G;
-  return r;
-}
-__device__ __forceinline__ bool next_seg8(const Doc8Params& p, Runs8& r, Seg8& s) {
-  while (r.t < r.t_end) {
-    s.u = r.u;
-    s.h = r.h;
-    s.gi = r.gi;
-    s.two = p.rows - s.gi * kGroupRows > 128;
-    const int v = r.t - r.u * p.plan.T;              // step of the unit
-    const int n = min(p.plan.T - v, r.t_end - r.t);
-    r.t += n;
-    if (v + n == p.plan.T) {
-      ++r.u;
-      if (++r.gi == p.plan.G) {
-        r.gi = 0;
-        ++r.h;
-      }
-    }
-    s.j0 = max(0, v - kKv8Lead);
-    s.n = v + n - kKv8Lead - s.j0;
-    if (s.n > 0) return true;
-  }
-  return false;
-}
 
 // One arrival for a warp whose lanes have all done what the barrier stands for.
 __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
@@ -235,7 +190,7 @@ __global__ void __maxnreg__(kRegs8) kv8_doc_tc(const Doc8Params p) {
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cta = blockIdx.x;
-  const Runs8 runs = first_run8(p, cta);
+  const Runs8 runs = first_run8(p.plan, cta);
   int32_t* status = p.L.status;
 
   if (threadIdx.x == 0) {
@@ -292,7 +247,7 @@ __global__ void __maxnreg__(kRegs8) kv8_doc_tc(const Doc8Params p) {
         vs = p.L.v_scale[(int64_t)pg * p.L.H + h];
       }
     };
-    while (ok && next_seg8(p, t, s)) {
+    while (ok && next_seg8(p.plan, p.rows, t, s)) {
       int b = s.j0 / per;
       int pg0 = page_of(entry(b), p.L.n_pages), e1 = entry(b + 1);
       float ks0, vs0, ks1, vs1;
@@ -394,15 +349,17 @@ __global__ void __maxnreg__(kRegs8) kv8_doc_tc(const Doc8Params p) {
     };
     Runs8 t = runs;
     Seg8 s;
-    int t0 = 0, nseg = 0;
-    uint32_t pf_ph = 0;
+    int t0 = 0;
+    uint32_t q_ph = 0, pf_ph = 0;   // bit st: the stream's parity
     bool ok = true;
-    while (ok && next_seg8(p, t, s)) {
+    while (ok && next_seg8(p.plan, p.rows, t, s)) {
       const int step = s.two ? 1 : 2;
       for (int st = 0; ok && st < 2; ++st) {
-        if (!(ok = warp_wait(q_full + st, nseg & 1, abort_flag, p.wait_limit, status))) break;
-        const int tile = s.two ? 0 : st;
-        if (tile >= s.n) continue;
+        if (!has_tile8(s, st)) continue;
+        if (!(ok = warp_wait(q_full + st, (q_ph >> st) & 1, abort_flag, p.wait_limit, status)))
+          break;
+        q_ph ^= 1u << st;
+        const int tile = first_tile8(s, st);
         const int half = 2 * (t0 + tile);
         if (!(ok = wait_f(half))) break;
         tc_fence_after();
@@ -434,7 +391,6 @@ __global__ void __maxnreg__(kRegs8) kv8_doc_tc(const Doc8Params p) {
         }
       }
       t0 += s.n;
-      ++nseg;
     }
     if (!ok) {
       commit(drain);
@@ -465,7 +421,7 @@ __global__ void __maxnreg__(kRegs8) kv8_doc_tc(const Doc8Params p) {
     Seg8 s;
     int kt = 0;
     bool ok = true;
-    while (ok && next_seg8(p, t, s)) {
+    while (ok && next_seg8(p.plan, p.rows, t, s)) {
       for (int j = 0; ok && j < s.n; ++j, ++kt) {
         for (int x = 0; x < (C::APART ? 1 : 2); ++x) {
           const int kv = C::APART ? kind : x;
@@ -521,13 +477,17 @@ __global__ void __maxnreg__(kRegs8) kv8_doc_tc(const Doc8Params p) {
     uint32_t s_ph = 0, od_ph = 0;
     int t0 = 0;
     bool ok = true;
-    while (ok && next_seg8(p, t, s)) {
-      const int step = s.two ? 1 : 2, first = s.two ? 0 : st;
+    while (ok && next_seg8(p.plan, p.rows, t, s)) {
+      const int step = s.two ? 1 : 2, first = first_tile8(s, st);
+      const bool tiles = has_tile8(s, st);
       const int row = s.gi * kGroupRows + (s.two ? st * 128 : 0) + rt;
       // (the previous run's last S has been seen: no MMA reads this tile of Q any more)
-      const float qs = load_queries<D>(p, tq, wq * 32, row - lane, s.h, lane) * p.sl2;
-      fence_proxy_async();
-      warp_arrive(q_full + st, lane);
+      float qs = 0.f;
+      if (tiles) {
+        qs = load_queries<D>(p, tq, wq * 32, row - lane, s.h, lane) * p.sl2;
+        fence_proxy_async();
+        warp_arrive(q_full + st, lane);
+      }
       float m = 0.f, l = 0.f;
       bool none = true;                        // no key so far
       for (int tile = first; tile < s.n; tile += step) {
@@ -660,7 +620,7 @@ __global__ void __maxnreg__(kRegs8) kv8_doc_tc(const Doc8Params p) {
       const int chunk =
           s.j0 == 0 ? 0 : cta - plan_cta_of(p.plan, (int64_t)s.u * p.plan.T + kKv8Lead);
       const int64_t prow = ((int64_t)s.u * p.plan.max_chunks + chunk) * kGroupRows + st * 128 + rt;
-      if (first < s.n) {
+      if (tiles) {
         if (!(ok = warp_wait(o_done + st, od_ph, abort_flag, p.wait_limit, status))) break;
         od_ph ^= 1;
         tc_fence_after();
@@ -739,7 +699,6 @@ cudaError_t launch_kv8_doc(const pp_kv8_layer& L, const pp_kv8_attn_args& a, con
   p.rows = a.rows * p.g;
   p.doc_len = a.doc_len;
   p.plan = plan;
-  p.steps = (int)plan.W;
   p.sl2 = a.scale * kLog2e;
   p.doc_o = part.doc_o; p.doc_ml = part.doc_ml;
   p.wait_limit = wait_limit;

@@ -134,6 +134,8 @@ _kv8_dec_ws = _sig("pp_kv8_decode_workspace_bytes", _sz, _i32, _i32, _i32, _i32,
 _kv8_pre_ws = _sig("pp_kv8_prefill_workspace_bytes", _sz, _i32, _i32, _i32, _i32, _i32, _OP)
 _kv8_decode = _sig("pp_kv8_decode_attn", _i32, _LP8, ctypes.c_char_p, _vp)
 _kv8_prefill = _sig("pp_kv8_prefill_attn", _i32, _LP8, ctypes.c_char_p, _vp)
+_kv8_runs = _sig("pp_debug_kv8_runs", _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32,
+                 ctypes.POINTER(ctypes.c_int64), _i32)
 _kv8_status = _sig("pp_kv8_get_device_status", _i32, _LP8, ctypes.POINTER(_i32), _vp)
 
 EXPORTED = ("pp_status_str", "pp_abi_version", "pp_kv_reset", "pp_kv_append",
@@ -143,7 +145,8 @@ EXPORTED = ("pp_status_str", "pp_abi_version", "pp_kv_reset", "pp_kv_append",
             "pp_doc_prefill_workspace_bytes", "pp_doc_prefill_attn", "pp_debug_split_plan_causal",
             "pp_kv_reset_streams", "pp_decode_step", "pp_kv8_reset", "pp_kv8_append",
             "pp_kv8_decode_workspace_bytes", "pp_kv8_prefill_workspace_bytes",
-            "pp_kv8_decode_attn", "pp_kv8_prefill_attn", "pp_kv8_get_device_status")
+            "pp_kv8_decode_attn", "pp_kv8_prefill_attn", "pp_kv8_get_device_status",
+            "pp_debug_kv8_runs")
 
 # Size of the scratch array built into the library for pp_decode_attn_noalloc.
 NOALLOC_SCRATCH_BYTES = 32 << 20
@@ -694,6 +697,23 @@ def kv8_device_status(layer: KV8Layer) -> int:
         if e.status != PP_ERR_DEVICE_TIMEOUT:
             raise
     return int(out.value)
+
+
+def kv8_runs(rows: int, Hq: int, H: int, doc_len: int, decode: bool = True, splits: int = 0,
+             num_sms: int = 148):
+    """The 8-bit document pass's plan: dict with T, units, W, C, max_chunks and
+    runs, a list of (CTA, unit, first tile, tiles, two M tiles, bits of the
+    streams that have a tile).  Host only."""
+    n = 6 + 6 * 4096
+    while True:
+        buf = (ctypes.c_int64 * n)()
+        rc = _kv8_runs(rows, Hq, H, doc_len, int(decode), splits, num_sms, buf, n)
+        if rc != PP_ERR_CAPACITY or n > 1 << 26:
+            break
+        n *= 4
+    _check(rc, "pp_debug_kv8_runs")
+    runs = [tuple(buf[6 + 6 * i:12 + 6 * i]) for i in range(buf[5])]
+    return dict(zip(("T", "units", "W", "C", "max_chunks"), buf[:5]), runs=runs)
 
 
 def split_plan(rows: int, H: int, doc_len: int, ctas: int, causal: bool = False):
