@@ -409,14 +409,16 @@ typedef struct pp_kv8_append_args {
 /*
  * Append n rows: rotate the keys, quantise keys and values, one launch.
  * In one call the rows of a stream stand next to each other at consecutive
- * positions; the first run of a stream counts, and a row that breaks this is
- * dropped and sets PP_DEV_ROW_ORDER.  Per page and head, with A the largest
- * magnitude of the call's rows in the page, need = 2^ceil(log2(A / 448))
- * within [2^-40, 2^40]: the page's scale becomes need when the rows begin at
- * its slot 0, else max(old scale, need), and if that grew, the page's slots
- * before the rows are rounded again.  Rounding is to nearest even.  A NaN
- * among a row's values makes every query that sees the row NaN in that head;
- * infinities count as the largest value; both set PP_DEV_NONFINITE.
+ * positions.  Of a call that breaks this the rows next to the stream's first one
+ * count that stand at the position their distance from it asks for, up to the
+ * first in their page that does not; the rest are dropped and set
+ * PP_DEV_ROW_ORDER (of 4 5 9 7 8 in one page the first two are kept).
+ * Per page and head, with A the largest magnitude of the call's rows in the page,
+ * need = 2^ceil(log2(A / 448)) within [2^-40, 2^40]: the page's scale becomes need
+ * when the rows begin at its slot 0, else max(old scale, need), and if that grew,
+ * the page's slots before the rows are rounded again.  Rounding is to nearest
+ * even.  A NaN among a row's values makes every query that sees the row NaN in
+ * that head; infinities count as the largest value; both set PP_DEV_NONFINITE.
  * Dropped rows: a slot past the table (PP_DEV_DOC_OUT_OF_RANGE,
  * PP_DEV_SEGMENT_OVERFLOW), no page (PP_DEV_BAD_PAGE), position < pos0 or past
  * the angles (PP_DEV_BAD_POSITION), sid > P_max (PP_DEV_BAD_STREAM).  Rows of

@@ -79,8 +79,11 @@ class Kv8Replay:
                 continue
             if i == 0 or sid[i - 1] != s:
                 start = runs_seen.setdefault(s, i)      # first run of the stream
-                run = i
-            ok = start == run and p - int(pos[run]) == i - run
+                run, whole = i, True
+            fits = p - int(pos[run]) == i - run
+            afresh = (p if s == 0 else p - self.pos0) % self.page == 0
+            whole = fits and (whole or afresh)          # no break in this page so far
+            ok = start == run and whole
             at = self.place(s, p) if ok else None
             if at is None or (cos_sin is not None and p >= len(cos_sin)):
                 dropped.append(i)

@@ -13,8 +13,9 @@
 // stream stand next to each other at consecutive positions (a question's or a
 // document's rows do): the rows of a page are then a run, its first row -- the
 // leader -- is found from its neighbour alone, and the leader's warps own the
-// page's heads without any ordering between CTAs.  A run that breaks the rule
-// is found by the leader's scan of the earlier stream ids and dropped.
+// page's heads without any ordering between CTAs.  A row that breaks the run is a
+// leader too; its scan of the earlier stream ids finds it out, and it is dropped
+// with the rest of its page.
 //
 // Bound: HBM (bf16 in, e4m3 out); a decode step's few kilobytes a row are
 // latency.
@@ -474,13 +475,19 @@ __device__ __forceinline__ Lead open_lead(const AppendParams& p, int i, int s, i
 }
 
 // The rows to write (none: 0) of a leader whose stream has cnt rows before it, the
-// last row of another being `last`: the stream's run must be its only one and its
-// positions consecutive.
+// last row of another being `last`: the stream's rows must all stand next to each
+// other, the leader at the position that its distance from their first asks for, and
+// in the middle of a page only that first one leads.  So a page has one leader: a
+// row's position names its place in the run, and a page that the run enters at slot
+// 0 is entered by one row only.  (Positions between are not read: every leader would
+// read all before it, 173 us instead of 165 for a document of 16384 tokens, 32 heads,
+// 180 instead of 120 for 60000 tokens, 4 heads.)
 __device__ __forceinline__ int rows_of(const AppendParams& p, const Lead& x, int cnt, int last,
                                        bool tell) {
   const int a = last + 1;               // first row of the run
   int err = 0, nr = x.nr;
-  if (cnt != x.i - a || (int64_t)x.ps - p.pos[a] != x.i - a) err = PP_DEV_ROW_ORDER;
+  if (cnt != x.i - a || (int64_t)x.ps - p.pos[a] != x.i - a || (x.off > 0 && x.i > a))
+    err = PP_DEV_ROW_ORDER;
   else if (!x.fits) err = x.s == 0 ? PP_DEV_DOC_OUT_OF_RANGE : PP_DEV_SEGMENT_OVERFLOW;
   else if (x.pg < 0) err = PP_DEV_BAD_PAGE;
   if (err) {
