@@ -446,9 +446,9 @@ size_t pp_kv8_prefill_workspace_bytes(int32_t R, int32_t Hq, int32_t H, int32_t 
  *          when q_pos < pos0)
  *   o      bf16 [rows][Hq][d];  lse  fp32 [rows][Hq] or NULL
  *   ws     workspace of ws_bytes, 256-byte aligned
- *   opt    NULL, or: splits (the document pass's CTAs; given, the pass is taken
- *          however small the work), debug_inject_timeout, wait_limit_log2 and
- *          events apply; the comparison modes and suffix_slices are refused
+ *   opt    NULL, or: splits (the document pass's CTAs, 46340 at most; given, the
+ *          pass is taken however small the work), debug_inject_timeout,
+ *          wait_limit_log2 and events apply; the comparison modes and suffix_slices are refused
  *   scale  softmax scale, finite and > 0
  */
 typedef struct pp_kv8_attn_args {

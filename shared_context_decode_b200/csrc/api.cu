@@ -339,7 +339,8 @@ SplitPlan kv8_plan(int32_t rows, int32_t Hq, int32_t H, int32_t doc_len, const p
     while (parts * parts < 2 * p.T) ++parts;
     ctas = (int)std::min<int64_t>(ctas, (int64_t)parts * p.units);
   }
-  p.C = (int32_t)std::min<int64_t>(std::max(ctas, 0), p.W);
+  // (46340^2 < 2^31: the kernel's products of two CTA counts hold in 32 bits)
+  p.C = (int32_t)std::min<int64_t>(std::min(std::max(ctas, 0), 46340), p.W);
   if (p.C < 1) return SplitPlan{};
   // a unit's steps lie in at most this many CTAs' ranges of floor(W / C) or one more
   const int64_t least = p.W / p.C;

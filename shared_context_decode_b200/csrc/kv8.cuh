@@ -75,8 +75,9 @@ __device__ __forceinline__ int page_of(int32_t entry, int n_pages) {
 constexpr int kKv8Lead = 4;
 
 // A run of tiles of one unit, (key head, row group), in a CTA of the document pass.
-// Steps are counted in 32 bits (the host sees to it), and only a CTA's first run
-// divides: 64-bit divisions at every role's start took 3600 cycles.
+// Steps are counted in 32 bits (the host keeps W, and C times a remainder by C, below
+// 2^31), and only a CTA's first run divides: 64-bit divisions at every role's start
+// took 3600 cycles.
 struct Seg8 {
   int u, h, gi, j0, n;
   bool two;     // two M tiles; else one, its tiles dealt out to the streams

@@ -247,6 +247,22 @@ def test_the_runs_cover_every_tile_once(pp):
             assert at == tiles
 
 
+@pytest.mark.parametrize("splits", [46340, 46341, 60000, 100351, 2 ** 31 - 1])
+def test_more_splits_than_32_bit_products_hold(pp, splits):
+    """256 questions of 32 rows, 32 heads, behind 12000 tokens: 100352 steps."""
+    p = pp.kv8_runs(8192, 32, 32, 12000, decode=False, splits=splits)
+    assert 0 < p["C"] and p["C"] * (p["W"] % p["C"]) < 2 ** 31
+    at = {}
+    for cta, u, j0, n, _, _ in p["runs"]:
+        assert 0 <= u < p["units"] and 0 <= cta < p["C"] and j0 == at.get(u, 0)
+        at[u] = j0 + n
+    assert at == dict.fromkeys(range(p["units"]), -(-12000 // 128))
+    # the workspace is that of the same plan
+    slots = p["units"] * p["max_chunks"] * 256
+    size = pp.kv8_prefill_workspace_bytes(8192, 32, 32, 128, 12000, pp.Options(splits=splits))
+    assert 0 <= size - slots * (128 + 2) * 4 < 1024
+
+
 def test_a_stream_takes_part_in_a_run_only_with_a_tile(pp):
     """Every head count to 64, documents to 8192 tokens."""
     lone = 0
