@@ -322,11 +322,13 @@ __device__ __forceinline__ DocRow doc_row(const Attn8Params& p, int row, int kvh
 }
 
 // A lane's share of row n = 2c + a of tile t of a partial: dims (D/8) r ..
+// (Partials are read by plain loads: the document pass may still write them while
+// this kernel runs, and only a plain load stays behind griddepcontrol.wait.)
 template <int D>
 __device__ __forceinline__ void load_part(float (&x)[D / 8], const float* row, int r) {
 #pragma unroll
   for (int i = 0; i < D / 8; i += 4) {
-    const float4 v = __ldg(reinterpret_cast<const float4*>(row + r * (D / 8) + i));
+    const float4 v = *reinterpret_cast<const float4*>(row + r * (D / 8) + i);
     x[i] = v.x; x[i + 1] = v.y; x[i + 2] = v.z; x[i + 3] = v.w;
   }
 }
@@ -406,7 +408,7 @@ __global__ void __launch_bounds__(WARPS * 32, (NT == 1 ? 16 : 12) / WARPS)
           dr2[t][a].two = __shfl_sync(0xffffffffu, d.two, n2);
           ml[t][a] = make_float2(-INFINITY, 0.f);
           if (dr2[t][a].n == 0) continue;
-          ml[t][a] = __ldg(reinterpret_cast<const float2*>(p.doc_ml) + dr2[t][a].slot);
+          ml[t][a] = reinterpret_cast<const float2*>(p.doc_ml)[dr2[t][a].slot];
           float x[D / 8];
           load_part<D>(x, p.doc_o + dr2[t][a].slot * D, r);
 #pragma unroll
@@ -532,7 +534,7 @@ __global__ void __launch_bounds__(WARPS * 32, (NT == 1 ? 16 : 12) / WARPS)
           if (n2 >= n_pairs) continue;
           for (int k = 1; p.has_doc && k < dr2[t][a].n; ++k) {
             const int64_t sl = dr2[t][a].at(k);
-            const float2 ml = __ldg(reinterpret_cast<const float2*>(p.doc_ml) + sl);
+            const float2 ml = reinterpret_cast<const float2*>(p.doc_ml)[sl];
             if (ml.x == -INFINITY) continue;
             float x[D / 8];
             load_part<D>(x, p.doc_o + sl * D, r);
@@ -609,13 +611,13 @@ __global__ void __launch_bounds__(WARPS * 32, (NT == 1 ? 16 : 12) / WARPS)
   };
   using Vec = typename std::conditional<E == 4, float4, float2>::type;
   auto doc_vec = [&](int64_t slot) {
-    return __ldg(reinterpret_cast<const Vec*>(p.doc_o + slot * D) + lane);
+    return reinterpret_cast<const Vec*>(p.doc_o + slot * D)[lane];
   };
   auto lane_ml = [&](const DocRow& d, int n, int j) {    // (m, l) of the row's partial j
     if (j < p.ways)
       return *reinterpret_cast<const float2*>(it + j * M::WARP + n * 8);
     if (j - p.ways < d.n)
-      return __ldg(reinterpret_cast<const float2*>(p.doc_ml) + d.at(j - p.ways));
+      return reinterpret_cast<const float2*>(p.doc_ml)[d.at(j - p.ways)];
     return make_float2(-INFINITY, 0.f);
   };
   // the next row's maxima and first document row are on their way while one is joined
