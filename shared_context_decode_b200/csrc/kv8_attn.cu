@@ -42,12 +42,12 @@ struct Attn8Params {
   const uint16_t* q;
   int64_t q_ld;
   int Hq, g, hg, gt, rt;   // query heads, per key head, per item, items per key head's group, rows per item
-  int rows, n_items;
+  int rows, n_items, row_groups;
   const int16_t* q_sid;
   const int32_t* q_pos;
   int doc_len;             // document keys read here (0: none, or left to the document pass)
   float sl2;               // scale * log2e
-  int ways;                // warps per item
+  int ways, base;          // warps per item, and of an item of few chunks
   int lper;                // log2 of the 16-key chunks per page
   int has_doc;             // document partials to merge
   int plan32;              // the plan's divisions fit 32 bits
@@ -282,6 +282,8 @@ __device__ __forceinline__ void part_of(int n, int w, int ways, int& c0, int& c1
 }
 
 constexpr int kMaxWays = 16;   // warps of a CTA, and of an item, at most
+// An item of more chunks than this is cut where it would be one warp's.
+constexpr int kShareChunks = 16;
 
 // A warp's shared memory: its ring, and over it, when the keys are done, its
 // partial result: (m, l) of its rows, then O, rows of D + 4 floats.
@@ -343,17 +345,50 @@ __global__ void __launch_bounds__(WARPS * 32, (NT == 1 ? 16 : 12) / WARPS)
   extern __shared__ __align__(128) uint8_t sm[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r = lane >> 2, c = lane & 3;
-  const int lways = 31 - __clz(p.ways);              // a power of two
-  const int item = (int)blockIdx.x * (WARPS >> lways) + (warp >> lways);
-  const int way = warp & (p.ways - 1);
-  const bool live = item < p.n_items;
+  // ---- the warp's item: place x among those of rows rt * rg ..
+  const int xs = p.L.H * p.gt;
+  int ways = WARPS, rg, x;
+  bool live = true;
+  if (WARPS == 1 || p.base == WARPS) {
+    rg = (int)blockIdx.x / xs;
+    x = (int)blockIdx.x - rg * xs;
+  } else {
+    // The table has room for long segments and this row's may be short, which the
+    // host does not know: then the first of a few blocks of the row takes their
+    // items, `base` warps each, and the others, which stand behind all first ones,
+    // end.  (Tables with room for 1024 further tokens, 256 streams of 17 to 112
+    // tokens, 32 heads: 124 us behind 16384, 64 streams behind 8192 49; all items cut
+    // as the table allows 195 and 70; tables without room, blocks of one warp, 116 and
+    // 47.  Answers of 1024 tokens pay 2 to 3 % for the question: 253 and 246.)
+    const int per = WARPS / p.base, groups = (xs + per - 1) / per;
+    const int leaders = p.row_groups * groups;
+    const bool leads = (int)blockIdx.x < leaders;
+    if (leads) {
+      rg = (int)blockIdx.x / groups;
+      x = ((int)blockIdx.x - rg * groups) * per;
+    } else {
+      const int b = (int)blockIdx.x - leaders, f = xs - groups;
+      rg = b / f;
+      x = (b - rg * f) / (per - 1) * per + 1 + (b - rg * f) % (per - 1);
+    }
+    const int slot = p.q_pos[rg] - p.L.pos0;
+    const bool some = p.q_pos[rg] >= p.L.pos0 && stream_query(p.q_sid[rg], p.L.P_max);
+    const int chunks = (some ? min(slot >> 4, p.L.seg_pages * p.L.page / 16 - 1) + 1 : 0) +
+                       ((p.doc_len + 15) >> 4);
+    if (chunks <= kShareChunks * p.base) {
+      if (!leads) return;
+      ways = p.base;
+      x += warp / ways;
+      live = x < xs;
+    }
+  }
+  const int way = warp & (ways - 1);
   uint8_t* ring = sm + warp * M::WARP;
   float* my_ml = reinterpret_cast<float*>(ring);
   float* my_o = my_ml + 2 * M::ROWS;
   int r0 = 0, kvh = 0, hb = 0, nh = 1, nrow = 0;
   if (live) {
-    const int x = item % (p.L.H * p.gt);
-    r0 = item / (p.L.H * p.gt) * p.rt;
+    r0 = rg * p.rt;
     kvh = x / p.gt;
     hb = (x % p.gt) * p.hg;               // first query head inside the group
     nh = min(p.hg, p.g - hb);
@@ -391,7 +426,7 @@ __global__ void __launch_bounds__(WARPS * 32, (NT == 1 ? 16 : 12) / WARPS)
         for (int j = 0; j < D / 16; ++j) st.o[t][j][a] = st.o[t][j][2 + a] = 0.f;
       }
     DocRow dr2[NT][2];
-    if (NT > 1 && p.has_doc && p.ways == 1) {
+    if (NT > 1 && p.has_doc && ways == 1) {
       asm volatile("griddepcontrol.wait;" ::: "memory");
       DocRow d{0, 0, 0};                   // of pair `lane`
       const int sid_p = __shfl_sync(0xffffffffu, sid_l, lane < n_pairs ? lane / nh : 0);
@@ -475,7 +510,7 @@ __global__ void __launch_bounds__(WARPS * 32, (NT == 1 ? 16 : 12) / WARPS)
 #pragma unroll
         for (int a = 0; a < 2; ++a) dl[t][a] = sidr[t][a] ? p.doc_len - 1 : -1;
       int c0, c1;
-      part_of((p.doc_len + 15) >> 4, way, p.ways, c0, c1);
+      part_of((p.doc_len + 15) >> 4, way, ways, c0, c1);
       // rows that are no queries see nothing; t_min by the document's end
       // alone would miss them, so every chunk is masked when there are any
       bool all = true;
@@ -515,13 +550,13 @@ __global__ void __launch_bounds__(WARPS * 32, (NT == 1 ? 16 : 12) / WARPS)
           lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o2));
         }
         int c0, c1;
-        part_of((hi + 16) >> 4, way, p.ways, c0, c1);
+        part_of((hi + 16) >> 4, way, ways, c0, c1);
         scan<D, NT>(st, qf, p, p.L.seg_table + (int64_t)(s - 1) * p.L.seg_pages, kvh, c0, c1, lm,
                     hi, lo, qs, ring, lane);
       }
       ra = rb;
     }
-    if (NT > 1 && p.ways == 1) {
+    if (NT > 1 && ways == 1) {
       // ---- the further document partials, and out
 #pragma unroll
       for (int t = 0; t < NT; ++t)
@@ -585,7 +620,7 @@ __global__ void __launch_bounds__(WARPS * 32, (NT == 1 ? 16 : 12) / WARPS)
               st.o[t][j][a], st.o[t][j][2 + a], st.o[t][j + 1][a], st.o[t][j + 1][2 + a]);
       }
   }
-  if (p.ways > 1) __syncthreads(); else __syncwarp();
+  if (ways > 1) __syncthreads(); else __syncwarp();
   if (!live) return;
   // (the segments did not need the document pass; its partials do)
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -614,10 +649,10 @@ __global__ void __launch_bounds__(WARPS * 32, (NT == 1 ? 16 : 12) / WARPS)
     return reinterpret_cast<const Vec*>(p.doc_o + slot * D)[lane];
   };
   auto lane_ml = [&](const DocRow& d, int n, int j) {    // (m, l) of the row's partial j
-    if (j < p.ways)
+    if (j < ways)
       return *reinterpret_cast<const float2*>(it + j * M::WARP + n * 8);
-    if (j - p.ways < d.n)
-      return reinterpret_cast<const float2*>(p.doc_ml)[d.at(j - p.ways)];
+    if (j - ways < d.n)
+      return reinterpret_cast<const float2*>(p.doc_ml)[d.at(j - ways)];
     return make_float2(-INFINITY, 0.f);
   };
   // the next row's maxima and first document row are on their way while one is joined
@@ -629,12 +664,12 @@ __global__ void __launch_bounds__(WARPS * 32, (NT == 1 ? 16 : 12) / WARPS)
     nml = lane_ml(nd, way, lane);
     if (nd.n) nv = doc_vec(nd.slot);
   }
-  for (int n = way; n < n_all; n += p.ways) {
+  for (int n = way; n < n_all; n += ways) {
     const int row = r0 + n / nh, head = kvh * p.g + hb + n % nh;
     const DocRow d = nd;
     const float2 ml0 = nml;
     const Vec v0 = nv;
-    const int n2 = n + p.ways;
+    const int n2 = n + ways;
     nd = row_of(n2 < n_all ? n2 : 0);
     if (n2 < n_all) {
       nml = lane_ml(nd, n2, lane);
@@ -644,7 +679,7 @@ __global__ void __launch_bounds__(WARPS * 32, (NT == 1 ? 16 : 12) / WARPS)
     float m = -INFINITY, l = 0.f, acc[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
-    const int cnt = query ? p.ways + d.n : 0;
+    const int cnt = query ? ways + d.n : 0;
     for (int b = 0; b < cnt; b += 32) {
       const float2 ml = b == 0 ? ml0 : lane_ml(d, n, b + lane);
       float mm = ml.x;
@@ -669,10 +704,10 @@ __global__ void __launch_bounds__(WARPS * 32, (NT == 1 ? 16 : 12) / WARPS)
         const float yj = __shfl_sync(0xffffffffu, y, j);
         if (!(saw >> j & 1)) continue;
         Vec v;
-        if (b + j < p.ways)
+        if (b + j < ways)
           v = reinterpret_cast<const Vec*>(it + j * M::WARP + M::ROWS * 8 + n * LD * 4)[lane];
         else
-          v = b + j == p.ways ? v0 : doc_vec(d.at(b + j - p.ways));
+          v = b + j == ways ? v0 : doc_vec(d.at(b + j - ways));
         const float* f = reinterpret_cast<const float*>(&v);
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] = fmaf(f[e], yj, acc[e]);
@@ -705,12 +740,10 @@ cudaError_t launch_as(const Attn8Params& p, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit);
   }
-  const int per = WARPS / p.ways;
-  const int64_t grid = ((int64_t)p.n_items + per - 1) / per;
   // Behind a document pass the blocks may start as its CTAs end: they read
   // the segments meanwhile and wait for it only where its partials are joined.
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)grid);
+  cfg.gridDim = dim3((unsigned)p.n_items);
   cfg.blockDim = dim3(WARPS * 32);
   cfg.dynamicSmemBytes = SMEM;
   cfg.stream = st;
@@ -759,15 +792,27 @@ cudaError_t launch_kv8_attn(const pp_kv8_layer& L, const pp_kv8_attn_args& a,
   p.doc_o = part.doc_o; p.doc_ml = part.doc_ml;
   p.o = a.o; p.lse = a.lse;
   // Warps per item: enough to fill the GPU when items are few (they share the
-  // item's merge too, however short its keys), and a long segment cut so that
-  // one item is not a CTA's whole tail.
-  const int64_t chunks = (int64_t)L.seg_pages * L.page / 16 + (p.doc_len + 15) / 16;
-  int ways = 1;
-  while (ways < 8 && (items * ways < 12LL * num_sms || (ways < 4 && chunks / ways > 16)))
-    ways *= 2;
+  // item's merge too, however short its keys), and a long document cut so that
+  // one item is not a CTA's whole tail.  A decode row's long segment is cut too, by
+  // the kernel, since only the row's position tells its length; question rows are
+  // not: a question's items are many (256 questions of 16..48 rows in tables for 1024
+  // further tokens 1486 us, cut by the table's length 1931; 8 of 1000 rows 1847 and 2223).
+  const int64_t seg_chunks = (int64_t)L.seg_pages * L.page / 16, doc_chunks = (p.doc_len + 15) / 16;
+  int base = 1;
+  while (base < 8 &&
+         (items * base < 12LL * num_sms || (base < 4 && doc_chunks / base > kShareChunks)))
+    base *= 2;
+  int ways = base;
+  if (one_row_per_stream)
+    while (ways < 4 && 2 * ways <= base * (int64_t)L.H * it.gt &&
+           (seg_chunks + doc_chunks) / ways > kShareChunks)
+      ways *= 2;
   // (a block an SM, and a document long enough to share)
-  if (ways == 8 && it.most == 8 && items <= 3 * num_sms / 2 && chunks > 40) ways = kMaxWays;
+  if (base == 8 && it.most == 8 && items <= 3 * num_sms / 2 && seg_chunks + doc_chunks > 40)
+    ways = base = kMaxWays;
   p.ways = ways;
+  p.base = base;
+  p.row_groups = (rows + it.rt - 1) / it.rt;
   p.lper = L.page == 16 ? 0 : L.page == 32 ? 1 : L.page == 64 ? 2 : 3;
   if (L.d == 128) return it.most == 8 ? launch<128, 1>(p, st) : launch<128, 2>(p, st);
   return it.most == 8 ? launch<64, 1>(p, st) : launch<64, 2>(p, st);
