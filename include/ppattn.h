@@ -521,7 +521,8 @@ pp_status pp_debug_split_plan_causal(int32_t doc_len, int32_t H, int32_t ctas, i
  * Test aid (host only): the runs of document tiles that the 8-bit cache's document
  * pass gives its CTAs, with `splits` as in pp_options (0: the calls' own choice, on a
  * device of num_sms SMs).  h_out[0..4] = T (steps per unit), units, W, C (0: no
- * pass), max_chunks; h_out[5] = number of runs; then per run six entries: CTA,
+ * pass), max_chunks; h_out[5..6] = (row, query head) pairs of a segment item at
+ * most, number of items; h_out[7] = number of runs; then per run six entries: CTA,
  * unit, first tile, tiles, whether the unit has two M tiles, and a bit for each of
  * the CTA's two streams that has a tile in the run.
  */

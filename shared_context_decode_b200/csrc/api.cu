@@ -436,22 +436,23 @@ size_t kv8_workspace(int32_t rows, int32_t Hq, int32_t H, int32_t d, int32_t doc
 }
 
 // The document pass's runs of every CTA, as the kernel's roles walk them.
-pp_status write_kv8_runs(const SplitPlan& p, int rows, int64_t* h_out, int32_t h_out_len) {
-  if (h_out_len < 6) return PP_ERR_CAPACITY;
-  const int64_t head[5] = {p.T, p.units, p.W, p.C, p.max_chunks};
-  for (int i = 0; i < 5; ++i) h_out[i] = head[i];
+pp_status write_kv8_runs(const SplitPlan& p, int rows, const pp::Kv8Items& items, int64_t* h_out,
+                         int32_t h_out_len) {
+  if (h_out_len < 8) return PP_ERR_CAPACITY;
+  const int64_t head[8] = {p.T, p.units, p.W, p.C, p.max_chunks, items.most, items.items, 0};
+  for (int i = 0; i < 8; ++i) h_out[i] = head[i];
   int64_t runs = 0;
   for (int cta = 0; cta < p.C; ++cta) {
     pp::Runs8 r = pp::first_run8(p, cta);
     pp::Seg8 s;
     for (; pp::next_seg8(p, rows, r, s); ++runs) {
-      if (6 + 6 * (runs + 1) > h_out_len) return PP_ERR_CAPACITY;
+      if (8 + 6 * (runs + 1) > h_out_len) return PP_ERR_CAPACITY;
       const int64_t run[6] = {cta, s.u, s.j0, s.n, s.two,
                               (int)pp::has_tile8(s, 0) + 2 * (int)pp::has_tile8(s, 1)};
-      for (int i = 0; i < 6; ++i) h_out[6 + 6 * runs + i] = run[i];
+      for (int i = 0; i < 6; ++i) h_out[8 + 6 * runs + i] = run[i];
     }
   }
-  h_out[5] = runs;
+  h_out[7] = runs;
   return PP_OK;
 }
 
@@ -662,7 +663,8 @@ PP_API pp_status pp_debug_kv8_runs(int32_t rows, int32_t Hq, int32_t H, int32_t 
   opt.splits = splits;
   const SplitPlan p = kv8_plan(rows, Hq, H, doc_len, &opt, decode != 0, num_sms);
   if (p.W > INT32_MAX) return PP_ERR_UNSUPPORTED;
-  return write_kv8_runs(p, rows * (Hq / H), h_out, h_out_len);
+  return write_kv8_runs(p, rows * (Hq / H), pp::kv8_items(rows, Hq / H, H, decode != 0), h_out,
+                        h_out_len);
 }
 
 PP_API pp_status pp_debug_exp2(const float* x, float* y_poly, float* y_hw, int32_t n,

@@ -701,10 +701,10 @@ def kv8_device_status(layer: KV8Layer) -> int:
 
 def kv8_runs(rows: int, Hq: int, H: int, doc_len: int, decode: bool = True, splits: int = 0,
              num_sms: int = 148):
-    """The 8-bit document pass's plan: dict with T, units, W, C, max_chunks and
-    runs, a list of (CTA, unit, first tile, tiles, two M tiles, bits of the
-    streams that have a tile).  Host only."""
-    n = 6 + 6 * 4096
+    """The 8-bit document pass's plan: dict with T, units, W, C, max_chunks, the
+    segment pass's pairs an item and items, and runs, a list of (CTA, unit, first
+    tile, tiles, two M tiles, bits of the streams that have a tile).  Host only."""
+    n = 8 + 6 * 4096
     while True:
         buf = (ctypes.c_int64 * n)()
         rc = _kv8_runs(rows, Hq, H, doc_len, int(decode), splits, num_sms, buf, n)
@@ -712,8 +712,8 @@ def kv8_runs(rows: int, Hq: int, H: int, doc_len: int, decode: bool = True, spli
             break
         n *= 4
     _check(rc, "pp_debug_kv8_runs")
-    runs = [tuple(buf[6 + 6 * i:12 + 6 * i]) for i in range(buf[5])]
-    return dict(zip(("T", "units", "W", "C", "max_chunks"), buf[:5]), runs=runs)
+    runs = [tuple(buf[8 + 6 * i:14 + 6 * i]) for i in range(buf[7])]
+    return dict(zip(("T", "units", "W", "C", "max_chunks", "pairs", "items"), buf[:7]), runs=runs)
 
 
 def split_plan(rows: int, H: int, doc_len: int, ctas: int, causal: bool = False):
