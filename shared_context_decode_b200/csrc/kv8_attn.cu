@@ -757,10 +757,11 @@ cudaError_t launch_as(const Attn8Params& p, cudaStream_t st) {
 
 template <int D, int NT>
 cudaError_t launch(const Attn8Params& p, cudaStream_t st) {
-  if constexpr (NT == 1)
+  if constexpr (NT == 1) {
     if (p.ways > 8) return launch_as<D, NT, 16>(p, st);
-  return p.ways > 4   ? launch_as<D, NT, 8>(p, st)
-         : p.ways > 2 ? launch_as<D, NT, 4>(p, st)
+    if (p.ways > 4) return launch_as<D, NT, 8>(p, st);
+  }
+  return p.ways > 2   ? launch_as<D, NT, 4>(p, st)
          : p.ways > 1 ? launch_as<D, NT, 2>(p, st)
                       : launch_as<D, NT, 1>(p, st);
 }
@@ -798,8 +799,9 @@ cudaError_t launch_kv8_attn(const pp_kv8_layer& L, const pp_kv8_attn_args& a,
   // not: a question's items are many (256 questions of 16..48 rows in tables for 1024
   // further tokens 1486 us, cut by the table's length 1931; 8 of 1000 rows 1847 and 2223).
   const int64_t seg_chunks = (int64_t)L.seg_pages * L.page / 16, doc_chunks = (p.doc_len + 15) / 16;
+  const int most = it.most == 8 ? 8 : 4;    // (items of 16 pairs are many)
   int base = 1;
-  while (base < 8 &&
+  while (base < most &&
          (items * base < 12LL * num_sms || (base < 4 && doc_chunks / base > kShareChunks)))
     base *= 2;
   int ways = base;
@@ -807,7 +809,9 @@ cudaError_t launch_kv8_attn(const pp_kv8_layer& L, const pp_kv8_attn_args& a,
     while (ways < 4 && 2 * ways <= base * (int64_t)L.H * it.gt &&
            (seg_chunks + doc_chunks) / ways > kShareChunks)
       ways *= 2;
-  // (a block an SM, and a document long enough to share)
+  // (a block an SM, and keys enough to share, if the table's room is used: 4 heads,
+  // segments of 1000 tokens 10.6 us so, by eight warps 10.8, of 8000 38 and 48; but
+  // of 12 tokens in a table for 1024 7.7 and 6.9)
   if (base == 8 && it.most == 8 && items <= 3 * num_sms / 2 && seg_chunks + doc_chunks > 40)
     ways = base = kMaxWays;
   p.ways = ways;

@@ -86,3 +86,29 @@ def test_question_rows_with_room_in_their_tables(H, g, d):
     assert m.kv8_device_status(layer) == 0 and torch.isfinite(o.float()).all()
     some = sorted(set([0, R - 1, R - 336] + [int(i) for i in rng.permutation(R)[:60]]))
     compare(layer, doc, segs, N, q, o, lse, sid, pos, d ** -0.5, some, "prefill")
+
+
+@pytest.mark.parametrize("N", [0, 300, 2000])
+@pytest.mark.parametrize("H,g,d,P", [(4, 1, 64, 5), (5, 2, 128, 30), (1, 8, 128, 40), (2, 4, 64, 90),
+                                     (3, 3, 128, 1)])
+def test_few_decode_rows_with_room_in_their_tables(H, g, d, P, N):
+    """Items few enough for sixteen warps each, of rows around the length from which
+    they get them (40 chunks of 16), far longer and far shorter."""
+    m = pp()
+    lens = [[639, 640, 641, 1, 2000, 656, 657, 37, 100, 2047][i % 10] for i in range(P)]
+    layer, doc, segs = make_cache(H, d, 16, N, lens, seed=P, seg_pages=128)
+    sid = list(range(P, 0, -1))
+    pos = [N + lens[x - 1] - 1 for x in sid]
+    if P > 3:
+        sid[2] = -1
+        pos[3] = N - 1
+    q = queries(P, H * g, d, 3)
+    s, p = ids(sid, pos)
+    lse = torch.zeros((P, H * g), device=DEV)
+    o = m.kv8_decode_attn(layer, N, q, s, p, d ** -0.5, lse=lse)
+    torch.cuda.synchronize()
+    assert m.kv8_device_status(layer) == 0
+    compare(layer, doc, segs, N, q, o, lse, sid, pos, d ** -0.5, list(range(P)), "decode")
+    # a few rows by themselves: the same within the bound, whatever shares a block
+    o2 = m.kv8_decode_attn(layer, N, q[:1], s[:1], p[:1], d ** -0.5, lse=lse[:1])
+    compare(layer, doc, segs, N, q, o2, lse, sid, pos, d ** -0.5, [0], "one row")
