@@ -337,7 +337,8 @@ pp_status pp_doc_prefill_attn(const pp_kv_layer *layer, int32_t doc_len, const u
  * for each page and head: half the bytes of pp_kv_layer's, pages instead of
  * fixed segments, and fewer key heads than query heads where the model groups
  * them.  The pages the method comes from serve a paged engine; they have no
- * counterpart of the 8-bit values.
+ * counterpart of the 8-bit values.  There is no causal attention of the
+ * document's own rows over this cache: pp_doc_prefill_attn reads a pp_kv_layer.
  *
  *   H          key/value heads;  d  64 or 128
  *   page       tokens of a page: 16, 32, 64 or 128
@@ -416,9 +417,12 @@ typedef struct pp_kv8_append_args {
  * Per page and head, with A the largest magnitude of the call's rows in the page,
  * need = 2^ceil(log2(A / 448)) within [2^-40, 2^40]: the page's scale becomes need
  * when the rows begin at its slot 0, else max(old scale, need), and if that grew,
- * the page's slots before the rows are rounded again.  Rounding is to nearest
- * even.  A NaN among a row's values makes every query that sees the row NaN in
- * that head; infinities count as the largest value; both set PP_DEV_NONFINITE.
+ * the page's slots before the rows are rounded again (what stood behind the rows
+ * in the page has to be appended again).  Rounding is to nearest even.  A NaN
+ * among a row's values, keys taken after the rotation, makes every query that sees
+ * the row NaN in that head; infinities count as the largest value (a rotated pair
+ * with one may come out NaN: infinity times a sine of zero); both set
+ * PP_DEV_NONFINITE.
  * Dropped rows: a slot past the table (PP_DEV_DOC_OUT_OF_RANGE,
  * PP_DEV_SEGMENT_OVERFLOW), no page (PP_DEV_BAD_PAGE), position < pos0 or past
  * the angles (PP_DEV_BAD_POSITION), sid > P_max (PP_DEV_BAD_STREAM).  Rows of
@@ -448,7 +452,8 @@ size_t pp_kv8_prefill_workspace_bytes(int32_t R, int32_t Hq, int32_t H, int32_t 
  *   ws     workspace of ws_bytes, 256-byte aligned
  *   opt    NULL, or: splits (the document pass's CTAs, 46340 at most; given, the
  *          pass is taken however small the work), debug_inject_timeout,
- *          wait_limit_log2 and events apply; the comparison modes and suffix_slices are refused
+ *          wait_limit_log2 and events apply; the comparison modes and suffix_slices
+ *          are refused
  *   scale  softmax scale, finite and > 0
  */
 typedef struct pp_kv8_attn_args {
@@ -472,7 +477,8 @@ typedef struct pp_kv8_attn_args {
  * Rows that see nothing, inactive rows and rows of stream 0 or > P_max (which
  * set PP_DEV_BAD_STREAM) get o = 0 and lse = -inf.  Keys on a page that is
  * not there are skipped (PP_DEV_BAD_PAGE).  A query with a NaN or infinity
- * gives NaN.  A workspace serves one call in flight; calls ordered on one
+ * gives NaN, and so may one with a score (scale q.k, in base 2) beyond 2^26, which
+ * the document pass's fp32 reference cannot hold closely enough.  A workspace serves one call in flight; calls ordered on one
  * stream may share it.
  * A probability p is rounded to f16 together with its page's value scale vs:
  * to 2^-11 of itself, but a key's share of o also to 2^-16 max(p vs), the

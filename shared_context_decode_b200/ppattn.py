@@ -595,7 +595,8 @@ def kv8_append(layer: KV8Layer, k: torch.Tensor, v: torch.Tensor, sid: torch.Ten
     """Append rows k, v [n, H, d] bf16 (rows may be strided) with stream ids
     sid [n] int16 and positions pos [n] int32: keys rotated by `rope`, both
     quantised into the streams' pages.  q [n, Hq, d]: queries to rotate as
-    well; returns q_out (new, given, or q itself)."""
+    well; returns q_out (new, given, or q itself).  Rows of q_out that the call
+    skips keep what they held (a new q_out: anything)."""
     _want8(sid, _I16, "sid", layer)
     _want8(pos, _I32, "pos", layer)
     shape = sid.shape
