@@ -478,8 +478,8 @@ typedef struct pp_kv8_attn_args {
  * set PP_DEV_BAD_STREAM) get o = 0 and lse = -inf.  Keys on a page that is
  * not there are skipped (PP_DEV_BAD_PAGE).  A query with a NaN or infinity
  * gives NaN, and so may one with a score (scale q.k, in base 2) beyond 2^26, which
- * the document pass's fp32 reference cannot hold closely enough.  A workspace serves one call in flight; calls ordered on one
- * stream may share it.
+ * the document pass's fp32 reference cannot hold closely enough.  A workspace
+ * serves one call in flight; calls ordered on one stream may share it.
  * A probability p is rounded to f16 together with its page's value scale vs:
  * to 2^-11 of itself, but a key's share of o also to 2^-16 max(p vs), the
  * largest of the row's keys (pages whose value scales lie 2^14 apart or more
