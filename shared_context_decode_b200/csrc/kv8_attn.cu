@@ -357,9 +357,9 @@ __global__ void __launch_bounds__(WARPS * 32, (NT == 1 ? 16 : 12) / WARPS)
     // host does not know: then the first of a few blocks of the row takes their
     // items, `base` warps each, and the others, which stand behind all first ones,
     // end.  (Tables with room for 1024 further tokens, 256 streams of 17 to 112
-    // tokens, 32 heads: 124 us behind 16384, 64 streams behind 8192 49; all items cut
+    // tokens, 32 heads: 122 us behind 16384, 64 streams behind 8192 49; all items cut
     // as the table allows 195 and 70; tables without room, blocks of one warp, 116 and
-    // 47.  Answers of 1024 tokens pay 2 to 3 % for the question: 253 and 246.)
+    // 47.  Answers of 1024 tokens pay 2 % for the question: 250.5 and 245.)
     const int per = WARPS / p.base, groups = (xs + per - 1) / per;
     const int leaders = p.row_groups * groups;
     const bool leads = (int)blockIdx.x < leaders;
@@ -371,16 +371,25 @@ __global__ void __launch_bounds__(WARPS * 32, (NT == 1 ? 16 : 12) / WARPS)
       rg = b / f;
       x = (b - rg * f) / (per - 1) * per + 1 + (b - rg * f) % (per - 1);
     }
-    const int slot = p.q_pos[rg] - p.L.pos0;
-    const bool some = p.q_pos[rg] >= p.L.pos0 && stream_query(p.q_sid[rg], p.L.P_max);
-    const int chunks = (some ? min(slot >> 4, p.L.seg_pages * p.L.page / 16 - 1) + 1 : 0) +
-                       ((p.doc_len + 15) >> 4);
-    if (chunks <= kShareChunks * p.base) {
+    const int sid = p.q_sid[rg], ps = p.q_pos[rg], slot = ps - p.L.pos0;
+    // (the block's queries, if it takes its own item, and then the first table entry
+    // are on their way meanwhile: 252.5 -> 250.5 with answers of 1024 tokens)
+    const int first = x % p.gt * p.hg, heads = min(p.hg, p.g - first);
+    if (lane * 64 < heads * D)
+      asm volatile("prefetch.global.L1 [%0];" ::"l"(
+          p.q + (int64_t)rg * p.q_ld + (int64_t)(x / p.gt * p.g + first) * D + lane * 64));
+    const bool some = ps >= p.L.pos0 && stream_query(sid, p.L.P_max);
+    const int seg = some ? min(slot >> 4, p.L.seg_pages * p.L.page / 16 - 1) + 1 : 0;
+    if (seg + ((p.doc_len + 15) >> 4) <= kShareChunks * p.base) {
       if (!leads) return;
       ways = p.base;
       x += warp / ways;
       live = x < xs;
     }
+    if (some && lane == 0)
+      asm volatile("prefetch.global.L1 [%0];" ::"l"(
+          p.L.seg_table + (int64_t)(sid - 1) * p.L.seg_pages +
+          ((seg * (warp & (ways - 1)) / ways) >> p.lper)));
   }
   const int way = warp & (ways - 1);
   uint8_t* ring = sm + warp * M::WARP;
