@@ -353,13 +353,12 @@ __global__ void __launch_bounds__(WARPS * 32, (NT == 1 ? 16 : 12) / WARPS)
     rg = (int)blockIdx.x / xs;
     x = (int)blockIdx.x - rg * xs;
   } else {
-    // The table has room for long segments and this row's may be short, which the
-    // host does not know: then the first of a few blocks of the row takes their
+    // The tables have room for long segments and these rows' may be short, which the
+    // host does not know: then the first of a few blocks of the rows takes their
     // items, `base` warps each, and the others, which stand behind all first ones,
-    // end.  (Tables with room for 1024 further tokens, 256 streams of 17 to 112
-    // tokens, 32 heads: 122 us behind 16384, 64 streams behind 8192 49; all items cut
-    // as the table allows 195 and 70; tables without room, blocks of one warp, 116 and
-    // 47.  Answers of 1024 tokens pay 2 % for the question: 250.5 and 245.)
+    // end.  (64 streams of 17..80 tokens, 32 heads, room for 1024 more 23.3 us, cut all
+    // the same 33.7, in tables without room 22.5; segments of 1024 tokens pay 2 % for
+    // the question, 99.7 and 97.7.)
     const int per = WARPS / p.base, groups = (xs + per - 1) / per;
     const int leaders = p.row_groups * groups;
     const bool leads = (int)blockIdx.x < leaders;
@@ -371,25 +370,18 @@ __global__ void __launch_bounds__(WARPS * 32, (NT == 1 ? 16 : 12) / WARPS)
       rg = b / f;
       x = (b - rg * f) / (per - 1) * per + 1 + (b - rg * f) % (per - 1);
     }
-    const int sid = p.q_sid[rg], ps = p.q_pos[rg], slot = ps - p.L.pos0;
-    // (the block's queries, if it takes its own item, and then the first table entry
-    // are on their way meanwhile: 252.5 -> 250.5 with answers of 1024 tokens)
-    const int first = x % p.gt * p.hg, heads = min(p.hg, p.g - first);
-    if (lane * 64 < heads * D)
-      asm volatile("prefetch.global.L1 [%0];" ::"l"(
-          p.q + (int64_t)rg * p.q_ld + (int64_t)(x / p.gt * p.g + first) * D + lane * 64));
-    const bool some = ps >= p.L.pos0 && stream_query(sid, p.L.P_max);
-    const int seg = some ? min(slot >> 4, p.L.seg_pages * p.L.page / 16 - 1) + 1 : 0;
+    const int row = rg * p.rt + lane;
+    int seg = 0;                           // 16-key chunks of the lane's row
+    if (lane < p.rt && row < p.rows && p.q_pos[row] >= p.L.pos0 &&
+        stream_query(p.q_sid[row], p.L.P_max))
+      seg = min((p.q_pos[row] - p.L.pos0) >> 4, p.L.seg_pages * p.L.page / 16 - 1) + 1;
+    seg = __reduce_max_sync(0xffffffffu, seg);
     if (seg + ((p.doc_len + 15) >> 4) <= kShareChunks * p.base) {
       if (!leads) return;
       ways = p.base;
       x += warp / ways;
       live = x < xs;
     }
-    if (some && lane == 0)
-      asm volatile("prefetch.global.L1 [%0];" ::"l"(
-          p.L.seg_table + (int64_t)(sid - 1) * p.L.seg_pages +
-          ((seg * (warp & (ways - 1)) / ways) >> p.lper)));
   }
   const int way = warp & (ways - 1);
   uint8_t* ring = sm + warp * M::WARP;
@@ -803,18 +795,23 @@ cudaError_t launch_kv8_attn(const pp_kv8_layer& L, const pp_kv8_attn_args& a,
   p.o = a.o; p.lse = a.lse;
   // Warps per item: enough to fill the GPU when items are few (they share the
   // item's merge too, however short its keys), and a long document cut so that
-  // one item is not a CTA's whole tail.  A decode row's long segment is cut too, by
-  // the kernel, since only the row's position tells its length; question rows are
-  // not: a question's items are many (256 questions of 16..48 rows in tables for 1024
-  // further tokens 1486 us, cut by the table's length 1931; 8 of 1000 rows 1847 and 2223).
+  // one item is not a CTA's whole tail.
   const int64_t seg_chunks = (int64_t)L.seg_pages * L.page / 16, doc_chunks = (p.doc_len + 15) / 16;
   const int most = it.most == 8 ? 8 : 4;    // (items of 16 pairs are many)
   int base = 1;
   while (base < most &&
          (items * base < 12LL * num_sms || (base < 4 && doc_chunks / base > kShareChunks)))
     base *= 2;
+  // Long segments are cut too where the items are fewer than 1.5 times the GPU's
+  // warps, if the kernel finds them long (the tables only tell how long they may be).
+  // Measured behind 256 tokens, one warp / cut: 80 streams of 1024 tokens, 32 heads
+  // 149 / 121 us, 100 167 / 146, 128 176 / 182, 256 of 300..600 159 / 200, of 1024
+  // 336 / 336; a question of 2000 rows, 8 heads 161 / 106, two of 700 rows, 8 x 4 heads
+  // 116 / 155.  Behind a long document one warp gains more: 128 streams of 1024 behind
+  // 8192 217 / 246, 256 questions of 16..48 rows behind 12000 1486 / 1931.
+  const int64_t slots = (it.most == 8 ? 16LL : 12LL) * num_sms;
   int ways = base;
-  if (one_row_per_stream)
+  if (2 * items < 3 * slots)
     while (ways < 4 && 2 * ways <= base * (int64_t)L.H * it.gt &&
            (seg_chunks + doc_chunks) / ways > kShareChunks)
       ways *= 2;

@@ -22,9 +22,10 @@ def compare(layer, doc, segs, N, q, o, lse, sid, pos, scale, rows, what):
 
 
 # heads, query heads per head, d, rows: items enough to fill the GPU (base 1 warp an
-# item), or half of that (base 2); blocks of four, two or one warps; items of 16 pairs
-SHAPES = [(5, 1, 128, 400), (8, 4, 64, 230), (2, 2, 64, 900), (1, 1, 64, 1800), (7, 3, 64, 150),
-          (3, 12, 128, 600), (6, 12, 64, 300), (4, 9, 128, 460)]
+# item), or half of that (base 2); blocks of four, two or one warps; items of 16 pairs;
+# items so many that none is cut
+SHAPES = [(16, 1, 128, 256), (8, 10, 64, 350), (5, 1, 128, 400), (8, 4, 64, 230),
+          (2, 2, 64, 900), (1, 1, 64, 1800), (7, 3, 64, 150), (3, 12, 128, 600), (6, 12, 64, 300), (4, 9, 128, 460)]
 
 
 @pytest.mark.parametrize("N,splits", [(0, 0), (150, 0), (300, 37)])
